@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libsdm.so")
-SOURCES = ["sdm_abi.cu", "decode.cu", "gather.cu"]
+SOURCES = ["sdm_abi.cu", "sdm_abi_quant.cu", "decode.cu", "gather.cu", "quant.cu", "qgather.cu", "qdecode.cu", "route.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

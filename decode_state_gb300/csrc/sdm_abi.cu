@@ -524,6 +524,12 @@ const char* sdm_status_string(int status) {
         case SDM_EROW: return "row0 outside 0..row0_max, row0_max + tokens beyond the index rows, or a plan step outside 0..T-1";
         case SDM_EDEVICE: return "the current device is not the plan's device";
         case SDM_EFLAGS: return "unknown bits in the flags of an _ex entry point";
+        case SDM_EFORMAT: return "the format is not one that this operation takes";
+        case SDM_EGROUP: return "a scale's group must be 32, 64 or 128 columns";
+        case SDM_EROUTE:
+            return "need 1 <= n <= 65536, 1 <= k <= min(n, 256), a known score, 1..256 groups that divide n, "
+                   "1 <= top_groups <= n_groups and group_top 1 or 2";
+        case SDM_ESTRIDE: return "a row stride is smaller than the row";
         default: break;
     }
     if (status > 0) return cudaGetErrorString(static_cast<cudaError_t>(status));
@@ -540,10 +546,15 @@ int sdm_device_status(unsigned int* status, int clear) {
         *status = 0;
         return (int)s;
     }
-    unsigned int a = 0, b = 0;
-    int e = sdm::decode_status(&a, clear != 0);
-    if (e == 0) e = sdm::gather_status(&b, clear != 0);
-    *status = a | b;
+    int e = 0;
+    unsigned int all = 0;
+    for (const auto read : {sdm::decode_status, sdm::gather_status, sdm::quant_status, sdm::qgather_status,
+                            sdm::qdecode_status, sdm::route_status}) {
+        unsigned int word = 0;
+        if (e == 0) e = read(&word, clear != 0);
+        all |= word;
+    }
+    *status = all;
     if (e != 0) (void)cudaGetLastError();
     return e;
 }

@@ -48,6 +48,80 @@ struct GatherArgs {
     int inputs_ready;  // the index and weight rows predate the preceding kernel: load them before waiting
 };
 
+// Rows into (rows read, codes and scales written) or out of a quantised bank.
+struct QuantRowsArgs {
+    uint8_t* codes;
+    float* scales;
+    void* rows;  // n_rows rows, row_stride elements apart
+    const void* slots;  // nullptr: row i is slot i
+    int64_t n_slots, row_stride, n_rows;
+    int hd, group, idx64;
+    int pieces, groups, lanes;  // 16-byte pieces and scale groups of a row; lanes that work on it
+    int vec;    // the rows' pieces are 16-byte aligned
+    int small;  // lane numbers fit 32 bits
+};
+
+// Weighted sums of quantised rows, or (dout, dw) the gradient of the weights.
+struct QGatherArgs {
+    const void* bank;  // codes, or the rows of an unquantised bank
+    const float* scales;
+    int64_t n_slots;
+    int hd, group, n_ops;
+    const void* idx[2];
+    const void* w[2];
+    float* out[2];
+    const float* dout[2];
+    void* dw[2];
+    int width[2];
+    int idx64, w_bf16;  // w_bf16: the weights' type, or the gradient's
+    int64_t tokens;
+    int chunk, valid;
+    const int32_t* chunk_valid;
+    int pieces, groups;    // 16-byte pieces and scale groups of a row
+    int64_t row_bytes;     // from one row to the next
+    int slices;            // column slices of a row, each the lanes of one row slot
+    int split;             // warps that share one token's entries
+    int vec_out;           // out / dout rows are 16-byte aligned
+};
+
+// Write-then-read tokens on a quantised bank.
+struct QDecodeArgs {
+    uint8_t* codes;
+    float* scales;
+    int64_t n_slots;
+    const void* k_idx;
+    const float* k_val;
+    const float* v;
+    const float* beta;
+    const float* g;
+    const void* q_idx;
+    const float* q_val;
+    void* out;
+    int64_t n_streams;
+    int hd, group, W, R, G, T;
+    int idx64, out_bf16;
+    int64_t tstride, sstride;  // as in DecodeArgs
+    int pieces, groups;        // 16-byte pieces and scale groups of a row
+    int slices;                // column slices of a row: one block each
+};
+
+struct RouteArgs {
+    const void* logits;
+    int64_t row_stride;
+    const float* bias;
+    const void* base;
+    void* idx;
+    float* w;
+    int64_t tokens;
+    int n, k, score, n_groups, top_groups, group_top;
+    float scale;
+    int renorm, idx64, logit_bf16;
+    // the gradient's: idx is read
+    const float* dw;
+    void* dlogits;
+    int64_t dlogits_stride;
+};
+
 // A resolved gather launch: the kernel instance, its geometry and every kernel argument.
 struct GatherLaunch {
     const void* fn;  // kernel (host stub of the template instance); nullptr: nothing to launch
@@ -76,9 +150,22 @@ int launch_gather(const GatherArgs& a, int bank_dtype, int idx_dtype, int w_dtyp
 int plan_gather(const GatherArgs& a, int bank_dtype, int idx_dtype, int w_dtype, GatherLaunch* L);
 int run_gather(const GatherLaunch& L, cudaStream_t stream);
 
+// The operators around them (arguments checked by the ABI layer). Return a cudaError_t or an SDM_E*
+// code when a launch would not hold the work.
+int launch_quant_rows(const QuantRowsArgs& a, int format, int row_dtype, bool write, cudaStream_t stream);
+int launch_qgather(const QGatherArgs& a, int format, cudaStream_t stream);
+int launch_gather_dw(const QGatherArgs& a, int format, cudaStream_t stream);
+int launch_qdecode(const QDecodeArgs& a, int format, cudaStream_t stream);
+int launch_route(const RouteArgs& a, cudaStream_t stream);
+int launch_route_backward(const RouteArgs& a, cudaStream_t stream);
+
 // Device status words of the kernel files (OR of SDM_DEV_* bits); read and optionally reset.
 int decode_status(unsigned int* word, bool clear);
 int gather_status(unsigned int* word, bool clear);
+int quant_status(unsigned int* word, bool clear);
+int qgather_status(unsigned int* word, bool clear);
+int qdecode_status(unsigned int* word, bool clear);
+int route_status(unsigned int* word, bool clear);
 
 // Multiprocessor count of the current device (cached per device).
 int sm_count();

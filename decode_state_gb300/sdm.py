@@ -24,6 +24,8 @@ ENTRY_POINTS = ("sdm_decode_step", "sdm_decode_step_ex", "sdm_decode_seq", "sdm_
                 "sdm_decode_plan_init", "sdm_decode_plan_launch", "sdm_decode_plan_walk", "sdm_gather",
                 "sdm_gather_kpos",
                 "sdm_gather_plan_init", "sdm_gather_plan_launch", "sdm_gather_plan_launch_ex", "sdm_gather_plan_walk",
+                "sdm_quant_row_bytes", "sdm_quantize_rows", "sdm_dequantize_rows", "sdm_qgather", "sdm_gather_dw",
+                "sdm_qdecode_step", "sdm_qdecode_seq", "sdm_route", "sdm_route_backward",
                 "sdm_status_string",
                 "sdm_device_status", "sdm_version")
 SDM_INPUTS_READY = 1  # flag of the _ex calls: the inputs predate the kernel launched just before
@@ -89,6 +91,21 @@ def library() -> ctypes.CDLL:
             lib.sdm_gather_plan_launch_ex.restype = i32
             lib.sdm_gather_plan_walk.argtypes = [vp, vp, vp, i32, ctypes.c_uint, vp]
             lib.sdm_gather_plan_walk.restype = i32
+            u32, pp, pi = ctypes.c_uint, ctypes.POINTER(vp), ctypes.POINTER(i32)
+            lib.sdm_quant_row_bytes.argtypes = [i32, i32]
+            lib.sdm_quantize_rows.argtypes = [vp, vp, i64, i32, i32, i32, vp, i64, i32, vp, i32, i64, vp]
+            lib.sdm_dequantize_rows.argtypes = lib.sdm_quantize_rows.argtypes
+            lib.sdm_qgather.argtypes = [vp, vp, i64, i32, i32, i32, i32, pp, pp, pp, pi, i32, i32, i64, i32, i32, vp, vp]
+            lib.sdm_gather_dw.argtypes = lib.sdm_qgather.argtypes
+            qdec = [vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, i32, i32]
+            lib.sdm_qdecode_step.argtypes = qdec + [i32, i32, vp]
+            lib.sdm_qdecode_seq.argtypes = qdec + [i32, i32, i32, u32, vp]
+            lib.sdm_route.argtypes = [vp, i64, i32, vp, vp, vp, vp, i64, i32, i32, i32, i32, i32, i32, ctypes.c_float,
+                                      u32, i32, vp]
+            lib.sdm_route_backward.argtypes = [vp, i64, i32, vp, vp, vp, vp, i64, i64, i32, i32, i32, ctypes.c_float,
+                                               u32, i32, vp]
+            for name in ENTRY_POINTS[ENTRY_POINTS.index("sdm_quant_row_bytes"):ENTRY_POINTS.index("sdm_status_string")]:
+                getattr(lib, name).restype = i32
             lib.sdm_status_string.argtypes = [i32]
             lib.sdm_status_string.restype = ctypes.c_char_p
             lib.sdm_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]

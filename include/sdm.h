@@ -10,6 +10,13 @@
  *                    checked launch, replayed per slab of an index tensor; _launch_ex: with
  *                    flags)
  *
+ *
+ * and the operators around them (routing and quantised banks, at the end of this file):
+ *   sdm_route          scores to slots and weights (top-k), sdm_route_backward its gradient
+ *   sdm_quantize_rows  rows into a quantised bank, sdm_dequantize_rows back out of it
+ *   sdm_qgather        weighted sums of quantised rows, sdm_gather_dw the weights' gradient
+ *   sdm_qdecode_step   write-then-read tokens on a quantised bank (sdm_qdecode_seq: T tokens)
+ *
  * Common rules
  *   - Every pointer argument except `stream` (and the host records and arrays named as such) is a
  *     DEVICE pointer the caller owns; the library keeps no pointer after the call returns (apart
@@ -72,6 +79,11 @@ typedef struct CUstream_st* sdm_stream_t;
 #define SDM_EROW (-13)      /* row0 outside 0..row0_max, row0_max + tokens beyond the index rows, or a plan step outside 0..T-1 */
 #define SDM_EDEVICE (-14)   /* the current device is not the one the plan was made on */
 #define SDM_EFLAGS (-15)    /* unknown bits in the flags of an _ex entry point */
+
+#define SDM_EFORMAT (-16)   /* the format is not one that this operation takes */
+#define SDM_EGROUP (-17)    /* a scale's group is not 32, 64 or 128 columns */
+#define SDM_EROUTE (-18)    /* routing sizes, score kind or groups out of range */
+#define SDM_ESTRIDE (-19)   /* a row stride is smaller than the row */
 
 /* bits of the device status word */
 #define SDM_DEV_TIMEOUT 1u   /* reserved: a kernel gave up a bounded wait (no current kernel waits) */
@@ -317,6 +329,155 @@ int sdm_gather_plan_launch_ex(const sdm_gather_plan* plan, int64_t row0, int val
  */
 int sdm_gather_plan_walk(const sdm_gather_plan* plan, const int64_t* row0, const int32_t* valid, int n,
                          unsigned flags, sdm_stream_t stream);
+
+/*
+ * Quantised banks
+ *
+ * A quantised bank holds n_slots rows of hd columns as two device arrays:
+ *   codes   [n_slots, row_bytes] bytes, 16-byte aligned; row_bytes = sdm_quant_row_bytes(hd, format):
+ *           one byte a column (SDM_INT8, SDM_FP8) or two columns a byte, the even one in the low half
+ *           (SDM_INT4), padded with zero bytes to a multiple of 16
+ *   scales  [n_slots, ceil(hd / group)] float32; group = 32, 64 or 128 columns share a scale
+ * and stands for scale * code, with code a two's complement integer (SDM_INT8, SDM_INT4) or a float
+ * with 4 exponent and 3 mantissa bits (SDM_FP8, e4m3 without infinities).
+ *
+ * A group of values x is stored as
+ *     scale = max|x| / L,  code = round(x * (L / max|x|)),  L = 127 (INT8), 448 (FP8), 7 (INT4)
+ * in float32, rounding codes to nearest even. A group whose max|x| is below 2^-100 is stored as
+ * zeros with scale 0; one that holds an infinity or NaN gets the scale NaN, so that it reads back
+ * as NaN rather than as something plausible.
+ */
+#define SDM_INT8 2
+#define SDM_FP8 3
+#define SDM_INT4 4
+
+/* Bytes from one row of codes to the next, or 0 for an unknown format or hd outside 1..65536. */
+int sdm_quant_row_bytes(int hd, int format);
+
+/*
+ * sdm_quantize_rows - write rows into a quantised bank: row i goes to slot slots[i], or to slot i
+ * when slots is NULL (then n_rows <= n_slots, else SDM_EROW). The slots of one call must be
+ * distinct. A slot outside [0, n_slots) is skipped and raises SDM_DEV_BAD_INDEX.
+ *
+ *   rows       n_rows rows of hd columns, row_dtype SDM_BF16 | SDM_F32, row i at rows + i * row_stride
+ *              elements (row_stride >= hd)
+ *   slots      [n_rows] idx dtype, or NULL
+ */
+int sdm_quantize_rows(void* codes, float* scales, int64_t n_slots, int hd, int group, int format, const void* rows,
+                      int64_t row_stride, int row_dtype, const void* slots, int idx_dtype, int64_t n_rows,
+                      sdm_stream_t stream);
+
+/*
+ * sdm_dequantize_rows - read rows of a quantised bank back: row i is scale * code of slot slots[i]
+ * (slot i when slots is NULL; repeats allowed), computed in float32 and rounded to row_dtype once.
+ * A slot outside [0, n_slots) gives a zero row and raises SDM_DEV_BAD_INDEX. Arguments as
+ * sdm_quantize_rows, with `rows` written.
+ */
+int sdm_dequantize_rows(const void* codes, const float* scales, int64_t n_slots, int hd, int group, int format,
+                        void* rows, int64_t row_stride, int row_dtype, const void* slots, int idx_dtype,
+                        int64_t n_rows, sdm_stream_t stream);
+
+/*
+ * sdm_qgather - sdm_gather (no stash) over a quantised bank:
+ *     out[o][t, :] = sum_n w[o][t, n] * row(idx[o][t, n])
+ * with the sum in float32 in an order that depends on the sizes alone. Padding tokens
+ * (t % chunk >= valid) read nothing and get zeros. Arguments as sdm_gather and above.
+ */
+int sdm_qgather(const void* codes, const float* scales, int64_t n_slots, int hd, int group, int format, int n_ops,
+                const void* const idx[2], const void* const w[2], float* const out[2], const int width[2],
+                int idx_dtype, int w_dtype, int64_t tokens, int chunk, int valid, const int32_t* chunk_valid,
+                sdm_stream_t stream);
+
+/*
+ * sdm_gather_dw - gradient of the weights of sdm_gather or sdm_qgather:
+ *     dw[o][t, n] = sum_c dout[o][t, c] * row(idx[o][t, n])[c]
+ * summed in float32 and rounded to dw_dtype once. Padding tokens read nothing and get zeros; an
+ * entry whose index is outside [0, n_slots) gets zero and raises SDM_DEV_BAD_INDEX.
+ *
+ *   bank       format SDM_BF16 | SDM_F32: the [n_slots, hd] bank (scales and group are ignored);
+ *              SDM_INT8 | SDM_FP8 | SDM_INT4: the codes of a quantised bank
+ *   dout[o]    [tokens, hd] float32
+ *   dw[o]      [tokens, width[o]] dw_dtype SDM_BF16 | SDM_F32
+ */
+int sdm_gather_dw(const void* bank, const float* scales, int64_t n_slots, int hd, int group, int format, int n_ops,
+                  const void* const idx[2], const float* const dout[2], void* const dw[2], const int width[2],
+                  int idx_dtype, int dw_dtype, int64_t tokens, int chunk, int valid, const int32_t* chunk_valid,
+                  sdm_stream_t stream);
+
+/*
+ * sdm_qdecode_step / sdm_qdecode_seq - sdm_decode_step / sdm_decode_seq on a quantised bank
+ * (SDM_INT8 or SDM_FP8; 4 bits are too few for rows that are written again and again):
+ *     retrieved      = sum_w k_val[w] * d_w * row(k_idx[w]),  d_w = exp(g[G == 1 ? 0 : w])
+ *     delta_v        = beta * (v - retrieved)
+ *     row(k_idx[w]) <- quantised(d_w * row(k_idx[w]) + k_val[w] * delta_v)
+ *     out            = sum_r q_val[r] * row(q_idx[r])       (after the write)
+ * All arithmetic is float32; k_val, v and q_val are used as given; the readings are rounded to
+ * out_dtype once. A decay alone (k_val = 0) goes into the scales and leaves the codes as they are.
+ * The slots of a stream are private to it and its W write slots distinct, as in sdm_decode_step; a
+ * slot outside [0, n_slots) reads as zeros, is not written, and raises SDM_DEV_BAD_INDEX.
+ * sdm_qdecode_seq takes time-major arrays, or with SDM_STREAM_MAJOR stream-major ones
+ * (sdm_decode_seq_ex); other flags return SDM_EFLAGS.
+ */
+int sdm_qdecode_step(void* codes, float* scales, int64_t n_slots, const void* k_idx, const float* k_val,
+                     const float* v, const float* beta, const float* g, const void* q_idx, const float* q_val,
+                     void* out, int64_t n_streams, int hd, int group, int format, int W, int R, int G, int idx_dtype,
+                     int out_dtype, sdm_stream_t stream);
+int sdm_qdecode_seq(void* codes, float* scales, int64_t n_slots, const void* k_idx, const float* k_val,
+                    const float* v, const float* beta, const float* g, const void* q_idx, const float* q_val,
+                    void* out, int64_t n_streams, int hd, int group, int format, int W, int R, int G, int T,
+                    int idx_dtype, int out_dtype, unsigned flags, sdm_stream_t stream);
+
+/*
+ * Routing: which k of n entries a token takes, and with which weights. The entries are a stream's
+ * memory slots (the results are then k_idx / k_val or q_idx / q_val of the decode, or idx / w of a
+ * gather) or experts (whose output rows a gather joins).
+ *
+ * sdm_route - for every token t with logits x = logits[t, :]:
+ *     s_j = exp(x_j - max x) / sum_i exp(x_i - max x)     (SDM_SOFTMAX)
+ *     s_j = 1 / (1 + exp(-x_j))                           (SDM_SIGMOID)
+ *   Entries are ranked by s_j + bias_j when bias is given, else by s_j (SDM_SIGMOID) or x_j
+ *   (SDM_SOFTMAX: the same order, without the rounding of s). Entries whose x is -inf or NaN, or
+ *   whose rank is -inf or NaN, are masked: they rank last and have weight 0. Several +inf under a
+ *   softmax share it evenly.
+ *   With n_groups > 1 the entries form n_groups consecutive groups of n / n_groups; the
+ *   top_groups best groups stay and the entries of the others are masked. A group's score is its
+ *   largest rank (group_top 1) or the sum of its two largest (group_top 2; for a softmax without a
+ *   bias the sum of the two largest exp(x_j - max x)); masked entries take no part, and a group
+ *   without others comes last.
+ *   The k best entries are taken, best first; equal ranks, of groups too, go by the lower index.
+ *   idx[t, i] is the entry's number j (plus base[t] when base is given), and
+ *     w[t, i] = scale * s_j, or with SDM_RENORM  scale * s_j / sum of the chosen s
+ *   (0 where that sum is 0). When fewer than k entries are not masked, masked ones fill up in
+ *   index order with weight 0, so the k indices are always distinct.
+ *
+ *   logits      row t at logits + t * row_stride elements (row_stride >= n), SDM_BF16 | SDM_F32
+ *   bias        [n] float32, or NULL; moves the choice only, never the weights
+ *   base        [tokens] idx dtype, or NULL: e.g. the first slot of the token's stream
+ *   idx, w      [tokens, k] idx dtype and float32
+ *   1 <= n <= 65536, 1 <= k <= min(n, 256); n_groups divides n, at most 256; 1 <= top_groups <=
+ *   n_groups; group_top 1 or 2 (else SDM_EROUTE); flags 0 or SDM_RENORM
+ */
+#define SDM_SOFTMAX 0
+#define SDM_SIGMOID 1
+#define SDM_RENORM 4u
+int sdm_route(const void* logits, int64_t row_stride, int logit_dtype, const float* bias, const void* base, void* idx,
+              float* w, int64_t tokens, int n, int k, int score, int n_groups, int top_groups, int group_top,
+              float scale, unsigned flags, int idx_dtype, sdm_stream_t stream);
+
+/*
+ * sdm_route_backward - gradient of the logits: with u_i = scale * dw[t, i], or with SDM_RENORM
+ * u_i = scale / S * (dw[t, i] - sum_m dw[t, m] * s_m / S), S the sum of the chosen s,
+ *     dlogits_j = u_j * s_j * (1 - s_j)                        (SDM_SIGMOID; 0 for entries not chosen)
+ *     dlogits_j = s_j * (u_j [chosen] - sum_i u_i * s_i)       (SDM_SOFTMAX)
+ * The choice itself, and the bias, have no gradient. idx is what sdm_route returned (base added);
+ * an index outside the row is skipped and raises SDM_DEV_BAD_INDEX; the k indices of a token are
+ * distinct. Masked logits get 0.
+ *
+ *   dlogits     row t at dlogits + t * dlogits_stride elements, logit dtype; all n columns written
+ */
+int sdm_route_backward(const void* logits, int64_t row_stride, int logit_dtype, const void* base, const void* idx,
+                       const float* dw, void* dlogits, int64_t dlogits_stride, int64_t tokens, int n, int k, int score,
+                       float scale, unsigned flags, int idx_dtype, sdm_stream_t stream);
 
 /* A static string naming a return code of the calls above. */
 const char* sdm_status_string(int status);
