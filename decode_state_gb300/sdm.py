@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -114,6 +115,29 @@ def library() -> ctypes.CDLL:
             lib.sdm_version.restype = i32
             _lib = lib
     return _lib
+
+
+_binding = None
+
+
+def binding():
+    """The loaded native binding of the per-token operators (``csrc/torch_binding.cpp``); raises if it
+    has not been built."""
+    global _binding
+    if _binding is None:
+        library()
+        with _lock:
+            if _binding is None:
+                path = os.path.join(os.path.dirname(_LIB_PATH), "sdm_torch.so")
+                if not os.path.exists(path):
+                    raise RuntimeError(f"the SDM binding is not built ({path} is missing); "
+                                       "run decode_state_gb300.build.build()")
+                spec = importlib.util.spec_from_file_location("sdm_torch", path)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                module.raise_with(_check)
+                _binding = module
+    return _binding
 
 
 def status_string(status: int) -> str:
