@@ -11,6 +11,12 @@
 // retrieval to the write-back: each row is read once and written once, and the group's maximum is
 // a shuffle among neighbouring lanes. The sums over rows go through shuffles within a warp and
 // shared memory across warps, in a fixed order.
+//
+// A token is a chain of dependent steps, so the waits for memory are taken off the chain. One thread
+// for each entry loads its slot, weight and gate two tokens ahead into registers, turns them into a
+// record in shared memory and warms the row in L2; a value column's thread does the same with v. And
+// behind the barrier that ends a token's writes its read rows and the next token's write rows are
+// requested together, without branches between the requests, so a token waits once, for L2.
 #include <algorithm>
 #include <climits>
 
@@ -24,12 +30,12 @@ __device__ unsigned int g_qdecode_status;
 
 constexpr unsigned kAll = 0xffffffffu;
 
-__device__ __forceinline__ int64_t bank_slot(const QDecodeArgs& a, const void* idx, int64_t i) {
-    const int64_t s = a.idx64 ? __ldg(static_cast<const int64_t*>(idx) + i) : __ldg(static_cast<const int32_t*>(idx) + i);
-    if (s >= 0 && s < a.n_slots) return s;
-    atomicOr(&g_qdecode_status, SDM_DEV_BAD_INDEX);
-    return -1;
-}
+// One entry of a token: where its row is, its weight, and for a write its decay.
+struct __align__(16) Entry {
+    int slot;  // -1: none
+    float weight, decay, unused;
+};
+constexpr int kRing = 3;  // tokens whose entries are kept
 
 // Sum x[0..16) over the row slots of a warp (lanes LR apart); x[0 .. 16 * LR / 32) then holds the
 // columns from the returned one on.
@@ -52,11 +58,14 @@ __device__ __forceinline__ int reduce_rows(float* x, int lane) {
     return first;
 }
 
-// F: Int8 or Fp8. LR: lanes of a row slice (its columns: 16 * LR). NT: threads. RPT: rows a thread holds.
-template <typename F, int LR, int NT, int RPT>
-__global__ void __launch_bounds__(NT) qdecode_kernel(const QDecodeArgs a) {
+// F: Int8 or Fp8. LR: lanes of a row slice (its columns: 16 * LR). NT: threads. RPT: rows a thread
+// holds. ITEMS: entries (W + R of them) that a thread prepares.
+template <typename F, int LR, int NT, int RPT, int ITEMS>
+__global__ void __launch_bounds__(NT, RPT == 8 ? 1 : 4) qdecode_kernel(const QDecodeArgs a) {
     static_assert(F::C == 16, "pieces of 16 columns");
     constexpr int COLS = 16 * LR, RS = NT / LR, WARPS = NT / 32, KEEP = 16 * LR / 32;
+    static_assert(COLS <= NT, "a thread for every column");
+    extern __shared__ __align__(16) Entry entries[];  // [kRing][W + R]
     __shared__ __align__(16) float part_k[WARPS][COLS];
     __shared__ __align__(16) float part_q[WARPS][COLS];
     __shared__ __align__(16) float delta[COLS];
@@ -64,119 +73,192 @@ __global__ void __launch_bounds__(NT) qdecode_kernel(const QDecodeArgs a) {
     const int rs = tid / LR, lp = tid % LR;
     const int64_t s = blockIdx.x / a.slices;
     const int slice = (int)(blockIdx.x % a.slices);
-    const int p = slice * LR + lp, c0 = slice * COLS, hd = a.hd;
+    const int p = slice * LR + lp, c0 = slice * COLS, hd = a.hd, W = a.W, R = a.R;
     const bool active = p < a.pieces;
     const int gl = min(a.group / 16, LR);  // lanes of a scale group
-    const int64_t group = p * 16 / a.group;
     uint4* codes = reinterpret_cast<uint4*>(a.codes) + p;
-    float* scales = a.scales + group;
+    float* scales = a.scales + p * 16 / a.group;
+    const bool column = tid < COLS && c0 + tid < hd;  // this thread has a value column
     grid_dependency_wait();
     grid_launch_dependents();
 
-    for (int t = 0; t < a.T; ++t) {
+    // this thread's entries of a token as they are loaded, and as they are kept
+    int64_t raw_slot[ITEMS];
+    float raw_weight[ITEMS], raw_gate[ITEMS], v_next = 0.0f, beta_next = 0.0f;
+    const auto load_entries = [&](int t) {
+        if (t >= a.T) return;
         const int64_t ts = t * a.tstride + s * a.sstride;
-        // the write rows, and their decayed sum
-        int64_t slot[RPT];
-        uint4 code[RPT];
-        float ds[RPT], kv[RPT], x[16], acc[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+        for (int n = 0; n < ITEMS; ++n) {
+            const int i = tid + n * NT;
+            if (i < W + R) {
+                const bool write = i < W;
+                const int64_t e = write ? ts * W + i : ts * R + (i - W);
+                const void* idx = write ? a.k_idx : a.q_idx;
+                raw_slot[n] = a.idx64 ? __ldg(static_cast<const int64_t*>(idx) + e) : __ldg(static_cast<const int32_t*>(idx) + e);
+                raw_weight[n] = __ldg((write ? a.k_val : a.q_val) + e);
+                raw_gate[n] = write ? __ldg(a.g + ts * a.G + (a.G == 1 ? 0 : i)) : 0.0f;
+            }
+        }
+    };
+    const auto load_value = [&](int t) {
+        if (t >= a.T) return;
+        const int64_t ts = t * a.tstride + s * a.sstride;
+        beta_next = __ldg(a.beta + ts);
+        if (column) v_next = __ldg(a.v + ts * hd + c0 + tid);
+    };
+    const auto keep_entries = [&](int t) {
+        if (t >= a.T) return;
+        Entry* to = entries + (t % kRing) * (W + R);
+#pragma unroll
+        for (int n = 0; n < ITEMS; ++n) {
+            const int i = tid + n * NT;
+            if (i < W + R) {
+                const int64_t x = raw_slot[n];
+                const bool in = x >= 0 && x < a.n_slots;
+                if (in) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.codes + (x * a.pieces + slice * LR) * 16));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.scales + x * a.groups + c0 / a.group));
+                } else {
+                    atomicOr(&g_qdecode_status, SDM_DEV_BAD_INDEX);
+                }
+                to[i] = Entry{in ? (int)x : -1, raw_weight[n], expf(raw_gate[n]), 0.0f};
+            }
+        }
+    };
+    int slot[RPT];
+    uint4 code[RPT];
+    float ds[RPT], kv[RPT];  // scale * decay, and the weight, of the write rows
+    // request the write rows of token t; ds holds the decay until scale_writes()
+    float row_scale[RPT];
+    const auto load_writes = [&](int t) {
+        const Entry* from = entries + (t % kRing) * (W + R);
 #pragma unroll
         for (int j = 0; j < RPT; ++j) {
             const int w = rs + j * RS;
-            slot[j] = -1;
-            kv[j] = ds[j] = 0.0f;
-            code[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (w < a.W) {
-                slot[j] = bank_slot(a, a.k_idx, ts * a.W + w);
-                kv[j] = __ldg(a.k_val + ts * a.W + w);
-                if (slot[j] >= 0 && active) {
-                    code[j] = __ldcg(codes + slot[j] * a.pieces);
-                    ds[j] = __ldcg(scales + slot[j] * a.groups) * expf(__ldg(a.g + ts * a.G + (a.G == 1 ? 0 : w)));
-                }
-            }
+            const Entry e = from[min(w, W - 1)];
+            const bool on = w < W && e.slot >= 0 && active;
+            slot[j] = on ? e.slot : -1;
+            kv[j] = w < W ? e.weight : 0.0f;
+            ds[j] = e.decay;
+            code[j] = load16_if(codes + (int64_t)e.slot * a.pieces, on);
+            row_scale[j] = load4_if(scales + (int64_t)e.slot * a.groups, on);
         }
+    };
+
+    load_entries(0);
+    load_value(0);
+    keep_entries(0);
+    load_entries(1);
+    keep_entries(1);
+    load_entries(2);
+    __syncthreads();
+    load_writes(0);
+
+    for (int t = 0; t < a.T; ++t) {
+        // the decayed sum of the write rows
+        f32x2 x[8], acc2[8];
+        float acc[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc2[i] = 0;
 #pragma unroll
         for (int j = 0; j < RPT; ++j) {
-            F::unpack(code[j], x);
-            const float f = kv[j] * ds[j];
+            ds[j] *= row_scale[j];
+            F::unpack2(code[j], x);
+            const f32x2 f = pair(kv[j] * ds[j], kv[j] * ds[j]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] = fmaf(f, x[i], acc[i]);
+            for (int i = 0; i < 8; ++i) acc2[i] = fma2(f, x[i], acc2[i]);
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split(acc2[i], acc[2 * i], acc[2 * i + 1]);
         int first = reduce_rows<LR>(acc, lane);
 #pragma unroll
         for (int i = 0; i < KEEP; ++i) part_k[warp][lp * 16 + first + i] = acc[i];
-        __syncthreads();
-        for (int c = tid; c < COLS; c += NT) {
-            float r = part_k[0][c];
+        __syncthreads();  // 1: the sums of this token's writes and of the last one's reads
+        const auto put_out = [&](int of) {
+            float r = part_q[0][tid];
 #pragma unroll
-            for (int q = 1; q < WARPS; ++q) r += part_k[q][c];
-            const bool in = c0 + c < hd;
-            delta[c] = in ? __ldg(a.beta + ts) * (__ldg(a.v + ts * hd + c0 + c) - r) : 0.0f;
+            for (int q = 1; q < WARPS; ++q) r += part_q[q][tid];
+            const int64_t o = (of * a.tstride + s * a.sstride) * hd + c0 + tid;
+            if (a.out_bf16)
+                static_cast<uint16_t*>(a.out)[o] = from_f32<uint16_t>(r);
+            else
+                static_cast<float*>(a.out)[o] = r;
+        };
+        if (tid < COLS) {
+            float r = part_k[0][tid];
+#pragma unroll
+            for (int q = 1; q < WARPS; ++q) r += part_k[q][tid];
+            delta[tid] = column ? beta_next * (v_next - r) : 0.0f;
         }
-        __syncthreads();
+        __syncthreads();  // 2: delta
+        if (column && t > 0) put_out(t - 1);
+        load_value(t + 1);
+        keep_entries(t + 2);
+        load_entries(t + 3);
         // the new rows
-        float dl[16];
+        f32x2 dl[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float4 f = *reinterpret_cast<const float4*>(&delta[lp * 16 + 4 * i]);
-            dl[4 * i] = f.x, dl[4 * i + 1] = f.y, dl[4 * i + 2] = f.z, dl[4 * i + 3] = f.w;
+            dl[2 * i] = pair(f.x, f.y);
+            dl[2 * i + 1] = pair(f.z, f.w);
         }
 #pragma unroll
         for (int j = 0; j < RPT; ++j) {
-            F::unpack(code[j], x);
+            F::unpack2(code[j], x);
+            const f32x2 k2 = pair(kv[j], kv[j]), d2 = pair(ds[j], ds[j]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = fmaf(kv[j], dl[i], ds[j] * x[i]);
+            for (int i = 0; i < 8; ++i) x[i] = fma2(k2, dl[i], mul2(d2, x[i]));
             float sc;
             const uint4 n = quantise_piece<F>(x, gl, &sc);
-            if (slot[j] >= 0 && active) {
-                codes[slot[j] * a.pieces] = n;
-                if (lp % gl == 0) scales[slot[j] * a.groups] = sc;
+            if (slot[j] >= 0) {
+                codes[(int64_t)slot[j] * a.pieces] = n;
+                if (lp % gl == 0) scales[(int64_t)slot[j] * a.groups] = sc;
             }
         }
-        __syncthreads();  // the rows are written: the reads below, and the next token, may touch them
-        // the readings
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-        for (int r0 = rs; r0 < a.R; r0 += RPT * RS) {
-            uint4 v[RPT];
-            float qs[RPT];
+        __syncthreads();  // 3: the rows are written, and may be read by this token and the next
+        uint4 v[RPT];
+        float qs[RPT], q_scale[RPT];
+        const Entry* reads = entries + (t % kRing) * (W + R) + W;
+        const auto load_reads = [&](int r0) {
 #pragma unroll
             for (int j = 0; j < RPT; ++j) {
                 const int r = r0 + j * RS;
-                v[j] = make_uint4(0u, 0u, 0u, 0u);
-                qs[j] = 0.0f;
-                if (r < a.R) {
-                    const int64_t sl = bank_slot(a, a.q_idx, ts * a.R + r);
-                    if (sl >= 0 && active) {
-                        v[j] = __ldcg(codes + sl * a.pieces);
-                        qs[j] = __ldg(a.q_val + ts * a.R + r) * __ldcg(scales + sl * a.groups);
-                    }
-                }
+                const Entry e = reads[min(r, R - 1)];
+                const bool on = r < R && e.slot >= 0 && active;
+                qs[j] = e.weight;
+                v[j] = load16_if(codes + (int64_t)e.slot * a.pieces, on);
+                q_scale[j] = load4_if(scales + (int64_t)e.slot * a.groups, on);
             }
+        };
+        load_reads(rs);
+        if (t + 1 < a.T) load_writes(t + 1);
+        // the readings
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc2[i] = 0;
+        for (int r0 = 0;;) {  // alike for all threads: rows behind the end are zeros
 #pragma unroll
             for (int j = 0; j < RPT; ++j) {
-                F::unpack(v[j], x);
+                F::unpack2(v[j], x);
+                const float q = qs[j] * q_scale[j];
+                const f32x2 f = pair(q, q);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = fmaf(qs[j], x[i], acc[i]);
+                for (int i = 0; i < 8; ++i) acc2[i] = fma2(f, x[i], acc2[i]);
             }
+            r0 += RPT * RS;
+            if (r0 >= R) break;
+            load_reads(r0 + rs);
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split(acc2[i], acc[2 * i], acc[2 * i + 1]);
         first = reduce_rows<LR>(acc, lane);
 #pragma unroll
         for (int i = 0; i < KEEP; ++i) part_q[warp][lp * 16 + first + i] = acc[i];
-        __syncthreads();
-        for (int c = tid; c < COLS; c += NT) {
-            if (c0 + c >= hd) break;
-            float r = part_q[0][c];
-#pragma unroll
-            for (int q = 1; q < WARPS; ++q) r += part_q[q][c];
-            if (a.out_bf16)
-                static_cast<uint16_t*>(a.out)[ts * hd + c0 + c] = from_f32<uint16_t>(r);
-            else
-                static_cast<float*>(a.out)[ts * hd + c0 + c] = r;
+        if (t + 1 == a.T) {
+            __syncthreads();
+            if (column) put_out(t);
         }
-        // part_k, delta and part_q of the next token are written behind barriers that follow their
-        // last reads here
     }
 }
 
@@ -185,13 +267,19 @@ struct Chosen {
     int threads;
 };
 
+template <typename F, int LR, int NT, int RPT>
+Chosen with_items(int entries) {
+    if (entries <= NT) return {(const void*)qdecode_kernel<F, LR, NT, RPT, 1>, NT};
+    return {(const void*)qdecode_kernel<F, LR, NT, RPT, 512 / NT>, NT};
+}
+
 template <typename F, int LR>
-Chosen choose(int W) {
+Chosen choose(int W, int R) {
     constexpr int S = 128 / LR;  // row slots of 128 threads
-    if (W <= 2 * S) return {(const void*)qdecode_kernel<F, LR, 128, 2>, 128};
-    if (W <= 4 * S) return {(const void*)qdecode_kernel<F, LR, 128, 4>, 128};
-    if (W <= 8 * S) return {(const void*)qdecode_kernel<F, LR, 128, 8>, 128};
-    return {(const void*)qdecode_kernel<F, LR, 256, 8>, 256};
+    if (W <= 2 * S) return with_items<F, LR, 128, 2>(W + R);
+    if (W <= 4 * S) return with_items<F, LR, 128, 4>(W + R);
+    if (W <= 8 * S) return with_items<F, LR, 128, 8>(W + R);
+    return with_items<F, LR, 256, 8>(W + R);
 }
 
 }  // namespace
@@ -204,10 +292,11 @@ int launch_qdecode(const QDecodeArgs& a0, int format, cudaStream_t stream) {
     a.slices = narrow ? 1 : (a.pieces + 7) / 8;
     const int64_t blocks = a.n_streams * a.slices;
     if (blocks > INT_MAX) return SDM_ECOUNT;
-    const Chosen c = format == SDM_INT8 ? (narrow ? choose<Int8, 4>(a.W) : choose<Int8, 8>(a.W))
-                                        : (narrow ? choose<Fp8, 4>(a.W) : choose<Fp8, 8>(a.W));
+    const Chosen c = format == SDM_INT8 ? (narrow ? choose<Int8, 4>(a.W, a.R) : choose<Int8, 8>(a.W, a.R))
+                                        : (narrow ? choose<Fp8, 4>(a.W, a.R) : choose<Fp8, 8>(a.W, a.R));
+    const size_t smem = (size_t)kRing * (a.W + a.R) * sizeof(Entry);
     void* args[] = {&a};
-    return launch_pdl_raw(c.fn, dim3((unsigned)blocks), dim3((unsigned)c.threads), 0, stream, args);
+    return launch_pdl_raw(c.fn, dim3((unsigned)blocks), dim3((unsigned)c.threads), smem, stream, args);
 }
 
 int qdecode_status(unsigned int* word, bool clear) {

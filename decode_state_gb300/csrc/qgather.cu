@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(kThreads) qgather_kernel(const QGatherArgs a) 
     if (!u.live) return;  // unshared units only: a shared one fills its block
     const int lane = threadIdx.x & 31, rs = lane / LR, p = u.slice * LR + lane % LR;
     const int hd = a.hd, NR = a.width[u.op];
-    float acc[C];
+    f32x2 acc2[C / 2];
 #pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < C / 2; ++i) acc2[i] = 0;
 
     if (!padding(a, u.t)) {
         const bool active = p < a.pieces;
@@ -155,15 +155,19 @@ __global__ void __launch_bounds__(kThreads) qgather_kernel(const QGatherArgs a) 
                 }
 #pragma unroll
                 for (int s = 0; s < BATCH; ++s) {
-                    float x[C];
-                    F::unpack(v[s], x);
+                    f32x2 x[C / 2];
+                    F::unpack2(v[s], x);
+                    const f32x2 f = pair(ws[s], ws[s]);
 #pragma unroll
-                    for (int i = 0; i < C; ++i) acc[i] = fmaf(ws[s], x[i], acc[i]);
+                    for (int i = 0; i < C / 2; ++i) acc2[i] = fma2(f, x[i], acc2[i]);
                 }
             }
         }
     }
 
+    float acc[C];
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) split(acc2[i], acc[2 * i], acc[2 * i + 1]);
     const int first = reduce_scatter<C, LR>(acc, lane);
     if (a.split > 1) {  // the other warps' sums of the same columns
         float* mine = joined + (threadIdx.x) * KEEP;
@@ -246,10 +250,13 @@ __global__ void __launch_bounds__(kThreads) gather_dw_kernel(const QGatherArgs a
                     }
 #pragma unroll
                     for (int s = 0; s < BATCH; ++s) {
-                        float x[C], sum = 0.0f;
-                        F::unpack(v[s], x);
+                        f32x2 x[C / 2], sum2 = 0;
+                        F::unpack2(v[s], x);
 #pragma unroll
-                        for (int i = 0; i < C; ++i) sum = fmaf(d[i], x[i], sum);
+                        for (int i = 0; i < C / 2; ++i) sum2 = fma2(pair(d[2 * i], d[2 * i + 1]), x[i], sum2);
+                        float sum, odd;
+                        split(sum2, sum, odd);
+                        sum += odd;
                         if constexpr (F::kQuantised)
                             dot[s0 + s] = fmaf(sum, sc[s], dot[s0 + s]);
                         else

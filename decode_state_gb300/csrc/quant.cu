@@ -38,9 +38,9 @@ __device__ __forceinline__ void load_columns(const E* p, int n, bool vec, float*
         for (int i = 0; i < C / PER; ++i) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
             if constexpr (sizeof(E) == 2)
-                Bf16::unpack(v, x + PER * i);
+                unpack<Bf16>(v, x + PER * i);
             else
-                F32::unpack(v, x + PER * i);
+                unpack<F32>(v, x + PER * i);
         }
     } else {
 #pragma unroll
@@ -88,7 +88,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantRowsArgs 
     float x[C];
     load_columns<E, C>(static_cast<const E*>(a.rows) + (live ? r * a.row_stride + p * C : 0), live ? n : 0, a.vec, x);
     float scale;
-    const uint4 codes = quantise_piece<F>(x, a.group / C, &scale);
+    f32x2 x2[C / 2];
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) x2[i] = pair(x[2 * i], x[2 * i + 1]);
+    const uint4 codes = quantise_piece<F>(x2, a.group / C, &scale);
     if (slot < 0) return;
     if (p < a.pieces) reinterpret_cast<uint4*>(a.codes)[slot * a.pieces + p] = codes;
     if (p % (a.group / C) == 0) a.scales[slot * a.groups + p / (a.group / C)] = scale;
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const QuantRowsArg
     const int64_t slot = row_slot(a, r);
     float x[C];
     if (slot >= 0) {
-        F::unpack(__ldg(reinterpret_cast<const uint4*>(a.codes) + slot * a.pieces + p), x);
+        unpack<F>(__ldg(reinterpret_cast<const uint4*>(a.codes) + slot * a.pieces + p), x);
         const float s = __ldg(a.scales + slot * a.groups + p * C / a.group);
 #pragma unroll
         for (int i = 0; i < C; ++i) x[i] *= s;

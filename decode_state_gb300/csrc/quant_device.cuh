@@ -10,35 +10,106 @@
 
 namespace sdm {
 
-// A format has C columns in a 16-byte piece; unpack() gives their values without the scale, pack()
-// rounds values that are already divided by the scale. Every scale group (32, 64 or 128 columns) is
-// a whole number of pieces.
+// ---------------------------------------------------------------- loads that may be left out
+// A load of bank memory where `on`, zeros elsewhere, without a branch: loads in branches wait for one
+// another where loads of a batch should be on their way together.
 
-// Integer to float32 without the conversion unit (half rate): the byte, offset to be unsigned, goes
-// into the mantissa of 2^23, and the offset is subtracted exactly.
+__device__ __forceinline__ uint4 load16_if(const void* p, bool on) {
+    uint4 r;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@q ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+        : "l"(p), "r"((int)on)
+        : "memory");
+    return r;
+}
+__device__ __forceinline__ float load4_if(const float* p, bool on) {
+    float r;
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t@q ld.global.cg.b32 %0, [%1];\n\t}"
+                 : "=&f"(r)
+                 : "l"(p), "r"((int)on)
+                 : "memory");
+    return r;
+}
+
+// ---------------------------------------------------------------- pairs of float32
+// Two columns in one 64-bit register for the packed float32 instructions, which round like their
+// scalar forms at twice the rate.
+
+using f32x2 = uint64_t;
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(f32x2 p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// ---------------------------------------------------------------- formats
+// A format has C columns in a 16-byte piece; unpack2() gives their values without the scale, in
+// pairs, and pack2() rounds values that are already divided by the scale. Every scale group (32, 64
+// or 128 columns) is a whole number of pieces.
+//
+// Integers pass to and from float32 without the conversion unit (a quarter of the rate): a byte,
+// offset to be unsigned, goes into the mantissa of 2^23, and the offset is subtracted exactly; the
+// other way, adding 1.5 * 2^23 rounds to the nearest even integer and leaves it in the low bits.
+__device__ __forceinline__ uint32_t round_bits(float y) {
+    // the scalar sum: a packed sum behind a packed product is contracted with it, which rounds once
+    // where the format's definition rounds twice
+    return __float_as_uint(__fadd_rn(y, 12582912.0f));
+}
+
+template <typename F>
+__device__ __forceinline__ void unpack(const uint4& v, float* x) {
+    f32x2 p[F::C / 2];
+    F::unpack2(v, p);
+#pragma unroll
+    for (int i = 0; i < F::C / 2; ++i) split(p[i], x[2 * i], x[2 * i + 1]);
+}
+
 struct Int8 {
     static constexpr int C = 16;
     static constexpr bool kQuantised = true;
     static constexpr float kLevels = 127.0f;
-    static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
+    static constexpr float kInvHigh = 0x1.020408p-7f, kInvLow = 0x1.020408p-35f;  // 1 / 127
+    static __device__ __forceinline__ void unpack2(const uint4& v, f32x2* x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const f32x2 off = pair(-8388736.0f, -8388736.0f);  // -(2^23 + 128)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t u = w[i] ^ 0x80808080u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[4 * i + j] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440u + j)) - 8388736.0f;
+            for (int j = 0; j < 2; ++j)
+                x[2 * i + j] = add2(pair(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440u + 2 * j)),
+                                         __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441u + 2 * j))),
+                                    off);
         }
     }
-    static __device__ __forceinline__ uint4 pack(const float* y) {
+    static __device__ __forceinline__ uint4 pack2(const f32x2* y) {
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // saturating pack of two integers above the two packed before
-            const int a = __float2int_rn(y[4 * i]), b = __float2int_rn(y[4 * i + 1]), c = __float2int_rn(y[4 * i + 2]),
-                      d = __float2int_rn(y[4 * i + 3]);
-            uint32_t hi;
-            asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(hi) : "r"(d), "r"(c));
-            asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w[i]) : "r"(b), "r"(a), "r"(hi));
+        for (int i = 0; i < 4; ++i) {
+            float a, b, c, d;
+            split(y[2 * i], a, b);
+            split(y[2 * i + 1], c, d);
+            w[i] = __byte_perm(__byte_perm(round_bits(a), round_bits(b), 0x0040u), __byte_perm(round_bits(c), round_bits(d), 0x0040u),
+                               0x5410u);
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -48,25 +119,29 @@ struct Fp8 {
     static constexpr int C = 16;
     static constexpr bool kQuantised = true;
     static constexpr float kLevels = 448.0f;
-    static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
+    static constexpr float kInvHigh = 0x1.24924ap-9f, kInvLow = -0x1.b6db6ep-34f;  // 1 / 448
+    static __device__ __forceinline__ void unpack2(const uint4& v, f32x2* x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint16_t two = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
             uint32_t h;
+            float lo, hi;
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-            asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.f32.f16 %0, lo; cvt.f32.f16 %1, hi; }"
-                : "=f"(x[2 * i]), "=f"(x[2 * i + 1])
-                : "r"(h));
+            asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h; }" : "=f"(lo), "=f"(hi) : "r"(h));
+            x[i] = pair(lo, hi);
         }
     }
-    static __device__ __forceinline__ uint4 pack(const float* y) {
+    static __device__ __forceinline__ uint4 pack2(const f32x2* y) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            float a, b, c, d;
+            split(y[2 * i], a, b);
+            split(y[2 * i + 1], c, d);
             uint16_t lo, hi;
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[4 * i + 1]), "f"(y[4 * i]));
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[4 * i + 3]), "f"(y[4 * i + 2]));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
             w[i] = (uint32_t)lo | ((uint32_t)hi << 16);
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
@@ -77,25 +152,30 @@ struct Int4 {
     static constexpr int C = 32;
     static constexpr bool kQuantised = true;
     static constexpr float kLevels = 7.0f;
-    static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
+    static constexpr float kInvHigh = 0x1.24924ap-3f, kInvLow = -0x1.b6db6ep-28f;  // 1 / 7
+    static __device__ __forceinline__ void unpack2(const uint4& v, f32x2* x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const f32x2 off = pair(-8388616.0f, -8388616.0f);  // -(2^23 + 8)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t u = w[i] ^ 0x88888888u;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[8 * i + j] = __uint_as_float(((u >> (4 * j)) & 15u) | 0x4B000000u) - 8388616.0f;
+            for (int j = 0; j < 4; ++j)
+                x[4 * i + j] = add2(pair(__uint_as_float(((u >> (8 * j)) & 15u) | 0x4B000000u),
+                                         __uint_as_float(((u >> (8 * j + 4)) & 15u) | 0x4B000000u)),
+                                    off);
         }
     }
-    static __device__ __forceinline__ uint4 pack(const float* y) {
+    static __device__ __forceinline__ uint4 pack2(const f32x2* y) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             w[i] = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int q = max(-7, min(7, __float2int_rn(y[8 * i + j])));
-                w[i] |= ((uint32_t)q & 15u) << (4 * j);
+            for (int j = 0; j < 4; ++j) {
+                float a, b;
+                split(y[4 * i + j], a, b);
+                w[i] |= (round_bits(a) & 15u) << (8 * j) | (round_bits(b) & 15u) << (8 * j + 4);
             }
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
@@ -106,13 +186,10 @@ struct Bf16 {
     static constexpr int C = 8;
     static constexpr bool kQuantised = false;
     using E = uint16_t;
-    static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
+    static __device__ __forceinline__ void unpack2(const uint4& v, f32x2* x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
 };
 
@@ -120,46 +197,54 @@ struct F32 {
     static constexpr int C = 4;
     static constexpr bool kQuantised = false;
     using E = float;
-    static __device__ __forceinline__ void unpack(const uint4& v, float* x) {
-        x[0] = __uint_as_float(v.x);
-        x[1] = __uint_as_float(v.y);
-        x[2] = __uint_as_float(v.z);
-        x[3] = __uint_as_float(v.w);
+    static __device__ __forceinline__ void unpack2(const uint4& v, f32x2* x) {
+        x[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+        x[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
     }
 };
 
-// Bits of |x|: as unsigned integers they order like |x|, with infinity above every number and NaN
-// above infinity, so that one maximum finds the largest magnitude and any non-finite value.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// The largest of three magnitudes; NaN if there is one among them.
+__device__ __forceinline__ float abs_max(float m, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
+}
 
-// The scale of a group whose largest magnitude has the bits m, and the factor `inv` its values are
+// The scale of a group whose largest magnitude is `top`, and the factor `inv` its values are
 // multiplied with before rounding (0: codes of zero). Groups below 2^-100 become zeros, since the
 // factor would overflow for subnormal magnitudes; a non-finite group gets the scale NaN.
 template <typename F>
-__device__ __forceinline__ float group_scale(uint32_t m, float* inv) {
-    constexpr uint32_t kTiny = 0x0D800000u;  // 2^-100
+__device__ __forceinline__ float group_scale(float top, float* inv) {
     *inv = 0.0f;
-    if (m >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-    if (m < kTiny) return 0.0f;
-    const float top = __uint_as_float(m);
+    if (!(top <= 3.402823466e38f)) return __uint_as_float(0x7fc00000u);
+    if (top < 7.888609052e-31f) return 0.0f;  // 2^-100
     *inv = __fdiv_rn(F::kLevels, top);
-    return __fdiv_rn(top, F::kLevels);
+    // top / L correctly rounded in two operations, since L is known (Brisebarre, Muller: 1 / L as the
+    // sum of two floats; checked for every significand and at the ends of the range of exponents)
+    return fmaf(F::kInvHigh, top, __fmul_rn(F::kInvLow, top));
 }
 
 // Quantise this lane's C columns of a row whose groups lie on `lanes` neighbouring lanes each (a
 // power of two, aligned): the piece of codes, and the group's scale on every one of its lanes.
 template <typename F>
-__device__ __forceinline__ uint4 quantise_piece(const float* x, int lanes, float* scale) {
-    uint32_t m = 0;
+__device__ __forceinline__ uint4 quantise_piece(f32x2* x, int lanes, float* scale) {
+    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < F::C; ++i) m = max(m, abs_bits(x[i]));
+    for (int i = 0; i < F::C / 2; ++i) {
+        float a, b;
+        split(x[i], a, b);
+        top = abs_max(top, a, b);
+    }
+    // non-negative floats order like their bits, NaN above infinity
+    uint32_t m = __float_as_uint(top) & 0x7fffffffu;
     for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     float inv;
-    *scale = group_scale<F>(m, &inv);
-    float y[F::C];
+    *scale = group_scale<F>(__uint_as_float(m), &inv);
+    const f32x2 f = pair(inv, inv);
 #pragma unroll
-    for (int i = 0; i < F::C; ++i) y[i] = inv > 0.0f ? x[i] * inv : 0.0f;
-    return F::pack(y);
+    for (int i = 0; i < F::C / 2; ++i) x[i] = mul2(x[i], f);
+    const uint4 c = F::pack2(x);
+    return inv > 0.0f ? c : make_uint4(0u, 0u, 0u, 0u);
 }
 
 }  // namespace sdm

@@ -116,9 +116,9 @@ __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArg
         for (int i = 0; i < E * (int)sizeof(L) / 16; ++i) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + j0) + i);
             if constexpr (sizeof(L) == 2)
-                Bf16::unpack(v, x + 8 * i);
+                unpack<Bf16>(v, x + 8 * i);
             else
-                F32::unpack(v, x + 4 * i);
+                unpack<F32>(v, x + 4 * i);
         }
     } else {
 #pragma unroll
