@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(NT, RPT == 8 ? 1 : 4) qdecode_kernel(const QDe
     grid_launch_dependents();
 
     // this thread's entries of a token as they are loaded, and as they are kept
-    int64_t raw_slot[ITEMS];
+    // (an index waits as it was loaded: widening it would wait for it)
+    uint32_t raw_lo[ITEMS], raw_hi[ITEMS];
     float raw_weight[ITEMS], raw_gate[ITEMS], v_next = 0.0f, beta_next = 0.0f;
     const auto load_entries = [&](int t) {
         if (t >= a.T) return;
@@ -95,7 +96,9 @@ __global__ void __launch_bounds__(NT, RPT == 8 ? 1 : 4) qdecode_kernel(const QDe
                 const bool write = i < W;
                 const int64_t e = write ? ts * W + i : ts * R + (i - W);
                 const void* idx = write ? a.k_idx : a.q_idx;
-                raw_slot[n] = a.idx64 ? __ldg(static_cast<const int64_t*>(idx) + e) : __ldg(static_cast<const int32_t*>(idx) + e);
+                const uint32_t* word = static_cast<const uint32_t*>(idx) + (a.idx64 ? 2 * e : e);
+                raw_lo[n] = __ldg(word);
+                if (a.idx64) raw_hi[n] = __ldg(word + 1);
                 raw_weight[n] = __ldg((write ? a.k_val : a.q_val) + e);
                 raw_gate[n] = write ? __ldg(a.g + ts * a.G + (a.G == 1 ? 0 : i)) : 0.0f;
             }
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(NT, RPT == 8 ? 1 : 4) qdecode_kernel(const QDe
         for (int n = 0; n < ITEMS; ++n) {
             const int i = tid + n * NT;
             if (i < W + R) {
-                const int64_t x = raw_slot[n];
+                const int64_t x = a.idx64 ? (int64_t)((uint64_t)raw_hi[n] << 32 | raw_lo[n]) : (int64_t)(int32_t)raw_lo[n];
                 const bool in = x >= 0 && x < a.n_slots;
                 if (in) {
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(a.codes + (x * a.pieces + slice * LR) * 16));
@@ -137,12 +140,14 @@ __global__ void __launch_bounds__(NT, RPT == 8 ? 1 : 4) qdecode_kernel(const QDe
         for (int j = 0; j < RPT; ++j) {
             const int w = rs + j * RS;
             const Entry e = from[min(w, W - 1)];
-            const bool on = w < W && e.slot >= 0 && active;
-            slot[j] = on ? e.slot : -1;
+            slot[j] = w < W && active ? e.slot : -1;
             kv[j] = w < W ? e.weight : 0.0f;
             ds[j] = e.decay;
-            code[j] = load16_if(codes + (int64_t)e.slot * a.pieces, on);
-            row_scale[j] = load4_if(scales + (int64_t)e.slot * a.groups, on);
+        }
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+            code[j] = load16_if(codes + (int64_t)slot[j] * a.pieces, slot[j] >= 0);
+            row_scale[j] = load4_if(scales + (int64_t)slot[j] * a.groups, slot[j] >= 0);
         }
     };
 
@@ -204,32 +209,44 @@ __global__ void __launch_bounds__(NT, RPT == 8 ? 1 : 4) qdecode_kernel(const QDe
             dl[2 * i] = pair(f.x, f.y);
             dl[2 * i + 1] = pair(f.z, f.w);
         }
-#pragma unroll
-        for (int j = 0; j < RPT; ++j) {
-            F::unpack2(code[j], x);
+        // first every row's scale, then every row's codes from the columns computed again: the rows'
+        // chains of shuffles and divisions overlap, where all the columns would not fit the registers
+        const auto new_row = [&](int j, f32x2* y) {
+            F::unpack2(code[j], y);
             const f32x2 k2 = pair(kv[j], kv[j]), d2 = pair(ds[j], ds[j]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = fma2(k2, dl[i], mul2(d2, x[i]));
-            float sc;
-            const uint4 n = quantise_piece<F>(x, gl, &sc);
-            if (slot[j] >= 0) {
-                codes[(int64_t)slot[j] * a.pieces] = n;
-                if (lp % gl == 0) scales[(int64_t)slot[j] * a.groups] = sc;
-            }
+            for (int i = 0; i < 8; ++i) y[i] = fma2(k2, dl[i], mul2(d2, y[i]));
+        };
+        float top[RPT], new_scale[RPT], inv[RPT];
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+            new_row(j, x);
+            top[j] = piece_top<F>(x);
+        }
+        group_scales<F, RPT>(top, gl, new_scale, inv);
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+            new_row(j, x);
+            store16_if(codes + (int64_t)slot[j] * a.pieces, pack_piece<F>(x, inv[j]), slot[j] >= 0);
+            store4_if(scales + (int64_t)slot[j] * a.groups, new_scale[j], slot[j] >= 0 && lp % gl == 0);
         }
         __syncthreads();  // 3: the rows are written, and may be read by this token and the next
         uint4 v[RPT];
         float qs[RPT], q_scale[RPT];
         const Entry* reads = entries + (t % kRing) * (W + R) + W;
         const auto load_reads = [&](int r0) {
+            int sl[RPT];
 #pragma unroll
             for (int j = 0; j < RPT; ++j) {
                 const int r = r0 + j * RS;
                 const Entry e = reads[min(r, R - 1)];
-                const bool on = r < R && e.slot >= 0 && active;
+                sl[j] = r < R && active ? e.slot : -1;
                 qs[j] = e.weight;
-                v[j] = load16_if(codes + (int64_t)e.slot * a.pieces, on);
-                q_scale[j] = load4_if(scales + (int64_t)e.slot * a.groups, on);
+            }
+#pragma unroll
+            for (int j = 0; j < RPT; ++j) {
+                v[j] = load16_if(codes + (int64_t)sl[j] * a.pieces, sl[j] >= 0);
+                q_scale[j] = load4_if(scales + (int64_t)sl[j] * a.groups, sl[j] >= 0);
             }
         };
         load_reads(rs);

@@ -91,7 +91,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantRowsArgs 
     f32x2 x2[C / 2];
 #pragma unroll
     for (int i = 0; i < C / 2; ++i) x2[i] = pair(x[2 * i], x[2 * i + 1]);
-    const uint4 codes = quantise_piece<F>(x2, a.group / C, &scale);
+    const float top = piece_top<F>(x2);
+    float inv;
+    group_scales<F, 1>(&top, a.group / C, &scale, &inv);
+    const uint4 codes = pack_piece<F>(x2, inv);
     if (slot < 0) return;
     if (p < a.pieces) reinterpret_cast<uint4*>(a.codes)[slot * a.pieces + p] = codes;
     if (p % (a.group / C) == 0) a.scales[slot * a.groups + p / (a.group / C)] = scale;

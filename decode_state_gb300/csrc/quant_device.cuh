@@ -10,9 +10,9 @@
 
 namespace sdm {
 
-// ---------------------------------------------------------------- loads that may be left out
+// ---------------------------------------------------------------- loads and stores that may be left out
 // A load of bank memory where `on`, zeros elsewhere, without a branch: loads in branches wait for one
-// another where loads of a batch should be on their way together.
+// another where loads of a batch should be on their way together. Stores likewise.
 
 __device__ __forceinline__ uint4 load16_if(const void* p, bool on) {
     uint4 r;
@@ -31,6 +31,16 @@ __device__ __forceinline__ float load4_if(const float* p, bool on) {
                  : "l"(p), "r"((int)on)
                  : "memory");
     return r;
+}
+
+__device__ __forceinline__ void store16_if(void* p, const uint4& v, bool on) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t@q st.global.v4.b32 [%4], {%0, %1, %2, %3};\n\t}" ::"r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w), "l"(p), "r"((int)on)
+                 : "memory");
+}
+__device__ __forceinline__ void store4_if(float* p, float v, bool on) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q st.global.b32 [%1], %0;\n\t}" ::"f"(v), "l"(p), "r"((int)on)
+                 : "memory");
 }
 
 // ---------------------------------------------------------------- pairs of float32
@@ -210,24 +220,36 @@ __device__ __forceinline__ float abs_max(float m, float a, float b) {
     return r;
 }
 
+// L / x, correctly rounded, for the normal x that a group's largest magnitude can be (2^-100 and up),
+// without a branch: a division's rare path keeps the rows around it from overlapping. Markstein's
+// method: the reciprocal, corrected by its own residual, then the quotient by its; both residuals are
+// exact in a fused multiply-add. Large x are scaled so that the reciprocal stays normal.
+__device__ __forceinline__ float levels_over(float levels, float x) {
+    const float f = x > 0x1p64f ? 0x1p-64f : 1.0f;
+    const float y = x * f;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+    r = fmaf(fmaf(-y, r, 1.0f), r, r);
+    const float q = __fmul_rn(levels, r);
+    return fmaf(fmaf(-y, q, levels), r, q) * f;
+}
+
 // The scale of a group whose largest magnitude is `top`, and the factor `inv` its values are
 // multiplied with before rounding (0: codes of zero). Groups below 2^-100 become zeros, since the
 // factor would overflow for subnormal magnitudes; a non-finite group gets the scale NaN.
 template <typename F>
 __device__ __forceinline__ float group_scale(float top, float* inv) {
-    *inv = 0.0f;
-    if (!(top <= 3.402823466e38f)) return __uint_as_float(0x7fc00000u);
-    if (top < 7.888609052e-31f) return 0.0f;  // 2^-100
-    *inv = __fdiv_rn(F::kLevels, top);
+    const bool finite = top <= 3.402823466e38f, some = top >= 7.888609052e-31f;  // 2^-100
+    *inv = finite && some ? levels_over(F::kLevels, top) : 0.0f;
     // top / L correctly rounded in two operations, since L is known (Brisebarre, Muller: 1 / L as the
     // sum of two floats; checked for every significand and at the ends of the range of exponents)
-    return fmaf(F::kInvHigh, top, __fmul_rn(F::kInvLow, top));
+    const float scale = fmaf(F::kInvHigh, top, __fmul_rn(F::kInvLow, top));
+    return !finite ? __uint_as_float(0x7fc00000u) : some ? scale : 0.0f;
 }
 
-// Quantise this lane's C columns of a row whose groups lie on `lanes` neighbouring lanes each (a
-// power of two, aligned): the piece of codes, and the group's scale on every one of its lanes.
+// The largest magnitude of this lane's C columns.
 template <typename F>
-__device__ __forceinline__ uint4 quantise_piece(f32x2* x, int lanes, float* scale) {
+__device__ __forceinline__ float piece_top(const f32x2* x) {
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < F::C / 2; ++i) {
@@ -235,11 +257,31 @@ __device__ __forceinline__ uint4 quantise_piece(f32x2* x, int lanes, float* scal
         split(x[i], a, b);
         top = abs_max(top, a, b);
     }
-    // non-negative floats order like their bits, NaN above infinity
-    uint32_t m = __float_as_uint(top) & 0x7fffffffu;
-    for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float inv;
-    *scale = group_scale<F>(__uint_as_float(m), &inv);
+    return top;
+}
+
+// From the largest magnitudes of N rows' pieces to the scales of their groups, which lie on `lanes`
+// neighbouring lanes each (a power of two up to 8, aligned), and the factors to the codes.
+template <typename F, int N>
+__device__ __forceinline__ void group_scales(const float* top, int lanes, float* scale, float* inv) {
+    uint32_t m[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) m[n] = __float_as_uint(top[n]) & 0x7fffffffu;  // they order like their bits, NaN above infinity
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, m[n], o);
+            m[n] = o < lanes ? max(m[n], other) : m[n];
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) scale[n] = group_scale<F>(__uint_as_float(m[n]), &inv[n]);
+}
+
+// Codes of a piece with the factor of its group.
+template <typename F>
+__device__ __forceinline__ uint4 pack_piece(f32x2* x, float inv) {
     const f32x2 f = pair(inv, inv);
 #pragma unroll
     for (int i = 0; i < F::C / 2; ++i) x[i] = mul2(x[i], f);
