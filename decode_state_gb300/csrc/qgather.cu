@@ -55,20 +55,21 @@ __device__ __forceinline__ bool padding(const QGatherArgs& a, int64_t t) {
 }
 
 // the slot of entry i, or -1 (flagged) when it lies outside the bank
-__device__ __forceinline__ int64_t entry_slot(const QGatherArgs& a, const void* idx, int64_t i) {
+__device__ __forceinline__ int entry_slot(const QGatherArgs& a, const void* idx, int64_t i) {
     const int64_t s = a.idx64 ? __ldg(static_cast<const int64_t*>(idx) + i) : __ldg(static_cast<const int32_t*>(idx) + i);
-    if (s >= 0 && s < a.n_slots) return s;
+    if (s >= 0 && s < a.n_slots) return (int)s;
     atomicOr(&g_qgather_status, SDM_DEV_BAD_INDEX);
     return -1;
 }
 
 // 16 bytes of a row; `n` columns from the piece's first one on. Unaligned rows are read by columns.
 template <typename F, bool ALIGNED>
-__device__ __forceinline__ uint4 load_piece(const unsigned char* p, int n) {
+__device__ __forceinline__ uint4 load_piece(const unsigned char* p, int n, bool on) {
     if constexpr (ALIGNED) {
-        return __ldg(reinterpret_cast<const uint4*>(p));
+        return load16_if(p, on);
     } else {
         uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (!on) n = 0;
         using E = typename F::E;
         const E* e = reinterpret_cast<const E*>(p);
 #pragma unroll
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) qgather_kernel(const QGatherArgs a) 
         const float* scales = a.scales + (p * C) / a.group;
         const int64_t e0 = u.t * NR;
         for (int base = u.part * 32; base < NR; base += 32 * a.split) {
-            int64_t slot = -1;
+            int slot = -1;
             float w = 0.0f;
             if (base + lane < NR) {
                 slot = entry_slot(a, a.idx[u.op], e0 + base + lane);
@@ -139,25 +140,22 @@ __global__ void __launch_bounds__(kThreads) qgather_kernel(const QGatherArgs a) 
             for (int s0 = 0; s0 < LR; s0 += BATCH) {
                 if (base + s0 * SLOTS >= NR) break;
                 uint4 v[BATCH];
-                float ws[BATCH];
+                float ws[BATCH], sc[BATCH];
 #pragma unroll
                 for (int s = 0; s < BATCH; ++s) {
                     const int src = (s0 + s) * SLOTS + rs;
-                    const int64_t sl = __shfl_sync(kAll, slot, src);
+                    const int sl = __shfl_sync(kAll, slot, src);
                     ws[s] = __shfl_sync(kAll, w, src);
-                    v[s] = make_uint4(0u, 0u, 0u, 0u);
-                    if (sl >= 0 && active) {
-                        v[s] = __ldg(reinterpret_cast<const uint4*>(bank + sl * a.row_bytes));
-                        ws[s] *= __ldg(scales + sl * a.groups);
-                    } else {
-                        ws[s] = 0.0f;
-                    }
+                    const bool on = sl >= 0 && active;
+                    v[s] = load16_if(bank + sl * a.row_bytes, on);
+                    sc[s] = load4_if(scales + (int64_t)sl * a.groups, on);
                 }
 #pragma unroll
                 for (int s = 0; s < BATCH; ++s) {
                     f32x2 x[C / 2];
                     F::unpack2(v[s], x);
-                    const f32x2 f = pair(ws[s], ws[s]);
+                    const float fs = ws[s] * sc[s];
+                    const f32x2 f = pair(fs, fs);
 #pragma unroll
                     for (int i = 0; i < C / 2; ++i) acc2[i] = fma2(f, x[i], acc2[i]);
                 }
@@ -228,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) gather_dw_kernel(const QGatherArgs a
 #pragma unroll
         for (int s = 0; s < LR; ++s) dot[s] = 0.0f;
         if (!pad) {
-            const int64_t slot = base + lane < NR ? entry_slot(a, a.idx[u.op], e0 + base + lane) : -1;
+            const int slot = base + lane < NR ? entry_slot(a, a.idx[u.op], e0 + base + lane) : -1;
             for (int slice = 0; slice < slices; ++slice) {
                 const int p = slice * LR + lane % LR;
                 if (slices > 1) load_dout(p);
@@ -239,14 +237,11 @@ __global__ void __launch_bounds__(kThreads) gather_dw_kernel(const QGatherArgs a
                     float sc[BATCH];
 #pragma unroll
                     for (int s = 0; s < BATCH; ++s) {
-                        const int64_t sl = __shfl_sync(kAll, slot, rs * LR + s0 + s);
-                        v[s] = make_uint4(0u, 0u, 0u, 0u);
-                        sc[s] = 0.0f;
-                        if (sl >= 0 && p < a.pieces) {
-                            v[s] = load_piece<F, ALIGNED>(static_cast<const unsigned char*>(a.bank) + sl * a.row_bytes + (int64_t)p * 16,
-                                                          hd - p * C);
-                            if constexpr (F::kQuantised) sc[s] = __ldg(a.scales + sl * a.groups + p * C / a.group);
-                        }
+                        const int sl = __shfl_sync(kAll, slot, rs * LR + s0 + s);
+                        const bool on = sl >= 0 && p < a.pieces;
+                        v[s] = load_piece<F, ALIGNED>(static_cast<const unsigned char*>(a.bank) + sl * a.row_bytes + (int64_t)p * 16,
+                                                      hd - p * C, on);
+                        if constexpr (F::kQuantised) sc[s] = load4_if(a.scales + (int64_t)sl * a.groups + p * C / a.group, on);
                     }
 #pragma unroll
                     for (int s = 0; s < BATCH; ++s) {
