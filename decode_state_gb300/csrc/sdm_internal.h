@@ -80,7 +80,6 @@ struct QGatherArgs {
     int pieces, groups;    // 16-byte pieces and scale groups of a row
     int64_t row_bytes;     // from one row to the next
     int slices;            // column slices of a row, each the lanes of one row slot
-    int split;             // warps that share one token's entries
     int vec_out;           // out / dout rows are 16-byte aligned
 };
 
