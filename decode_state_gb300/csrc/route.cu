@@ -3,15 +3,20 @@
 // Math (include/sdm.h): scores s = softmax(x) or 1 / (1 + exp(-x)); entries ranked by x, s or
 // s + bias; best groups, then best entries, ties to the lower index; weights s, renormalised.
 //
-// Ranks are compared as 32-bit integers in the order of the floats: 0 for entries already taken (or
-// behind the end of a row), 1 for masked entries, and more for all others.
+// Ranks are compared as 32-bit integers in the order of the floats, 1 for masked entries and more for
+// all others.
 //
-// Two kernels. route_warp_kernel (n <= 1024, k <= 32): a warp keeps a token's ranks in registers,
-// lane l the consecutive entries from l * E on, so that the lowest lane that holds the maximum also
-// holds the lowest index; k rounds of a warp-wide maximum take the entries in order. route_block_kernel:
-// a block narrows the k-th rank down by histograms of its leading 11, then 11, then 10 bits, until at
-// most kCandidates entries can still be chosen (one or two passes over ranks kept in shared memory),
-// and sorts those by counting.
+// Both forward kernels find a lower bound of the k-th rank first: of the largest ranks of 32 lanes, or
+// of all threads of a block, the k-th largest is one, since k entries at least reach it. The entries
+// that reach it are few more than k; they are collected in shared memory and ranked by counting.
+// Where they are too many (equal ranks), or fewer than k entries are not masked, a slower path
+// follows that takes any ranks.
+//
+// route_warp_kernel (n <= 1024, k <= 32): a warp for each token, its ranks in registers, lane l the
+// consecutive entries from l * E on, so that lane order is index order. Bound by instructions (an
+// exponential and a reciprocal for every entry of a biased sigmoid), not by its 2 or 4 bytes.
+// route_block_kernel: a block for each token, its ranks staged in shared memory. The slower path
+// narrows the k-th rank down by histograms of its leading 11, then 11, then 10 bits.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -25,7 +30,7 @@ namespace {
 __device__ unsigned int g_route_status;
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr uint32_t kTaken = 0, kMasked = 1;
+constexpr uint32_t kMasked = 1;
 constexpr int kMaxGroups = 256, kMaxK = 256;
 constexpr int kCandidates = 512;
 constexpr size_t kStagedBytes = 192 * 1024;  // ranks a block keeps in shared memory
@@ -37,18 +42,33 @@ __device__ __forceinline__ bool masked(float x) { return !(x > minus_inf()); }  
 __device__ __forceinline__ float exp_below(float x, float m) {
     return masked(x) ? 0.0f : x == m ? 1.0f : expf(x - m);
 }
-__device__ __forceinline__ float sigmoid(float x) { return masked(x) ? 0.0f : __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x))); }
+__device__ __forceinline__ float sigmoid(float x) { return masked(x) ? 0.0f : __frcp_rn(__fadd_rn(1.0f, expf(-x))); }
+
+// Scores of N logits: sigmoid() bit by bit (any value for masked ones), but without a branch for each,
+// so that they overlap. A reciprocal of a float in [1, 2^126] is correctly rounded by one Newton step from the
+// hardware's approximation (checked for every significand); the rare others are done again.
+template <int N>
+__device__ __forceinline__ void sigmoids(const float* x, float* s) {
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float y = __fadd_rn(1.0f, expf(masked(x[i]) ? 0.0f : -x[i]));
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+        s[i] = fmaf(fmaf(-y, r, 1.0f), r, r);
+        most = fmaxf(most, y);
+    }
+    if (most > 0x1p126f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = __frcp_rn(__fadd_rn(1.0f, expf(-x[i])));
+    }
+}
 
 // A float as an unsigned integer in the same order (-0 and +0 alike); masked ranks become kMasked.
 __device__ __forceinline__ uint32_t ordered(float r) {
     if (masked(r)) return kMasked;
     const uint32_t b = __float_as_uint(r + 0.0f);
     return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
-}
-
-__device__ __forceinline__ float logit(const RouteArgs& a, int64_t t, int j) {
-    const int64_t i = t * a.row_stride + j;
-    return a.logit_bf16 ? to_f32(__ldg(static_cast<const uint16_t*>(a.logits) + i)) : __ldg(static_cast<const float*>(a.logits) + i);
 }
 
 __device__ __forceinline__ void put_index(const RouteArgs& a, int64_t t, int i, int j) {
@@ -78,6 +98,10 @@ struct Top2 {
         a = fmaxf(a, x);
         b = fmaxf(b, low);
     }
+    __device__ __forceinline__ void join(float oa, float ob) {  // the two largest of another set
+        add(oa);
+        b = fmaxf(b, ob);  // ob <= oa: it is second at best
+    }
     // a group's score, as an ordered integer: 0 for a group of masked entries
     __device__ __forceinline__ uint32_t score(int group_top) const {
         if (a == minus_inf()) return 0;
@@ -93,25 +117,59 @@ __device__ __forceinline__ bool group_stays(const uint32_t* scores, int groups, 
     return better < top;
 }
 
+// The inputs of a rank as 64 bits that order first by rank, then by the lower index.
+__device__ __forceinline__ uint64_t candidate(uint32_t rank, int j) { return (uint64_t)rank << 32 | (uint32_t)~j; }
+__device__ __forceinline__ int candidate_index(uint64_t c) { return (int)~(uint32_t)c; }
+
 // ---------------------------------------------------------------- a warp for each token
 
-constexpr int kWarpThreads = 128;
+constexpr int kWarpThreads = 256;
+constexpr int kWarpCandidates = 64;
+
+// The k-th largest of the 32 lanes' values, and the largest, on every lane (a bitonic sort).
+__device__ __forceinline__ float kth_of_lanes(float x, int k, float* most) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+        for (int o = size / 2; o >= 1; o /= 2) {
+            const float y = __shfl_xor_sync(kAll, x, o);
+            const bool larger = ((lane & o) == 0) == ((lane & size) == 0);  // falling order
+            x = larger ? fmaxf(x, y) : fminf(x, y);
+        }
+    }
+    *most = __shfl_sync(kAll, x, 0);
+    return __shfl_sync(kAll, x, k - 1);
+}
+
+__device__ __forceinline__ int lanes_before(int own, int* all) {
+    const int lane = threadIdx.x & 31;
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, sum, o);
+        if (lane >= o) sum += y;
+    }
+    *all = __shfl_sync(kAll, sum, 31);
+    return sum - own;
+}
 
 // E: entries of a lane. L: uint16_t (bf16) or float logits.
 template <int E, typename L>
 __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArgs a) {
-    extern __shared__ float staged[];  // with groups: every warp's group values [n] and scores [n_groups]
+    constexpr int WARPS = kWarpThreads / 32;
+    extern __shared__ float staged[];  // groups that are no whole lanes: every warp's group values [n] and scores [n_groups]
+    __shared__ uint64_t found[WARPS][kWarpCandidates];
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * (kWarpThreads / 32) + warp;
+    const int64_t t = (int64_t)blockIdx.x * WARPS + warp;
     if (t >= a.tokens) return;
-    const int n = a.n, j0 = lane * E;
+    const int n = a.n, k = a.k, j0 = lane * E;
     const L* row = static_cast<const L*>(a.logits) + t * a.row_stride;
 
     float x[E];
-    const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0 && j0 + E <= n;
-    if (vec) {
+    if ((reinterpret_cast<uintptr_t>(row) & 15u) == 0 && j0 + E <= n) {
 #pragma unroll
         for (int i = 0; i < E * (int)sizeof(L) / 16; ++i) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + j0) + i);
@@ -125,115 +183,191 @@ __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArg
         for (int i = 0; i < E; ++i) x[i] = j0 + i < n ? to_f32(__ldg(row + j0 + i)) : minus_inf();
     }
 
-    const bool softmax = a.score == SDM_SOFTMAX;
-    const bool by_sum = a.n_groups > 1 && a.group_top == 2;
-    float m = 0.0f, total = 1.0f;
-    if (softmax) {
-        m = minus_inf();
+    const bool softmax = a.score == SDM_SOFTMAX, biased = a.bias != nullptr;
+    const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups, by_sum = grouped && a.group_top == 2;
+    float m = minus_inf(), total = 1.0f;
+    if (softmax && (biased || !a.renorm || by_sum)) {
 #pragma unroll
         for (int i = 0; i < E; ++i) m = fmaxf(m, x[i]);  // NaN takes no part
         m = warp_max(m);
-        if (a.bias != nullptr || !a.renorm) {
+        if (biased || !a.renorm) {
             total = 0.0f;
 #pragma unroll
             for (int i = 0; i < E; ++i) total += exp_below(x[i], m);
             total = warp_sum(total);
         }
     }
-    uint32_t key[E];
+    // ranks, -inf where masked
+    float r[E];
+    if (!softmax) {
+        sigmoids<E>(x, r);
+    } else if (biased) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        float r = x[i];
-        if (!masked(x[i])) {
-            if (!softmax)
-                r = sigmoid(x[i]);
-            else if (a.bias != nullptr)
-                r = __fdiv_rn(exp_below(x[i], m), total);
-            if (a.bias != nullptr) r += __ldg(a.bias + j0 + i);
-        }
-        key[i] = j0 + i < n ? ordered(r) : kTaken;
-        // what the groups are judged by, from here on in x
-        x[i] = masked(r) ? minus_inf() : softmax && a.bias == nullptr && by_sum ? exp_below(x[i], m) : r;
+        for (int i = 0; i < E; ++i) r[i] = __fdiv_rn(exp_below(x[i], m), total);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) r[i] = x[i];
     }
-
-    if (a.n_groups > 1 && a.top_groups < a.n_groups) {
-        float* value = staged + (size_t)warp * (n + a.n_groups);
-        uint32_t* scores = reinterpret_cast<uint32_t*>(value + n);
-        const int per = n / a.n_groups;
+    if (biased) {
+        if ((reinterpret_cast<uintptr_t>(a.bias) & 15u) == 0 && j0 + E <= n) {
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (j0 + i < n) value[j0 + i] = x[i];
-        __syncwarp();
-        for (int g = lane; g < a.n_groups; g += 32) {
+            for (int i = 0; i < E / 4; ++i) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(a.bias + j0) + i);
+                r[4 * i] += f.x, r[4 * i + 1] += f.y, r[4 * i + 2] += f.z, r[4 * i + 3] += f.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (j0 + i < n) r[i] += __ldg(a.bias + j0 + i);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) r[i] = masked(x[i]) || masked(r[i]) ? minus_inf() : r[i];
+
+    if (grouped) {
+        const bool sums = by_sum && softmax && !biased;  // judged by exp(x - m), not by the ranks
+        const int per = n / a.n_groups, lanes = per / E;
+        if (per % E == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0) {
+            // whole lanes, a power of two of them: by shuffles
             Top2 top;
-            int at = lane % per;  // lanes start apart, since groups are often a multiple of the banks
-            for (int i = 0; i < per; ++i) {
-                top.add(value[g * per + at]);
-                at = at + 1 == per ? 0 : at + 1;
+#pragma unroll
+            for (int i = 0; i < E; ++i) top.add(sums ? (r[i] == minus_inf() ? minus_inf() : exp_below(x[i], m)) : r[i]);
+            for (int o = 1; o < lanes; o <<= 1) top.join(__shfl_xor_sync(kAll, top.a, o), __shfl_xor_sync(kAll, top.b, o));
+            const uint32_t mine = top.score(a.group_top);
+            const int g = lane / lanes;
+            int better = 0;
+            for (int q = 0; q < a.n_groups; ++q) {
+                const uint32_t other = __shfl_sync(kAll, mine, q * lanes);
+                better += other > mine || (other == mine && q < g);
             }
-            scores[g] = top.score(a.group_top);
-        }
-        __syncwarp();
-        uint32_t stays[kMaxGroups / 32];  // bit `lane` of word i: group 32 i + lane
+            if (better >= a.top_groups) {
 #pragma unroll
-        for (int i = 0; i < kMaxGroups / 32; ++i) {
-            const int g = 32 * i + lane;
-            if (32 * i < a.n_groups)
-                stays[i] = __ballot_sync(kAll, g < a.n_groups && group_stays(scores, a.n_groups, a.top_groups, g));
-        }
-        __syncwarp();
-        if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < kMaxGroups / 32; ++i)
-                if (32 * i < a.n_groups) scores[i] = stays[i];
-        }
-        __syncwarp();
-        int g = j0 / per, left = per - j0 % per;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (j0 + i < n && !((scores[g >> 5] >> (g & 31)) & 1u)) key[i] = kMasked;
-            if (--left == 0) {
-                ++g;
-                left = per;
+                for (int i = 0; i < E; ++i) r[i] = minus_inf();
             }
-        }
-    }
-
-    uint32_t best = 0;
+        } else {
+            float* value = staged + (size_t)warp * (n + a.n_groups);
+            uint32_t* scores = reinterpret_cast<uint32_t*>(value + n);
 #pragma unroll
-    for (int i = 0; i < E; ++i) best = max(best, key[i]);
-    int mine = 0;  // lane r: the entry taken in round r, and whether it is a live one
-    bool live = false;
-    for (int r = 0; r < a.k; ++r) {
-        const uint32_t top = __reduce_max_sync(kAll, best);
-        const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
-        int at = 0;
-        if (lane == src) {
+            for (int i = 0; i < E; ++i)
+                if (j0 + i < n) value[j0 + i] = sums ? (r[i] == minus_inf() ? minus_inf() : exp_below(x[i], m)) : r[i];
+            __syncwarp();
+            for (int g = lane; g < a.n_groups; g += 32) {
+                Top2 top;
+                int at = lane % per;  // lanes start apart, since groups are often a multiple of the banks
+                for (int i = 0; i < per; ++i) {
+                    top.add(value[g * per + at]);
+                    at = at + 1 == per ? 0 : at + 1;
+                }
+                scores[g] = top.score(a.group_top);
+            }
+            __syncwarp();
+            uint32_t stays[kMaxGroups / 32];  // bit `lane` of word i: group 32 i + lane
 #pragma unroll
-            for (int i = E - 1; i >= 0; --i)
-                if (key[i] == top) at = i;
-            best = 0;
+            for (int i = 0; i < kMaxGroups / 32; ++i) {
+                const int g = 32 * i + lane;
+                if (32 * i < a.n_groups)
+                    stays[i] = __ballot_sync(kAll, g < a.n_groups && group_stays(scores, a.n_groups, a.top_groups, g));
+            }
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < kMaxGroups / 32; ++i)
+                    if (32 * i < a.n_groups) scores[i] = stays[i];
+            }
+            __syncwarp();
+            int g = j0 / per, left = per - j0 % per;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                if (i == at) key[i] = kTaken;
-                best = max(best, key[i]);
+                if (j0 + i < n && !((scores[g >> 5] >> (g & 31)) & 1u)) r[i] = minus_inf();
+                if (--left == 0) {
+                    ++g;
+                    left = per;
+                }
             }
         }
-        const int j = __shfl_sync(kAll, j0 + at, src);
-        if (lane == r) {
-            mine = j;
-            live = top != kMasked;
+    }
+
+    // the entries that reach the k-th largest of the lanes' maxima
+    float best = r[0];
+#pragma unroll
+    for (int i = 1; i < E; ++i) best = fmaxf(best, r[i]);
+    float most;
+    const float bound = kth_of_lanes(best, k, &most);
+    if (softmax && !biased && a.renorm) m = most;  // any reference does: it cancels in the weights
+    int own = 0, count;
+#pragma unroll
+    for (int i = 0; i < E; ++i) own += r[i] >= bound && r[i] > minus_inf();
+    int at = lanes_before(own, &count);
+    uint64_t* cand = found[warp];
+    const bool many = count > kWarpCandidates;
+    if (!many) {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (r[i] >= bound && r[i] > minus_inf()) cand[at++] = candidate(ordered(r[i]), j0 + i);
+    } else {
+        // too many alike: k rounds of a maximum over the warp, the lowest index first
+        for (int round = 0; round < k; ++round) {
+            const uint32_t top = __reduce_max_sync(kAll, ordered(best));
+            const int src = __ffs(__ballot_sync(kAll, ordered(best) == top)) - 1;  // there are more than k live ones
+            if (lane == src) {
+                int hit = 0;
+#pragma unroll
+                for (int i = E - 1; i >= 0; --i)
+                    if (ordered(r[i]) == top) hit = i;
+                best = minus_inf();
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    if (i == hit) r[i] = minus_inf();
+                    best = fmaxf(best, r[i]);
+                }
+                cand[round] = candidate(top, j0 + hit);
+            }
+        }
+        count = k;
+    }
+    __syncwarp();
+    uint64_t mine[kWarpCandidates / 32];
+    int rank[kWarpCandidates / 32];
+    float score[kWarpCandidates / 32], sum = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kWarpCandidates / 32; ++q) {
+        rank[q] = k;
+        score[q] = 0.0f;
+        if (lane + 32 * q < count) {
+            mine[q] = cand[lane + 32 * q];
+            rank[q] = 0;
+            for (int o = 0; o < count; ++o) rank[q] += cand[o] > mine[q];
+            if (rank[q] < k) {
+                const float y = to_f32(__ldg(row + candidate_index(mine[q])));
+                score[q] = softmax ? exp_below(y, m) : sigmoid(y);
+                sum += score[q];
+            }
         }
     }
-    float s = 0.0f;
-    if (lane < a.k && live) {
-        const float y = to_f32(__ldg(row + mine));
-        s = softmax ? exp_below(y, m) : sigmoid(y);
+    if (a.renorm) total = warp_sum(sum);
+#pragma unroll
+    for (int q = 0; q < kWarpCandidates / 32; ++q) {
+        if (rank[q] < k) {
+            put_index(a, t, rank[q], candidate_index(mine[q]));
+            a.w[t * k + rank[q]] = total > 0.0f && (softmax || a.renorm) ? __fdiv_rn(score[q], total) * a.scale : score[q] * a.scale;
+        }
     }
-    if (a.renorm) total = warp_sum(s);
-    if (lane < a.k) {
-        put_index(a, t, lane, mine);
-        a.w[t * a.k + lane] = total > 0.0f && (softmax || a.renorm) ? __fdiv_rn(s, total) * a.scale : s * a.scale;
+    if (count < k) {  // fill up with masked entries, in index order
+        own = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) own += j0 + i < n && r[i] == minus_inf();
+        int all;
+        at = count + lanes_before(own, &all);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (j0 + i < n && r[i] == minus_inf()) {
+                if (at < k) {
+                    put_index(a, t, at, j0 + i);
+                    a.w[t * k + at] = 0.0f;
+                }
+                ++at;
+            }
+        }
     }
 }
 
@@ -251,10 +385,10 @@ __device__ __forceinline__ float block_reduce(float x, bool sum, float* tmp, int
     return r;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(NT) route_block_kernel(const RouteArgs a, int staged) {
+template <int NT, typename L>
+__global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(const RouteArgs a, int staged) {
     constexpr int WARPS = NT / 32;
-    extern __shared__ uint32_t keys[];  // [n] when staged
+    extern __shared__ __align__(16) uint32_t keys[];  // [n] when staged
     __shared__ int hist[kBins];
     __shared__ uint64_t cand[kCandidates];
     __shared__ uint32_t scores[kMaxGroups];
@@ -272,20 +406,56 @@ __global__ void __launch_bounds__(NT) route_block_kernel(const RouteArgs a, int 
     const bool softmax = a.score == SDM_SOFTMAX, biased = a.bias != nullptr;
     const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups;
     const int per = n / a.n_groups;
+    const L* row = static_cast<const L*>(a.logits) + t * a.row_stride;
+    const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+    constexpr int V = 16 / sizeof(L);  // logits of a 16-byte load
 
-    float m = 0.0f, total = 1.0f;
-    if (softmax) {
-        m = minus_inf();
-        for (int j = tid; j < n; j += NT) m = fmaxf(m, logit(a, t, j));
+    // f(j, x) for every logit: whole 16 bytes where the row is aligned
+    const auto each = [&](const auto& f) {
+        int first = 0;
+        if (vec) {
+            first = n / V * V;
+            int j = tid * V;
+            for (; j + 3 * NT * V < first; j += 4 * NT * V) {  // four loads on their way together
+                uint4 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[u] = __ldg(reinterpret_cast<const uint4*>(row + j + u * NT * V));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float x[V];
+                    if constexpr (sizeof(L) == 2)
+                        unpack<Bf16>(v[u], x);
+                    else
+                        unpack<F32>(v[u], x);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) f(j + u * NT * V + i, x[i]);
+                }
+            }
+            for (; j < first; j += NT * V) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + j));
+                float x[V];
+                if constexpr (sizeof(L) == 2)
+                    unpack<Bf16>(v, x);
+                else
+                    unpack<F32>(v, x);
+#pragma unroll
+                for (int i = 0; i < V; ++i) f(j + i, x[i]);
+            }
+        }
+        for (int j = first + tid; j < n; j += NT) f(j, to_f32(__ldg(row + j)));
+    };
+
+    float m = minus_inf(), total = 1.0f;
+    if (softmax && (biased || !a.renorm || (grouped && a.group_top == 2))) {
+        each([&](int, float x) { m = fmaxf(m, x); });
         m = block_reduce(m, false, tmp, WARPS);
         if (biased || !a.renorm) {
             total = 0.0f;
-            for (int j = tid; j < n; j += NT) total += exp_below(logit(a, t, j), m);
+            each([&](int, float x) { total += exp_below(x, m); });
             total = block_reduce(total, true, tmp, WARPS);
         }
     }
-    const auto rank_of = [&](int j) {
-        const float x = logit(a, t, j);
+    const auto rank_of = [&](int j, float x) {
         if (masked(x)) return x;
         float r = x;
         if (!softmax)
@@ -300,14 +470,10 @@ __global__ void __launch_bounds__(NT) route_block_kernel(const RouteArgs a, int 
             Top2 top;
             for (int i = lane; i < per; i += 32) {
                 const int j = g * per + i;
-                const float r = rank_of(j);
-                top.add(masked(r) ? minus_inf() : softmax && !biased && a.group_top == 2 ? exp_below(logit(a, t, j), m) : r);
+                const float x = to_f32(__ldg(row + j)), r = rank_of(j, x);
+                top.add(masked(r) ? minus_inf() : softmax && !biased && a.group_top == 2 ? exp_below(x, m) : r);
             }
-            for (int o = 16; o; o >>= 1) {
-                const float oa = __shfl_xor_sync(kAll, top.a, o), ob = __shfl_xor_sync(kAll, top.b, o);
-                top.add(oa);
-                top.b = fmaxf(top.b, ob);  // ob <= oa: it is second at best
-            }
+            for (int o = 16; o; o >>= 1) top.join(__shfl_xor_sync(kAll, top.a, o), __shfl_xor_sync(kAll, top.b, o));
             if (lane == 0) scores[g] = top.score(a.group_top);
         }
         __syncthreads();
@@ -318,49 +484,33 @@ __global__ void __launch_bounds__(NT) route_block_kernel(const RouteArgs a, int 
         }
         __syncthreads();
     }
-    const auto make_key = [&](int j) -> uint32_t {
+    const auto make_key = [&](int j, float x) -> uint32_t {
         if (grouped) {
             const int g = j / per;
             if (!((stays[g >> 5] >> (g & 31)) & 1u)) return kMasked;
         }
-        return ordered(rank_of(j));
+        return ordered(rank_of(j, x));
     };
-    if (staged) {
-        for (int j = tid; j < n; j += NT) keys[j] = make_key(j);
-    }
-    const auto key_at = [&](int j) -> uint32_t { return staged ? keys[j] : make_key(j); };
+    uint32_t best = 0;  // the largest rank of this thread's entries
+    each([&](int j, float x) {
+        const uint32_t key = make_key(j, x);
+        best = max(best, key);
+        if (staged) keys[j] = key;
+    });
+    const auto key_at = [&](int j) -> uint32_t { return staged ? keys[j] : make_key(j, to_f32(__ldg(row + j))); };
 
-    // narrow the k-th rank down: `above` live entries lie above the prefix, and those of the prefix
-    // and above are at most kCandidates, or all their bits are fixed
-    uint32_t lowest = 0;  // candidates are the live entries with key >= lowest
-    int above = 0, need = k, inside = 0;
-    bool few = false, exact = false;  // fewer than k live entries; the prefix is a whole key
-    uint32_t prefix = 0;
-    for (int level = 0; level < 3; ++level) {
-        const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
-        for (int b = tid; b < kBins; b += NT) hist[b] = 0;
-        __syncthreads();
-        for (int j = tid; j < n; j += NT) {
-            const uint32_t key = key_at(j);
-            if (key > kMasked && (level == 0 || key >> (shift + bits) == prefix))
-                atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1);
-        }
-        __syncthreads();
-        // the bin of the need-th largest: thread i owns the PER bins from the top, i * PER on
-        constexpr int PER = kBins / NT;
+    // the bin of the need-th largest of the values counted in hist, from the top: found_bin (-1: there
+    // are fewer), and found_above, those in higher bins; counts holds the warps' shares of all of them
+    const auto find_bin = [&](int need) {
+        constexpr int PER = kBins / NT;  // thread i owns the PER bins from i * PER on, counted from the top
         int own = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) own += hist[kBins - 1 - (tid * PER + i)];
-        int sum = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kAll, sum, o);
-            if (lane >= o) sum += y;
-        }
-        if (lane == 31) counts[warp] = sum;
+        int all;
+        int before = lanes_before(own, &all);
+        if (lane == 31) counts[warp] = all;
         if (tid == 0) found_bin = -1;
         __syncthreads();
-        int before = sum - own;
         for (int i = 0; i < warp; ++i) before += counts[i];
         if (before < need && before + own >= need) {
             for (int i = 0; i < PER; ++i) {
@@ -374,44 +524,97 @@ __global__ void __launch_bounds__(NT) route_block_kernel(const RouteArgs a, int 
             }
         }
         __syncthreads();
-        if (found_bin < 0) {  // level 0 only: all live entries are taken
-            few = true;
-            int all = 0;
-            for (int i = 0; i < WARPS; ++i) all += counts[i];
-            above = all;
-            lowest = kMasked + 1;
-            break;
-        }
-        above += found_above;
-        need -= found_above;
-        prefix = (prefix << bits) | (uint32_t)found_bin;
-        inside = hist[found_bin];
-        lowest = prefix << shift;
-        exact = level == 2;
+    };
+    const auto clear_bins = [&]() {
+        for (int b = tid; b < kBins; b += NT) hist[b] = 0;
         __syncthreads();
-        if (above + inside <= kCandidates) break;
-    }
-    // candidates: everything from `lowest` on, or only what lies above when too many share the last rank
-    const bool ties = !few && exact && above + inside > kCandidates;
-    if (tid == 0) n_cand = 0;
-    __syncthreads();
-    for (int j = tid; j < n; j += NT) {
-        const uint32_t key = key_at(j);
-        if (key > kMasked && (ties ? key > lowest : key >= lowest))
-            cand[atomicAdd(&n_cand, 1)] = ((uint64_t)key << 32) | (uint32_t)~j;
-    }
-    __syncthreads();
-    const int C = n_cand;
-    for (int c = tid; c < C; c += NT) {
-        const uint64_t mine = cand[c];
-        int better = 0;
-        for (int o = 0; o < C; ++o) better += cand[o] > mine;
-        if (better < k) {
-            const int j = (int)~(uint32_t)mine;
-            sel_j[better] = j;
-            const float x = logit(a, t, j);
-            sel_s[better] = softmax ? exp_below(x, m) : sigmoid(x);
+    };
+    // candidates: the live entries with key >= lowest; those that fit are kept
+    const auto collect = [&](uint32_t lowest) {
+        if (tid == 0) n_cand = 0;
+        __syncthreads();
+        const auto test = [&](uint32_t key, int j) {
+            if (key > kMasked && key >= lowest) {
+                const int c = atomicAdd(&n_cand, 1);
+                if (c < kCandidates) cand[c] = candidate(key, j);
+            }
+        };
+        if (staged) {
+            const int whole = n / 4 * 4;
+            for (int j = tid * 4; j < whole; j += NT * 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(keys + j);
+                test(v.x, j), test(v.y, j + 1), test(v.z, j + 2), test(v.w, j + 3);
+            }
+            for (int j = whole + tid; j < n; j += NT) test(keys[j], j);
+        } else {
+            for (int j = tid; j < n; j += NT) test(key_at(j), j);
         }
+        __syncthreads();
+    };
+
+    // a lower bound by the threads' maxima
+    clear_bins();
+    if (best > kMasked) atomicAdd(&hist[best >> 21], 1);
+    __syncthreads();
+    find_bin(k);
+    bool done = false, few = false, ties = false;
+    uint32_t lowest = 0;
+    int C = 0;
+    if (found_bin >= 0) {
+        collect((uint32_t)found_bin << 21);
+        C = n_cand;
+        done = C <= kCandidates;
+    }
+    if (!done) {
+        // narrow the k-th rank down: `above` live entries lie above the prefix, and those of the prefix
+        // and above are at most kCandidates, or all their bits are fixed
+        int above = 0, need = k, inside = 0;
+        bool exact = false;  // the prefix is a whole key
+        uint32_t prefix = 0;
+        for (int level = 0; level < 3; ++level) {
+            const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
+            __syncthreads();
+            clear_bins();
+            for (int j = tid; j < n; j += NT) {
+                const uint32_t key = key_at(j);
+                if (key > kMasked && (level == 0 || key >> (shift + bits) == prefix))
+                    atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1);
+            }
+            __syncthreads();
+            find_bin(need);
+            if (found_bin < 0) {  // level 0 only: all live entries are taken
+                few = true;
+                lowest = kMasked + 1;
+                break;
+            }
+            above += found_above;
+            need -= found_above;
+            prefix = (prefix << bits) | (uint32_t)found_bin;
+            inside = hist[found_bin];
+            lowest = prefix << shift;
+            exact = level == 2;
+            if (above + inside <= kCandidates) break;
+        }
+        // only what lies above the last rank when too many share it
+        ties = !few && exact && above + inside > kCandidates;
+        collect(ties ? lowest + 1 : lowest);
+        C = n_cand;
+    }
+    // rank the candidates by counting, four threads for each
+    for (int c0 = 0; c0 < C; c0 += NT / 4) {
+        const int c = c0 + tid / 4;
+        const uint64_t mine = c < C ? cand[c] : 0;
+        int better = 0;
+        for (int o = tid % 4; o < C; o += 4) better += cand[o] > mine;
+        better += __shfl_xor_sync(kAll, better, 1);
+        better += __shfl_xor_sync(kAll, better, 2);
+        if (c < C && better < k && tid % 4 == 0) sel_j[better] = candidate_index(mine);
+    }
+    __syncthreads();
+    if (softmax && !biased && a.renorm && C > 0) m = to_f32(__ldg(row + sel_j[0]));  // any reference does: it cancels
+    for (int i = tid; i < min(C, k); i += NT) {
+        const float x = to_f32(__ldg(row + sel_j[i]));
+        sel_s[i] = softmax ? exp_below(x, m) : sigmoid(x);
     }
     // fill up, in index order, with entries of the shared last rank, or with masked ones of weight 0
     if (few || ties) {
@@ -430,7 +633,8 @@ __global__ void __launch_bounds__(NT) route_block_kernel(const RouteArgs a, int 
             }
             if (hit && at < k) {
                 sel_j[at] = j;
-                const float x = logit(a, t, j);
+                const float x = to_f32(__ldg(row + j));
+                if (softmax && !biased && a.renorm && C == 0) m = x;  // all that are taken share this logit
                 sel_s[at] = few ? 0.0f : softmax ? exp_below(x, m) : sigmoid(x);
             }
             __syncthreads();
@@ -569,12 +773,14 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     if (a.tokens > INT_MAX) return SDM_ECOUNT;
     int staged = (size_t)a.n * 4 <= kStagedBytes ? 1 : 0;
     const size_t smem = staged ? (size_t)a.n * 4 : 0;
-    const void* fn = a.n > 4096 ? (const void*)route_block_kernel<512> : (const void*)route_block_kernel<128>;
+    const bool large = a.n > 4096;
+    const void* fn = a.logit_bf16 ? (large ? (const void*)route_block_kernel<512, uint16_t> : (const void*)route_block_kernel<128, uint16_t>)
+                                  : (large ? (const void*)route_block_kernel<512, float> : (const void*)route_block_kernel<128, float>);
     // the limit without a request counts the kernel's static arrays (16 KB) too
     const int rc = allow_smem(fn, smem > 32 * 1024 ? std::max(smem, (size_t)48 * 1024 + 16) : smem);
     if (rc != 0) return rc;
     void* args[] = {&a, &staged};
-    return launch_pdl_raw(fn, dim3((unsigned)a.tokens), dim3(a.n > 4096 ? 512 : 128), smem, stream, args);
+    return launch_pdl_raw(fn, dim3((unsigned)a.tokens), dim3(large ? 512 : 128), smem, stream, args);
 }
 
 int launch_route_backward(const RouteArgs& a0, cudaStream_t stream) {
