@@ -14,7 +14,8 @@
 //
 // route_warp_kernel (n <= 1024, k <= 32): a warp for each token, its ranks in registers, lane l the
 // consecutive entries from l * E on, so that lane order is index order. Bound by instructions (an
-// exponential and a reciprocal for every entry of a biased sigmoid), not by its 2 or 4 bytes.
+// exponential and a reciprocal for every entry of a biased sigmoid), not by its 2 or 4 bytes; small
+// rows get half a warp, which halves what is spent on a token rather than on its entries.
 // route_block_kernel: a block for each token, its ranks staged in shared memory. The slower path
 // narrows the k-th rank down by histograms of its leading 11, then 11, then 10 bits.
 #include <algorithm>
@@ -102,70 +103,115 @@ struct Top2 {
         add(oa);
         b = fmaxf(b, ob);  // ob <= oa: it is second at best
     }
-    // a group's score, as an ordered integer: 0 for a group of masked entries
-    __device__ __forceinline__ uint32_t score(int group_top) const {
-        if (a == minus_inf()) return 0;
-        return ordered(group_top == 1 ? a : a + (b == minus_inf() ? 0.0f : b));
+    // a group's score: -inf for a group of masked entries
+    __device__ __forceinline__ float value(int group_top) const {
+        return group_top == 1 || b == minus_inf() ? a : a + b;
     }
 };
 
 // Whether group g is among the `top` best of scores[0 .. groups), ties to the lower index.
-__device__ __forceinline__ bool group_stays(const uint32_t* scores, int groups, int top, int g) {
-    const uint32_t mine = scores[g];
+__device__ __forceinline__ bool group_stays(const float* scores, int groups, int top, int g) {
+    const float mine = scores[g];
     int better = 0;
     for (int o = 0; o < groups; ++o) better += scores[o] > mine || (scores[o] == mine && o < g);
     return better < top;
 }
 
-// The inputs of a rank as 64 bits that order first by rank, then by the lower index.
+// A candidate as 64 bits that order first by rank, then by the lower index.
 __device__ __forceinline__ uint64_t candidate(uint32_t rank, int j) { return (uint64_t)rank << 32 | (uint32_t)~j; }
 __device__ __forceinline__ int candidate_index(uint64_t c) { return (int)~(uint32_t)c; }
 
-// ---------------------------------------------------------------- a warp for each token
-
-constexpr int kWarpThreads = 256;
-constexpr int kWarpCandidates = 64;
-
-// The k-th largest of the 32 lanes' values, and the largest, on every lane (a bitonic sort).
-__device__ __forceinline__ float kth_of_lanes(float x, int k, float* most) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int size = 2; size <= 32; size *= 2) {
-#pragma unroll
-        for (int o = size / 2; o >= 1; o /= 2) {
-            const float y = __shfl_xor_sync(kAll, x, o);
-            const bool larger = ((lane & o) == 0) == ((lane & size) == 0);  // falling order
-            x = larger ? fmaxf(x, y) : fminf(x, y);
-        }
-    }
-    *most = __shfl_sync(kAll, x, 0);
-    return __shfl_sync(kAll, x, k - 1);
-}
-
+// The sum of `own` over the lanes of this lane's LANES before it, and over all of them.
+template <int LANES>
 __device__ __forceinline__ int lanes_before(int own, int* all) {
-    const int lane = threadIdx.x & 31;
+    const int l = threadIdx.x % LANES;
     int sum = own;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kAll, sum, o);
-        if (lane >= o) sum += y;
+    for (int o = 1; o < LANES; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, sum, o, LANES);
+        if (l >= o) sum += y;
     }
-    *all = __shfl_sync(kAll, sum, 31);
+    *all = __shfl_sync(kAll, sum, LANES - 1, LANES);
     return sum - own;
 }
 
-// E: entries of a lane. L: uint16_t (bf16) or float logits.
-template <int E, typename L>
+// ---------------------------------------------------------------- a warp, or half of one, for each token
+
+constexpr int kWarpThreads = 256;
+
+// The k-th largest of V values on each of LANES lanes, on every lane: a bitonic sort, in falling order,
+// value s of lane l at place l * V + s. Where a stage sorts in rising order the signs are turned, so
+// that a step asks for one bit of the lane only.
+template <int LANES, int V>
+__device__ __forceinline__ float kth_of_lanes(float* x, int k) {
+    static_assert(V == 1 || V == 2, "one or two values");
+    const uint32_t l = threadIdx.x % LANES;
+    uint32_t turned = 0;
+#pragma unroll
+    for (int size = 2; size <= LANES * V; size *= 2) {
+        const uint32_t turn = size < LANES * V && (l & size / V) ? 0x80000000u : 0u;
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = __uint_as_float(__float_as_uint(x[v]) ^ turn ^ turned);
+        turned = turn;
+#pragma unroll
+        for (int o = size / 2; o >= V; o /= 2) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float y = __shfl_xor_sync(kAll, x[v], o / V);
+                x[v] = l & o / V ? fminf(x[v], y) : fmaxf(x[v], y);
+            }
+        }
+        if (V == 2) {
+            const float high = fmaxf(x[0], x[V - 1]);
+            x[V - 1] = fminf(x[0], x[V - 1]);
+            x[0] = high;
+        }
+    }
+    return __shfl_sync(kAll, V == 2 && !(k & 1) ? x[V - 1] : x[0], (k - 1) / V, LANES);
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float x) {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, o));
+    return x;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+    return x;
+}
+
+// A sigmoid from the hardware's approximations: within 2^-21 of the score (ex2 to 2^-22, its argument
+// rounded once, rcp to 2^-23, and the score's own roundings).
+__device__ __forceinline__ float rough_sigmoid(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
+// LANES lanes work on a token, E entries each, the consecutive ones from l * E on, so that the order of
+// the lanes is the order of the indices. L: uint16_t (bf16) or float logits.
+//
+// The ranks of a sigmoid are first computed roughly, with a margin, at a third of the instructions;
+// what is near enough to matter is computed exactly: the candidates, and all entries where two groups
+// are too close to call.
+template <int LANES, int E, bool SOFTMAX, typename L>
 __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArgs a) {
-    constexpr int WARPS = kWarpThreads / 32;
-    extern __shared__ float staged[];  // groups that are no whole lanes: every warp's group values [n] and scores [n_groups]
-    __shared__ uint64_t found[WARPS][kWarpCandidates];
+    constexpr int TEAMS = kWarpThreads / LANES, CANDS = 2 * LANES;
+    extern __shared__ float staged[];  // groups that are no whole lanes: every team's group values [n] and scores [n_groups]
+    __shared__ uint16_t found[TEAMS][CANDS];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * WARPS + warp;
-    if (t >= a.tokens) return;
-    const int n = a.n, k = a.k, j0 = lane * E;
+    const int l = threadIdx.x % LANES, team = threadIdx.x / LANES, first_lane = threadIdx.x % 32 / LANES * LANES;
+    const int64_t token = (int64_t)blockIdx.x * TEAMS + team;
+    if (token - (threadIdx.x % 32) / LANES >= a.tokens) return;  // a whole warp
+    const bool there = token < a.tokens;
+    const int64_t t = there ? token : a.tokens - 1;  // spare teams work along on the last token, and write nothing
+    const int n = a.n, k = a.k, j0 = l * E;
+    const uint32_t team_bits = LANES == 32 ? kAll : (1u << LANES % 32) - 1u;
     const L* row = static_cast<const L*>(a.logits) + t * a.row_stride;
 
     float x[E];
@@ -183,32 +229,29 @@ __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArg
         for (int i = 0; i < E; ++i) x[i] = j0 + i < n ? to_f32(__ldg(row + j0 + i)) : minus_inf();
     }
 
-    const bool softmax = a.score == SDM_SOFTMAX, biased = a.bias != nullptr;
+    constexpr bool softmax = SOFTMAX;
+    const bool biased = a.bias != nullptr;
     const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups, by_sum = grouped && a.group_top == 2;
+    const bool by_exp = by_sum && softmax && !biased;  // groups judged by exp(x - m), not by the ranks
     float m = minus_inf(), total = 1.0f;
-    if (softmax && (biased || !a.renorm || by_sum)) {
+    if (softmax) {
 #pragma unroll
         for (int i = 0; i < E; ++i) m = fmaxf(m, x[i]);  // NaN takes no part
-        m = warp_max(m);
+        m = lanes_max<LANES>(m);
         if (biased || !a.renorm) {
             total = 0.0f;
 #pragma unroll
             for (int i = 0; i < E; ++i) total += exp_below(x[i], m);
-            total = warp_sum(total);
+            total = lanes_sum<LANES>(total);
         }
     }
+    const int per = n / a.n_groups, group_lanes = per / E;
+    const bool by_lanes = per % E == 0 && group_lanes <= LANES && (group_lanes & (group_lanes - 1)) == 0;
+    bool rough = !softmax && (!grouped || by_lanes);
+
     // ranks, -inf where masked
     float r[E];
-    if (!softmax) {
-        sigmoids<E>(x, r);
-    } else if (biased) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) r[i] = __fdiv_rn(exp_below(x[i], m), total);
-    } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) r[i] = x[i];
-    }
-    if (biased) {
+    const auto add_bias = [&]() {
         if ((reinterpret_cast<uintptr_t>(a.bias) & 15u) == 0 && j0 + E <= n) {
 #pragma unroll
             for (int i = 0; i < E / 4; ++i) {
@@ -220,153 +263,209 @@ __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArg
             for (int i = 0; i < E; ++i)
                 if (j0 + i < n) r[i] += __ldg(a.bias + j0 + i);
         }
-    }
+    };
+    const auto exact_ranks = [&]() {
+        if (!softmax) {
+            sigmoids<E>(x, r);
+        } else {
 #pragma unroll
-    for (int i = 0; i < E; ++i) r[i] = masked(x[i]) || masked(r[i]) ? minus_inf() : r[i];
+            for (int i = 0; i < E; ++i) r[i] = biased ? __fdiv_rn(exp_below(x[i], m), total) : x[i];
+        }
+        if (biased) add_bias();
+#pragma unroll
+        for (int i = 0; i < E; ++i) r[i] = masked(x[i]) ? minus_inf() : fmaxf(r[i], minus_inf());  // the number of the two
+    };
+    if (rough) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) r[i] = rough_sigmoid(x[i]);
+        if (biased) add_bias();
+#pragma unroll
+        for (int i = 0; i < E; ++i) r[i] = masked(x[i]) ? minus_inf() : fmaxf(r[i], minus_inf());
+    } else {
+        exact_ranks();
+    }
+    const auto margin = [](float at) { return fmaf(fabsf(at), 0x1p-20f, 0x1p-18f); };  // eight errors, for differences of sums of two
 
-    if (grouped) {
-        const bool sums = by_sum && softmax && !biased;  // judged by exp(x - m), not by the ranks
-        const int per = n / a.n_groups, lanes = per / E;
-        if (per % E == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0) {
-            // whole lanes, a power of two of them: by shuffles
+    if (grouped && by_lanes) {
+        // groups of whole lanes, a power of two of them
+        const auto judge = [&]() {
             Top2 top;
 #pragma unroll
-            for (int i = 0; i < E; ++i) top.add(sums ? (r[i] == minus_inf() ? minus_inf() : exp_below(x[i], m)) : r[i]);
-            for (int o = 1; o < lanes; o <<= 1) top.join(__shfl_xor_sync(kAll, top.a, o), __shfl_xor_sync(kAll, top.b, o));
-            const uint32_t mine = top.score(a.group_top);
-            const int g = lane / lanes;
-            int better = 0;
+            for (int i = 0; i < E; ++i) top.add(by_exp ? (r[i] == minus_inf() ? minus_inf() : exp_below(x[i], m)) : r[i]);
+            for (int o = 1; o < group_lanes; o <<= 1) top.join(__shfl_xor_sync(kAll, top.a, o), __shfl_xor_sync(kAll, top.b, o));
+            return top.value(a.group_top);
+        };
+        const int g = l / group_lanes;
+        float mine = judge();
+        int better = 0, near = 0;  // groups that are surely better; and those that may be
+        if (rough) {
+            const float d = mine == minus_inf() ? 0.0f : margin(mine), high = mine + d, low = mine - d;
+            for (int q = 0, from = 0; q < a.n_groups; ++q, from += group_lanes) {
+                const float other = __shfl_sync(kAll, mine, from, LANES);
+                better += other > high;
+                near += other >= low;
+            }
+            --near;  // the group itself
+        }
+        if (!rough || __any_sync(kAll, better < a.top_groups && near >= a.top_groups)) {
+            if (rough) {
+                exact_ranks();
+                mine = judge();
+                rough = false;
+            }
+            better = 0;
             for (int q = 0; q < a.n_groups; ++q) {
-                const uint32_t other = __shfl_sync(kAll, mine, q * lanes);
+                const float other = __shfl_sync(kAll, mine, q * group_lanes, LANES);
                 better += other > mine || (other == mine && q < g);
             }
-            if (better >= a.top_groups) {
+        }
+        if (better >= a.top_groups) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) r[i] = minus_inf();
+            for (int i = 0; i < E; ++i) r[i] = minus_inf();
+        }
+    } else if (grouped) {
+        float* value = staged + (size_t)team * (n + a.n_groups);
+        float* scores = value + n;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (j0 + i < n) value[j0 + i] = by_exp ? (r[i] == minus_inf() ? minus_inf() : exp_below(x[i], m)) : r[i];
+        __syncwarp();
+        for (int g = l; g < a.n_groups; g += LANES) {
+            Top2 top;
+            int at = l % per;  // lanes start apart, since groups are often a multiple of the banks
+            for (int i = 0; i < per; ++i) {
+                top.add(value[g * per + at]);
+                at = at + 1 == per ? 0 : at + 1;
             }
-        } else {
-            float* value = staged + (size_t)warp * (n + a.n_groups);
-            uint32_t* scores = reinterpret_cast<uint32_t*>(value + n);
+            scores[g] = top.value(a.group_top);
+        }
+        __syncwarp();
+        uint32_t* stays = reinterpret_cast<uint32_t*>(value);  // the values have been read
+        for (int g = l; g < a.n_groups; g += LANES) stays[g] = group_stays(scores, a.n_groups, a.top_groups, g);
+        __syncwarp();
+        int g = j0 / per, left = per - j0 % per;
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (j0 + i < n) value[j0 + i] = sums ? (r[i] == minus_inf() ? minus_inf() : exp_below(x[i], m)) : r[i];
-            __syncwarp();
-            for (int g = lane; g < a.n_groups; g += 32) {
-                Top2 top;
-                int at = lane % per;  // lanes start apart, since groups are often a multiple of the banks
-                for (int i = 0; i < per; ++i) {
-                    top.add(value[g * per + at]);
-                    at = at + 1 == per ? 0 : at + 1;
-                }
-                scores[g] = top.score(a.group_top);
-            }
-            __syncwarp();
-            uint32_t stays[kMaxGroups / 32];  // bit `lane` of word i: group 32 i + lane
-#pragma unroll
-            for (int i = 0; i < kMaxGroups / 32; ++i) {
-                const int g = 32 * i + lane;
-                if (32 * i < a.n_groups)
-                    stays[i] = __ballot_sync(kAll, g < a.n_groups && group_stays(scores, a.n_groups, a.top_groups, g));
-            }
-            __syncwarp();
-            if (lane == 0) {
-#pragma unroll
-                for (int i = 0; i < kMaxGroups / 32; ++i)
-                    if (32 * i < a.n_groups) scores[i] = stays[i];
-            }
-            __syncwarp();
-            int g = j0 / per, left = per - j0 % per;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                if (j0 + i < n && !((scores[g >> 5] >> (g & 31)) & 1u)) r[i] = minus_inf();
-                if (--left == 0) {
-                    ++g;
-                    left = per;
-                }
+        for (int i = 0; i < E; ++i) {
+            if (j0 + i < n && !stays[g]) r[i] = minus_inf();
+            if (--left == 0) {
+                ++g;
+                left = per;
             }
         }
     }
 
-    // the entries that reach the k-th largest of the lanes' maxima
-    float best = r[0];
+    // the entries that reach the k-th largest of the maxima of the lanes' entries (half a warp: of both halves of them)
+    constexpr int V = 32 / LANES;
+    float best[V];
 #pragma unroll
-    for (int i = 1; i < E; ++i) best = fmaxf(best, r[i]);
-    float most;
-    const float bound = kth_of_lanes(best, k, &most);
-    if (softmax && !biased && a.renorm) m = most;  // any reference does: it cancels in the weights
-    int own = 0, count;
+    for (int v = 0; v < V; ++v) {
+        best[v] = r[v * (E / V)];
 #pragma unroll
-    for (int i = 0; i < E; ++i) own += r[i] >= bound && r[i] > minus_inf();
-    int at = lanes_before(own, &count);
-    uint64_t* cand = found[warp];
-    const bool many = count > kWarpCandidates;
-    if (!many) {
+        for (int i = 1; i < E / V; ++i) best[v] = fmaxf(best[v], r[v * (E / V) + i]);
+    }
+    float bound = kth_of_lanes<LANES, V>(best, k);
+    if (rough && bound > minus_inf()) bound -= margin(bound);
+    bound = fmaxf(bound, -3.402823466e38f);  // masked entries never reach it
+    uint32_t reach = 0;  // bit i: entry i does
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (r[i] >= bound && r[i] > minus_inf()) cand[at++] = candidate(ordered(r[i]), j0 + i);
-    } else {
-        // too many alike: k rounds of a maximum over the warp, the lowest index first
+    for (int i = 0; i < E; ++i) reach |= r[i] >= bound ? 1u << i : 0u;
+    int count;
+    int at = lanes_before<LANES>(__popc(reach), &count);
+    uint16_t* cand = found[team];
+    if (__any_sync(kAll, count > CANDS)) {
+        // too many alike: k rounds of a maximum over the lanes, the lowest index first
+        if (rough) {
+            uint32_t gone = 0;
+#pragma unroll
+            for (int i = 0; i < E; ++i) gone |= r[i] == minus_inf() ? 1u << i : 0u;
+            exact_ranks();
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (gone >> i & 1u) r[i] = minus_inf();
+        }
+        uint32_t live = 0, taken = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) live |= r[i] > minus_inf() ? 1u << i : 0u;
+        int all;
+        lanes_before<LANES>(__popc(live), &all);
+        count = min(k, all);
         for (int round = 0; round < k; ++round) {
-            const uint32_t top = __reduce_max_sync(kAll, ordered(best));
-            const int src = __ffs(__ballot_sync(kAll, ordered(best) == top)) - 1;  // there are more than k live ones
-            if (lane == src) {
-                int hit = 0;
+            float own = minus_inf();
 #pragma unroll
-                for (int i = E - 1; i >= 0; --i)
-                    if (ordered(r[i]) == top) hit = i;
-                best = minus_inf();
+            for (int i = 0; i < E; ++i) own = taken >> i & 1u ? own : fmaxf(own, r[i]);
+            const float top = lanes_max<LANES>(own);
+            const uint32_t holders = __ballot_sync(kAll, own == top) >> first_lane & team_bits;
+            if (round < count && l == __ffs(holders) - 1) {
+                uint32_t hit = 0;
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    if (i == hit) r[i] = minus_inf();
-                    best = fmaxf(best, r[i]);
-                }
-                cand[round] = candidate(top, j0 + hit);
+                for (int i = 0; i < E; ++i) hit |= r[i] == top ? 1u << i : 0u;
+                const int i = __ffs(hit & ~taken) - 1;
+                taken |= 1u << i;
+                cand[round] = (uint16_t)(j0 + i);
             }
         }
-        count = k;
+    } else {
+        for (; reach; reach &= reach - 1) cand[at++] = (uint16_t)(j0 + __ffs(reach) - 1);
     }
     __syncwarp();
-    uint64_t mine[kWarpCandidates / 32];
-    int rank[kWarpCandidates / 32];
-    float score[kWarpCandidates / 32], sum = 0.0f;
+    // exact ranks of the candidates; where they were collected their order is that of the indices,
+    // and where they were taken in rounds it is that of the ranks: equal ranks go by the place
+    int j[2], rank[2] = {0, 0};
+    float score[2] = {0.0f, 0.0f}, key[2] = {minus_inf(), minus_inf()};
+    const bool two = __any_sync(kAll, count > LANES);  // a second candidate for some lanes
+    const auto rate = [&](int q) {
+        if (l + LANES * q < count) {
+            j[q] = cand[l + LANES * q];
+            const float y = to_f32(__ldg(row + j[q]));
+            score[q] = softmax ? exp_below(y, m) : sigmoid(y);
+            key[q] = !softmax ? score[q] : biased ? __fdiv_rn(score[q], total) : y;
+            if (biased) key[q] += __ldg(a.bias + j[q]);
+        }
+    };
+    rate(0);
+    if (two) rate(1);
+    const int most = min(LANES, LANES == 32 ? count : max(count, __shfl_xor_sync(kAll, count, 16)));
+    for (int o0 = 0; o0 < most; o0 += 4) {
 #pragma unroll
-    for (int q = 0; q < kWarpCandidates / 32; ++q) {
-        rank[q] = k;
-        score[q] = 0.0f;
-        if (lane + 32 * q < count) {
-            mine[q] = cand[lane + 32 * q];
-            rank[q] = 0;
-            for (int o = 0; o < count; ++o) rank[q] += cand[o] > mine[q];
-            if (rank[q] < k) {
-                const float y = to_f32(__ldg(row + candidate_index(mine[q])));
-                score[q] = softmax ? exp_below(y, m) : sigmoid(y);
-                sum += score[q];
-            }
+        for (int o = o0; o < o0 + 4; ++o) {
+            const float other = __shfl_sync(kAll, key[0], o, LANES);  // -inf behind the last one: better than none
+            rank[0] += other > key[0] || (other == key[0] && o < l);
+            if (two) rank[1] += other >= key[1];
         }
     }
-    if (a.renorm) total = warp_sum(sum);
-#pragma unroll
-    for (int q = 0; q < kWarpCandidates / 32; ++q) {
-        if (rank[q] < k) {
-            put_index(a, t, rank[q], candidate_index(mine[q]));
-            a.w[t * k + rank[q]] = total > 0.0f && (softmax || a.renorm) ? __fdiv_rn(score[q], total) * a.scale : score[q] * a.scale;
+    if (two) {
+        for (int o = 0; o < LANES; ++o) {
+            const float other = __shfl_sync(kAll, key[1], o, LANES);
+            rank[0] += other > key[0];
+            rank[1] += other > key[1] || (other == key[1] && o < l);
         }
     }
+    const bool mine[2] = {l < count && rank[0] < k, two && l + LANES < count && rank[1] < k};
+    if (a.renorm) total = lanes_sum<LANES>((mine[0] ? score[0] : 0.0f) + (mine[1] ? score[1] : 0.0f));
+    const float factor = (softmax || a.renorm) && total > 0.0f ? __fdividef(a.scale, total) : a.scale;
+    if (!there) return;
+    const int64_t to = t * k;
+    const auto put = [&](int q) {
+        if (mine[q]) {
+            put_index(a, t, rank[q], j[q]);
+            a.w[to + rank[q]] = score[q] * factor;
+        }
+    };
+    put(0);
+    if (two) put(1);
     if (count < k) {  // fill up with masked entries, in index order
-        own = 0;
+        uint32_t gone = 0;
 #pragma unroll
-        for (int i = 0; i < E; ++i) own += j0 + i < n && r[i] == minus_inf();
-        int all;
-        at = count + lanes_before(own, &all);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (j0 + i < n && r[i] == minus_inf()) {
-                if (at < k) {
-                    put_index(a, t, at, j0 + i);
-                    a.w[t * k + at] = 0.0f;
-                }
-                ++at;
-            }
+        for (int i = 0; i < E; ++i) gone |= j0 + i < n && r[i] == minus_inf() ? 1u << i : 0u;
+        const int own = __popc(gone);
+        at = count;
+        for (int o = 0; o < LANES; ++o) {
+            const int y = __shfl_sync(team_bits << first_lane, own, o, LANES);
+            if (o < l) at += y;
+        }
+        for (; gone && at < k; gone &= gone - 1, ++at) {
+            put_index(a, t, at, j0 + __ffs(gone) - 1);
+            a.w[to + at] = 0.0f;
         }
     }
 }
@@ -391,7 +490,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
     extern __shared__ __align__(16) uint32_t keys[];  // [n] when staged
     __shared__ int hist[kBins];
     __shared__ uint64_t cand[kCandidates];
-    __shared__ uint32_t scores[kMaxGroups];
+    __shared__ float scores[kMaxGroups];
     __shared__ uint32_t stays[kMaxGroups / 32];
     __shared__ float tmp[WARPS];
     __shared__ int counts[WARPS];
@@ -474,7 +573,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
                 top.add(masked(r) ? minus_inf() : softmax && !biased && a.group_top == 2 ? exp_below(x, m) : r);
             }
             for (int o = 16; o; o >>= 1) top.join(__shfl_xor_sync(kAll, top.a, o), __shfl_xor_sync(kAll, top.b, o));
-            if (lane == 0) scores[g] = top.score(a.group_top);
+            if (lane == 0) scores[g] = top.value(a.group_top);
         }
         __syncthreads();
         for (int g0 = warp * 32; g0 < a.n_groups; g0 += NT) {
@@ -507,7 +606,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
 #pragma unroll
         for (int i = 0; i < PER; ++i) own += hist[kBins - 1 - (tid * PER + i)];
         int all;
-        int before = lanes_before(own, &all);
+        int before = lanes_before<32>(own, &all);
         if (lane == 31) counts[warp] = all;
         if (tid == 0) found_bin = -1;
         __syncthreads();
@@ -749,11 +848,17 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel
     (void)lane;
 }
 
+template <typename L, bool SOFTMAX>
+const void* warp_kernel(int n, bool half) {
+    if (half) return n <= 128 ? (const void*)route_warp_kernel<16, 8, SOFTMAX, L> : (const void*)route_warp_kernel<16, 16, SOFTMAX, L>;
+    return n <= 256   ? (const void*)route_warp_kernel<32, 8, SOFTMAX, L>
+           : n <= 512 ? (const void*)route_warp_kernel<32, 16, SOFTMAX, L>
+                      : (const void*)route_warp_kernel<32, 32, SOFTMAX, L>;
+}
+
 template <typename L>
-const void* warp_kernel(int n) {
-    return n <= 256   ? (const void*)route_warp_kernel<8, L>
-           : n <= 512 ? (const void*)route_warp_kernel<16, L>
-                      : (const void*)route_warp_kernel<32, L>;
+const void* warp_kernel(int n, bool half, bool softmax) {
+    return softmax ? warp_kernel<L, true>(n, half) : warp_kernel<L, false>(n, half);
 }
 
 }  // namespace
@@ -761,13 +866,18 @@ const void* warp_kernel(int n) {
 int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     RouteArgs a = a0;
     if (a.n <= 1024 && a.k <= 32) {
-        constexpr int WARPS = kWarpThreads / 32;
-        const int64_t blocks = (a.tokens + WARPS - 1) / WARPS;
-        if (blocks > INT_MAX) return SDM_ECOUNT;
+        // half a warp for each token where the maxima of its lanes (two each) whose groups stay bound k entries well
         const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups;
-        const size_t smem = grouped ? (size_t)WARPS * (a.n + a.n_groups) * 4 : 0;
+        const int live = (grouped ? a.n / a.n_groups * a.top_groups : a.n) / (a.n <= 128 ? 4 : 8);
+        const bool half = a.n <= 256 && 2 * a.k <= live;
+        const int teams = kWarpThreads / (half ? 16 : 32);
+        const int64_t blocks = (a.tokens + teams - 1) / teams;
+        if (blocks > INT_MAX) return SDM_ECOUNT;
+        const size_t smem = grouped ? (size_t)teams * (a.n + a.n_groups) * 4 : 0;
         void* args[] = {&a};
-        return launch_pdl_raw(a.logit_bf16 ? warp_kernel<uint16_t>(a.n) : warp_kernel<float>(a.n), dim3((unsigned)blocks),
+        return launch_pdl_raw(a.logit_bf16 ? warp_kernel<uint16_t>(a.n, half, a.score == SDM_SOFTMAX)
+                                           : warp_kernel<float>(a.n, half, a.score == SDM_SOFTMAX),
+                              dim3((unsigned)blocks),
                               dim3(kWarpThreads), smem, stream, args);
     }
     if (a.tokens > INT_MAX) return SDM_ECOUNT;
