@@ -117,6 +117,9 @@ __device__ __forceinline__ bool group_stays(const float* scores, int groups, int
     return better < top;
 }
 
+// The float of an ordered integer above kMasked; NaN beyond +inf.
+__device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); }
+
 // A candidate as 64 bits that order first by rank, then by the lower index.
 __device__ __forceinline__ uint64_t candidate(uint32_t rank, int j) { return (uint64_t)rank << 32 | (uint32_t)~j; }
 __device__ __forceinline__ int candidate_index(uint64_t c) { return (int)~(uint32_t)c; }
@@ -193,12 +196,12 @@ __device__ __forceinline__ float rough_sigmoid(float x) {
 }
 
 // LANES lanes work on a token, E entries each, the consecutive ones from l * E on, so that the order of
-// the lanes is the order of the indices. L: uint16_t (bf16) or float logits.
+// the lanes is the order of the indices. V: maxima of a lane's entries that the bound is taken from. L: uint16_t (bf16) or float logits.
 //
 // The ranks of a sigmoid are first computed roughly, with a margin, at a third of the instructions;
 // what is near enough to matter is computed exactly: the candidates, and all entries where two groups
 // are too close to call.
-template <int LANES, int E, bool SOFTMAX, typename L>
+template <int LANES, int E, int V, bool SOFTMAX, typename L>
 __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArgs a) {
     constexpr int TEAMS = kWarpThreads / LANES, CANDS = 2 * LANES;
     extern __shared__ float staged[];  // groups that are no whole lanes: every team's group values [n] and scores [n_groups]
@@ -354,8 +357,7 @@ __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArg
         }
     }
 
-    // the entries that reach the k-th largest of the maxima of the lanes' entries (half a warp: of both halves of them)
-    constexpr int V = 32 / LANES;
+    // the entries that reach the k-th largest of the maxima of the lanes' entries (V 2: of both halves of them)
     float best[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -484,10 +486,11 @@ __device__ __forceinline__ float block_reduce(float x, bool sum, float* tmp, int
     return r;
 }
 
-template <int NT, typename L>
+// PLAIN: a softmax without bias and groups, whose ranks are the logits.
+template <int NT, bool PLAIN, typename L>
 __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(const RouteArgs a, int staged) {
     constexpr int WARPS = NT / 32;
-    extern __shared__ __align__(16) uint32_t keys[];  // [n] when staged
+    extern __shared__ __align__(16) float ranks[];  // [n] when staged
     __shared__ int hist[kBins];
     __shared__ uint64_t cand[kCandidates];
     __shared__ float scores[kMaxGroups];
@@ -502,55 +505,57 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t t = blockIdx.x;
     const int n = a.n, k = a.k;
-    const bool softmax = a.score == SDM_SOFTMAX, biased = a.bias != nullptr;
-    const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups;
+    const bool softmax = PLAIN || a.score == SDM_SOFTMAX, biased = !PLAIN && a.bias != nullptr;
+    const bool grouped = !PLAIN && a.n_groups > 1 && a.top_groups < a.n_groups;
     const int per = n / a.n_groups;
     const L* row = static_cast<const L*>(a.logits) + t * a.row_stride;
     const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
     constexpr int V = 16 / sizeof(L);  // logits of a 16-byte load
 
-    // f(j, x) for every logit: whole 16 bytes where the row is aligned
+    // f(j, x, count) for `count` logits x from j on, V of them where the row is aligned, all in all every one
     const auto each = [&](const auto& f) {
         int first = 0;
         if (vec) {
             first = n / V * V;
+            const auto piece = [&](int j, const uint4& v) {
+                float x[V];
+                if constexpr (sizeof(L) == 2)
+                    unpack<Bf16>(v, x);
+                else
+                    unpack<F32>(v, x);
+                f(j, x, V);
+            };
             int j = tid * V;
             for (; j + 3 * NT * V < first; j += 4 * NT * V) {  // four loads on their way together
                 uint4 v[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) v[u] = __ldg(reinterpret_cast<const uint4*>(row + j + u * NT * V));
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    float x[V];
-                    if constexpr (sizeof(L) == 2)
-                        unpack<Bf16>(v[u], x);
-                    else
-                        unpack<F32>(v[u], x);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) f(j + u * NT * V + i, x[i]);
-                }
+                for (int u = 0; u < 4; ++u) piece(j + u * NT * V, v[u]);
             }
-            for (; j < first; j += NT * V) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + j));
-                float x[V];
-                if constexpr (sizeof(L) == 2)
-                    unpack<Bf16>(v, x);
-                else
-                    unpack<F32>(v, x);
-#pragma unroll
-                for (int i = 0; i < V; ++i) f(j + i, x[i]);
-            }
+            for (; j < first; j += NT * V) piece(j, __ldg(reinterpret_cast<const uint4*>(row + j)));
         }
-        for (int j = first + tid; j < n; j += NT) f(j, to_f32(__ldg(row + j)));
+        for (int j = first + tid; j < n; j += NT) {
+            float x[V] = {to_f32(__ldg(row + j))};
+            f(j, x, 1);
+        }
     };
 
     float m = minus_inf(), total = 1.0f;
     if (softmax && (biased || !a.renorm || (grouped && a.group_top == 2))) {
-        each([&](int, float x) { m = fmaxf(m, x); });
+        each([&](int, const float* x, int count) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < count) m = fmaxf(m, x[i]);
+        });
         m = block_reduce(m, false, tmp, WARPS);
         if (biased || !a.renorm) {
             total = 0.0f;
-            each([&](int, float x) { total += exp_below(x, m); });
+            each([&](int, const float* x, int count) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i < count) total += exp_below(x[i], m);
+            });
             total = block_reduce(total, true, tmp, WARPS);
         }
     }
@@ -583,20 +588,33 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
         }
         __syncthreads();
     }
-    const auto make_key = [&](int j, float x) -> uint32_t {
+    // an entry's rank, -inf where it is masked
+    const auto final_rank = [&](int j, float x) {
+        if (PLAIN) return fmaxf(x, minus_inf());  // the number of the two
         if (grouped) {
             const int g = j / per;
-            if (!((stays[g >> 5] >> (g & 31)) & 1u)) return kMasked;
+            if (!((stays[g >> 5] >> (g & 31)) & 1u)) return minus_inf();
         }
-        return ordered(rank_of(j, x));
+        return fmaxf(rank_of(j, x), minus_inf());
     };
-    uint32_t best = 0;  // the largest rank of this thread's entries
-    each([&](int j, float x) {
-        const uint32_t key = make_key(j, x);
-        best = max(best, key);
-        if (staged) keys[j] = key;
+    float best = minus_inf();  // the largest rank of this thread's entries
+    each([&](int j, const float* x, int count) {
+        float r[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            r[i] = i < count ? final_rank(j + i, x[i]) : minus_inf();
+            best = fmaxf(best, r[i]);
+        }
+        if (!staged) return;
+        if (count == V) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(ranks + j + i) = make_float4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+        } else {
+            ranks[j] = r[0];
+        }
     });
-    const auto key_at = [&](int j) -> uint32_t { return staged ? keys[j] : make_key(j, to_f32(__ldg(row + j))); };
+    const auto rank_at = [&](int j) { return staged ? ranks[j] : final_rank(j, to_f32(__ldg(row + j))); };
+    const auto key_at = [&](int j) { return ordered(rank_at(j)); };
 
     // the bin of the need-th largest of the values counted in hist, from the top: found_bin (-1: there
     // are fewer), and found_above, those in higher bins; counts holds the warps' shares of all of them
@@ -628,32 +646,34 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
         for (int b = tid; b < kBins; b += NT) hist[b] = 0;
         __syncthreads();
     };
-    // candidates: the live entries with key >= lowest; those that fit are kept
+    // candidates: the live entries with a key from `lowest` on; those that fit are kept
     const auto collect = [&](uint32_t lowest) {
         if (tid == 0) n_cand = 0;
         __syncthreads();
-        const auto test = [&](uint32_t key, int j) {
-            if (key > kMasked && key >= lowest) {
+        // keys and ranks have the same order, and -inf is no live entry's rank
+        const float bound = fmaxf(unordered(lowest), -3.402823466e38f);
+        const auto keep = [&](float r, int j) {
+            if (r >= bound) {
                 const int c = atomicAdd(&n_cand, 1);
-                if (c < kCandidates) cand[c] = candidate(key, j);
+                if (c < kCandidates) cand[c] = candidate(ordered(r), j);
             }
         };
         if (staged) {
             const int whole = n / 4 * 4;
             for (int j = tid * 4; j < whole; j += NT * 4) {
-                const uint4 v = *reinterpret_cast<const uint4*>(keys + j);
-                test(v.x, j), test(v.y, j + 1), test(v.z, j + 2), test(v.w, j + 3);
+                const float4 v = *reinterpret_cast<const float4*>(ranks + j);
+                if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= bound) keep(v.x, j), keep(v.y, j + 1), keep(v.z, j + 2), keep(v.w, j + 3);
             }
-            for (int j = whole + tid; j < n; j += NT) test(keys[j], j);
+            for (int j = whole + tid; j < n; j += NT) keep(ranks[j], j);
         } else {
-            for (int j = tid; j < n; j += NT) test(key_at(j), j);
+            for (int j = tid; j < n; j += NT) keep(rank_at(j), j);
         }
         __syncthreads();
     };
 
     // a lower bound by the threads' maxima
     clear_bins();
-    if (best > kMasked) atomicAdd(&hist[best >> 21], 1);
+    if (best > minus_inf()) atomicAdd(&hist[ordered(best) >> 21], 1);
     __syncthreads();
     find_bin(k);
     bool done = false, few = false, ties = false;
@@ -849,43 +869,60 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel
 }
 
 template <typename L, bool SOFTMAX>
-const void* warp_kernel(int n, bool half) {
-    if (half) return n <= 128 ? (const void*)route_warp_kernel<16, 8, SOFTMAX, L> : (const void*)route_warp_kernel<16, 16, SOFTMAX, L>;
-    return n <= 256   ? (const void*)route_warp_kernel<32, 8, SOFTMAX, L>
-           : n <= 512 ? (const void*)route_warp_kernel<32, 16, SOFTMAX, L>
-                      : (const void*)route_warp_kernel<32, 32, SOFTMAX, L>;
+const void* warp_kernel(int lanes, int e, int v) {
+    if (lanes == 16) return e == 8 ? (const void*)route_warp_kernel<16, 8, 2, SOFTMAX, L> : (const void*)route_warp_kernel<16, 16, 2, SOFTMAX, L>;
+    if (v == 1)
+        return e == 8    ? (const void*)route_warp_kernel<32, 8, 1, SOFTMAX, L>
+               : e == 16 ? (const void*)route_warp_kernel<32, 16, 1, SOFTMAX, L>
+                         : (const void*)route_warp_kernel<32, 32, 1, SOFTMAX, L>;
+    return e == 8    ? (const void*)route_warp_kernel<32, 8, 2, SOFTMAX, L>
+           : e == 16 ? (const void*)route_warp_kernel<32, 16, 2, SOFTMAX, L>
+                     : (const void*)route_warp_kernel<32, 32, 2, SOFTMAX, L>;
 }
 
 template <typename L>
-const void* warp_kernel(int n, bool half, bool softmax) {
-    return softmax ? warp_kernel<L, true>(n, half) : warp_kernel<L, false>(n, half);
+const void* block_kernel(bool large, bool plain) {
+    if (large) return plain ? (const void*)route_block_kernel<512, true, L> : (const void*)route_block_kernel<512, false, L>;
+    return plain ? (const void*)route_block_kernel<128, true, L> : (const void*)route_block_kernel<128, false, L>;
 }
 
 }  // namespace
 
 int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     RouteArgs a = a0;
+    // The warp kernel, with as few lanes and maxima as leave twice k maxima among the entries whose groups
+    // stay: the k-th largest of them is then a close bound. Half a warp and two maxima a lane for 65536 rows
+    // of 256 with 8 of 4 groups of 32: 48 us, a whole one and one each: 62; without two k of them (one
+    // maximum each for half a warp, 8 in all) 76.
+    const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups;
+    const int live = grouped ? a.n / a.n_groups * a.top_groups : a.n;
     if (a.n <= 1024 && a.k <= 32) {
-        // half a warp for each token where the maxima of its lanes (two each) whose groups stay bound k entries well
-        const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups;
-        const int live = (grouped ? a.n / a.n_groups * a.top_groups : a.n) / (a.n <= 128 ? 4 : 8);
-        const bool half = a.n <= 256 && 2 * a.k <= live;
-        const int teams = kWarpThreads / (half ? 16 : 32);
-        const int64_t blocks = (a.tokens + teams - 1) / teams;
-        if (blocks > INT_MAX) return SDM_ECOUNT;
-        const size_t smem = grouped ? (size_t)teams * (a.n + a.n_groups) * 4 : 0;
-        void* args[] = {&a};
-        return launch_pdl_raw(a.logit_bf16 ? warp_kernel<uint16_t>(a.n, half, a.score == SDM_SOFTMAX)
-                                           : warp_kernel<float>(a.n, half, a.score == SDM_SOFTMAX),
-                              dim3((unsigned)blocks),
-                              dim3(kWarpThreads), smem, stream, args);
+        const int e32 = a.n <= 256 ? 8 : a.n <= 512 ? 16 : 32, e16 = a.n <= 128 ? 8 : 16;
+        int lanes = 0, e = 0, v = 0;
+        if (a.n <= 256 && 2 * a.k <= live / (e16 / 2))
+            lanes = 16, e = e16, v = 2;
+        else if (2 * a.k <= live / e32)
+            lanes = 32, e = e32, v = 1;
+        else if (3 * a.k <= 2 * (live / (e32 / 2)) || a.n <= 256)
+            lanes = 32, e = e32, v = 2;
+        if (lanes != 0) {
+            const int teams = kWarpThreads / lanes;
+            const int64_t blocks = (a.tokens + teams - 1) / teams;
+            if (blocks > INT_MAX) return SDM_ECOUNT;
+            const size_t smem = grouped ? (size_t)teams * (a.n + a.n_groups) * 4 : 0;
+            const bool softmax = a.score == SDM_SOFTMAX;
+            const void* fn = a.logit_bf16 ? (softmax ? warp_kernel<uint16_t, true>(lanes, e, v) : warp_kernel<uint16_t, false>(lanes, e, v))
+                                          : (softmax ? warp_kernel<float, true>(lanes, e, v) : warp_kernel<float, false>(lanes, e, v));
+            void* args[] = {&a};
+            return launch_pdl_raw(fn, dim3((unsigned)blocks), dim3(kWarpThreads), smem, stream, args);
+        }
     }
     if (a.tokens > INT_MAX) return SDM_ECOUNT;
     int staged = (size_t)a.n * 4 <= kStagedBytes ? 1 : 0;
     const size_t smem = staged ? (size_t)a.n * 4 : 0;
     const bool large = a.n > 4096;
-    const void* fn = a.logit_bf16 ? (large ? (const void*)route_block_kernel<512, uint16_t> : (const void*)route_block_kernel<128, uint16_t>)
-                                  : (large ? (const void*)route_block_kernel<512, float> : (const void*)route_block_kernel<128, float>);
+    const bool plain = a.score == SDM_SOFTMAX && a.bias == nullptr && !grouped;
+    const void* fn = a.logit_bf16 ? block_kernel<uint16_t>(large, plain) : block_kernel<float>(large, plain);
     // the limit without a request counts the kernel's static arrays (16 KB) too
     const int rc = allow_smem(fn, smem > 32 * 1024 ? std::max(smem, (size_t)48 * 1024 + 16) : smem);
     if (rc != 0) return rc;
