@@ -488,17 +488,19 @@ __device__ __forceinline__ float block_reduce(float x, bool sum, float* tmp, int
 
 // PLAIN: a softmax without bias and groups, whose ranks are the logits.
 template <int NT, bool PLAIN, typename L>
-__global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(const RouteArgs a, int staged) {
+__global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_block_kernel(const RouteArgs a, int staged) {
     constexpr int WARPS = NT / 32;
     extern __shared__ __align__(16) float ranks[];  // [n] when staged
-    __shared__ int hist[kBins];
-    __shared__ uint64_t cand[kCandidates];
+    __shared__ __align__(16) int hist[kBins];
+    // the histogram has been read when candidates are collected and chosen
+    uint64_t* cand = reinterpret_cast<uint64_t*>(hist);                     // [kCandidates]
+    int* sel_j = hist + 2 * kCandidates;                                    // [kMaxK]
+    float* sel_s = reinterpret_cast<float*>(hist + 2 * kCandidates + kMaxK);  // [kMaxK]
+    static_assert(2 * kCandidates + 2 * kMaxK <= kBins, "they fit the histogram");
     __shared__ float scores[kMaxGroups];
     __shared__ uint32_t stays[kMaxGroups / 32];
-    __shared__ float tmp[WARPS];
+    __shared__ float tmp[2 * WARPS];
     __shared__ int counts[WARPS];
-    __shared__ int sel_j[kMaxK];
-    __shared__ float sel_s[kMaxK];
     __shared__ int found_bin, found_above, n_cand;
     grid_dependency_wait();
     grid_launch_dependents();
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
     };
 
     float m = minus_inf(), total = 1.0f;
-    if (softmax && (biased || !a.renorm || (grouped && a.group_top == 2))) {
+    if (!PLAIN && softmax && (biased || !a.renorm || (grouped && a.group_top == 2))) {
         each([&](int, const float* x, int count) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -588,23 +590,45 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
         }
         __syncthreads();
     }
-    // an entry's rank, -inf where it is masked
-    const auto final_rank = [&](int j, float x) {
-        if (PLAIN) return fmaxf(x, minus_inf());  // the number of the two
-        if (grouped) {
-            const int g = j / per;
-            if (!((stays[g >> 5] >> (g & 31)) & 1u)) return minus_inf();
+    const auto stays_at = [&](int j) {
+        const int g = j / per;
+        return ((stays[g >> 5] >> (g & 31)) & 1u) != 0;
+    };
+    // the ranks of V entries from j on, or of one, -inf where they are masked
+    const auto final_ranks = [&](int j, const float* x, int count, float* r) {
+        if (PLAIN || softmax) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) r[i] = !biased ? x[i] : i < count ? rank_of(j + i, x[i]) : 0.0f;
+        } else {
+            sigmoids<V>(x, r);
+#pragma unroll
+            for (int i = 0; i < V; ++i) r[i] = masked(x[i]) ? minus_inf() : r[i];
+            if (biased) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i < count) r[i] += __ldg(a.bias + j + i);
+            }
         }
-        return fmaxf(rank_of(j, x), minus_inf());
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = i < count ? fmaxf(r[i], minus_inf()) : minus_inf();  // the number of the two
+        if (grouped) {
+            if (per % V == 0) {  // a group, or none, for all of them
+                const bool on = stays_at(j);
+#pragma unroll
+                for (int i = 0; i < V; ++i) r[i] = on ? r[i] : minus_inf();
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i < count && !stays_at(j + i)) r[i] = minus_inf();
+            }
+        }
     };
     float best = minus_inf();  // the largest rank of this thread's entries
     each([&](int j, const float* x, int count) {
         float r[V];
+        final_ranks(j, x, count, r);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            r[i] = i < count ? final_rank(j + i, x[i]) : minus_inf();
-            best = fmaxf(best, r[i]);
-        }
+        for (int i = 0; i < V; ++i) best = fmaxf(best, r[i]);
         if (!staged) return;
         if (count == V) {
 #pragma unroll
@@ -613,7 +637,18 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
             ranks[j] = r[0];
         }
     });
-    const auto rank_at = [&](int j) { return staged ? ranks[j] : final_rank(j, to_f32(__ldg(row + j))); };
+    const auto rank_at = [&](int j) {
+        if (staged) return ranks[j];
+        float x[V] = {to_f32(__ldg(row + j))}, r[V];
+        final_ranks(j, x, 1, r);
+        return r[0];
+    };
+    if (PLAIN && !a.renorm) {  // the ranks are the logits
+        m = block_reduce(best, false, tmp, WARPS);
+        total = 0.0f;
+        for (int j = tid; j < n; j += NT) total += exp_below(rank_at(j), m);
+        total = block_reduce(total, true, tmp, WARPS);
+    }
     const auto key_at = [&](int j) { return ordered(rank_at(j)); };
 
     // the bin of the need-th largest of the values counted in hist, from the top: found_bin (-1: there
@@ -671,16 +706,34 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
         __syncthreads();
     };
 
-    // a lower bound by the threads' maxima
+    // a lower bound by the threads' maxima: the bin of the k-th largest of them among bins of equal width
+    // from the least to the greatest
+    float low = best > minus_inf() ? best : 3.402823466e38f, high = best;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        low = fminf(low, __shfl_xor_sync(kAll, low, o));
+        high = fmaxf(high, __shfl_xor_sync(kAll, high, o));
+    }
+    if (lane == 0) {
+        tmp[warp] = low;
+        tmp[WARPS + warp] = high;
+    }
     clear_bins();
-    if (best > minus_inf()) atomicAdd(&hist[ordered(best) >> 21], 1);
+    for (int i = 0; i < WARPS; ++i) {
+        low = fminf(low, tmp[i]);
+        high = fmaxf(high, tmp[WARPS + i]);
+    }
+    const float width = (high - low) * (1.0f / kBins);
+    const bool spread = width > 0x1p-100f && width < 0x1p100f;
+    if (best > minus_inf()) atomicAdd(&hist[spread ? min(kBins - 1, (int)__fdividef(best - low, width)) : 0], 1);
     __syncthreads();
     find_bin(k);
     bool done = false, few = false, ties = false;
     uint32_t lowest = 0;
     int C = 0;
     if (found_bin >= 0) {
-        collect((uint32_t)found_bin << 21);
+        // one bin lower, for the roundings
+        collect(ordered(spread && found_bin > 0 ? fmaf((float)(found_bin - 1), width, low) : low));
         C = n_cand;
         done = C <= kCandidates;
     }
@@ -724,17 +777,19 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
         const int c = c0 + tid / 4;
         const uint64_t mine = c < C ? cand[c] : 0;
         int better = 0;
+#pragma unroll 4
         for (int o = tid % 4; o < C; o += 4) better += cand[o] > mine;
         better += __shfl_xor_sync(kAll, better, 1);
         better += __shfl_xor_sync(kAll, better, 2);
-        if (c < C && better < k && tid % 4 == 0) sel_j[better] = candidate_index(mine);
+        if (c < C && better < k && tid % 4 == 0) {
+            sel_j[better] = candidate_index(mine);
+            sel_s[better] = PLAIN ? unordered((uint32_t)(mine >> 32)) : to_f32(__ldg(row + candidate_index(mine)));
+        }
     }
     __syncthreads();
-    if (softmax && !biased && a.renorm && C > 0) m = to_f32(__ldg(row + sel_j[0]));  // any reference does: it cancels
-    for (int i = tid; i < min(C, k); i += NT) {
-        const float x = to_f32(__ldg(row + sel_j[i]));
-        sel_s[i] = softmax ? exp_below(x, m) : sigmoid(x);
-    }
+    if (softmax && !biased && a.renorm && C > 0) m = sel_s[0];  // any reference does: it cancels
+    __syncthreads();
+    for (int i = tid; i < min(C, k); i += NT) sel_s[i] = softmax ? exp_below(sel_s[i], m) : sigmoid(sel_s[i]);
     // fill up, in index order, with entries of the shared last rank, or with masked ones of weight 0
     if (few || ties) {
         const uint32_t want = few ? kMasked : lowest;
@@ -775,14 +830,13 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 4) route_block_kernel(cons
 // ---------------------------------------------------------------- the gradient
 
 // A team of TEAM threads (a warp, or a block) for each token. Only a softmax that is not
-// renormalised has gradients outside the chosen entries; all others just get zeros there.
-template <int TEAM, typename L>
+// renormalised has gradients outside the chosen entries: its row is read once, E logits a thread, and
+// its exponentials stay in registers until the gradients are written (E 0: rows too long for that are
+// read three times). All others get zeros there. The chosen entries are written over that.
+template <int TEAM, int E, typename L>
 __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel(const RouteArgs a) {
-    constexpr int NT = TEAM == 32 ? 128 : TEAM, TEAMS = NT / TEAM, WARPS = TEAM / 32;
-    __shared__ float u_of[TEAMS][kMaxK];  // gradients of the chosen scores
-    __shared__ float s_of[TEAMS][kMaxK];
-    __shared__ int j_of[TEAMS][kMaxK];
-    __shared__ float tmp[NT / 32];
+    constexpr int NT = TEAM == 32 ? 128 : TEAM, TEAMS = NT / TEAM, WARPS = TEAM / 32, V = 16 / sizeof(L);
+    __shared__ float largest[NT / 32], sums[NT / 32];
     grid_dependency_wait();
     grid_launch_dependents();
     const int team = threadIdx.x / TEAM, tid = threadIdx.x % TEAM, lane = threadIdx.x & 31;
@@ -791,9 +845,10 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel
     const int n = a.n, k = a.k;
     const L* row = static_cast<const L*>(a.logits) + t * a.row_stride;
     L* out = static_cast<L*>(a.dlogits) + t * a.dlogits_stride;
-    float *u = u_of[team], *s = s_of[team];
-    int* at = j_of[team];
     const bool softmax = a.score == SDM_SOFTMAX, dense = softmax && !a.renorm;
+    // thread tid has logits from (p * TEAM + tid) * V on, V of them, p = 0, 1, ...; or, in rows that are not
+    // 16-byte aligned, logits p * TEAM + tid
+    const bool vec = ((reinterpret_cast<uintptr_t>(row) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0 && n % V == 0;
 
     const auto sync = [] {
         if constexpr (TEAM == 32)
@@ -801,71 +856,179 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel
         else
             __syncthreads();
     };
-    const auto team_sum = [&](float v) {
-        if constexpr (TEAM == 32)
-            return warp_sum(v);
-        else
-            return block_reduce(v, true, tmp, WARPS);
+    // the largest value m of the team's threads, with the sum of their `own` sums of exp(x - their m)
+    const auto join = [&](float& m, float& own) {
+        const float mine = m;
+        m = warp_max(m);
+        own = warp_sum(mine == m ? own : own * exp_below(mine, m));
+        if constexpr (TEAM > 32) {
+            if (lane == 0) {
+                largest[tid >> 5] = m;
+                sums[tid >> 5] = own;
+            }
+            __syncthreads();
+            own = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) m = fmaxf(m, largest[w]);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) own += sums[w] * exp_below(largest[w], m);
+        }
     };
-    const auto team_max = [&](float v) {
-        if constexpr (TEAM == 32)
-            return warp_max(v);
-        else
-            return block_reduce(v, false, tmp, WARPS);
-    };
-
-    float m = minus_inf(), total = 1.0f;
-    if (dense) {
-        for (int j = tid; j < n; j += TEAM) m = fmaxf(m, to_f32(__ldg(row + j)));
-        m = team_max(m);
-        total = 0.0f;
-        for (int j = tid; j < n; j += TEAM) total += exp_below(to_f32(__ldg(row + j)), m);
-        total = team_sum(total);
-    }
-    for (int i = tid; i < k; i += TEAM) {
+    // chosen entry i: its column (-1: outside the row), its logit and the gradient of its weight
+    const auto chosen = [&](int i, float& x, float& dw) {
         const int64_t e = t * k + i;
         const int64_t j = (a.idx64 ? __ldg(static_cast<const int64_t*>(a.idx) + e) : __ldg(static_cast<const int32_t*>(a.idx) + e)) -
                           (a.base == nullptr ? 0 : a.idx64 ? __ldg(static_cast<const int64_t*>(a.base) + t) : __ldg(static_cast<const int32_t*>(a.base) + t));
         const bool in = j >= 0 && j < n;
-        if (!in) atomicOr(&g_route_status, SDM_DEV_BAD_INDEX);
-        at[i] = in ? (int)j : -1;
-        s[i] = in ? to_f32(__ldg(row + j)) : minus_inf();
-        u[i] = __ldg(a.dw + e) * a.scale;
-    }
-    if (softmax && a.renorm) {
-        for (int i = tid; i < k; i += TEAM) m = fmaxf(m, s[i]);  // each thread's own entries
-        m = team_max(m);
-    }
-    float own = 0.0f;
-    for (int i = tid; i < k; i += TEAM) {
-        s[i] = !softmax ? sigmoid(s[i]) : dense ? (total > 0.0f ? __fdiv_rn(exp_below(s[i], m), total) : 0.0f) : exp_below(s[i], m);
-        own += s[i];
-    }
-    // u: the gradients of the scores (of exp(x - m) when a softmax is renormalised, which is as good:
-    // the factor between them cancels in u * s)
-    if (a.renorm) {
-        const float all = team_sum(own);
-        float dot = 0.0f;
-        for (int i = tid; i < k; i += TEAM) dot += all > 0.0f ? u[i] * __fdiv_rn(s[i], all) : 0.0f;
-        dot = team_sum(dot);
-        for (int i = tid; i < k; i += TEAM) u[i] = all > 0.0f ? __fdiv_rn(u[i] - dot, all) : 0.0f;
-    }
-    float mean = 0.0f;
+        x = in ? to_f32(__ldg(row + j)) : minus_inf();
+        dw = __ldg(a.dw + e) * a.scale;
+        return in ? (int)j : -1;
+    };
+    const auto put16 = [&](int j, const float* d) {  // V gradients from j on
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(L) == 2) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(d[2 * i], d[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+                w[i] = __float_as_uint(d[i]);
+            }
+        }
+        *reinterpret_cast<uint4*>(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
+    };
+
+    float m = minus_inf(), total = 0.0f, mean = 0.0f, factor = 0.0f;
+    float x[E > 0 ? E : 1];
     if (dense) {
-        for (int i = tid; i < k; i += TEAM) mean += u[i] * s[i];
-        mean = team_sum(mean);
+        float own = 0.0f, rescale = 1.0f;
+        if constexpr (E > 0) {
+            if (vec) {
+#pragma unroll
+                for (int i = 0; i < E; i += V) {
+                    const int j = (i / V * TEAM + tid) * V;
+                    if (j < n) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + j));
+                        if constexpr (sizeof(L) == 2)
+                            unpack<Bf16>(v, x + i);
+                        else
+                            unpack<F32>(v, x + i);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < V; ++c) x[i + c] = minus_inf();
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i) x[i] = i * TEAM + tid < n ? to_f32(__ldg(row + i * TEAM + tid)) : minus_inf();
+            }
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                x[i] = fmaxf(x[i], minus_inf());  // NaN is masked
+                m = fmaxf(m, x[i]);
+            }
+            const bool plain = fabsf(m) <= 3.402823466e38f;  // neither +inf nor masked throughout
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                x[i] = plain ? expf(x[i] - m) : exp_below(x[i], m);
+                own += x[i];
+            }
+            const float mine = m;
+            join(m, own);
+            rescale = exp_below(mine, m);  // x holds exp(logit - mine)
+        } else {
+            for (int j = tid; j < n; j += TEAM) m = fmaxf(m, to_f32(__ldg(row + j)));
+            for (int j = tid; j < n; j += TEAM) own += exp_below(to_f32(__ldg(row + j)), m);
+            join(m, own);
+        }
+        total = own;
+        // every warp for itself: a barrier would cost more
+        for (int i = lane; i < k; i += 32) {
+            float y, dw;
+            chosen(i, y, dw);
+            mean += dw * exp_below(y, m);
+        }
+        mean = total > 0.0f ? __fdiv_rn(warp_sum(mean), total) : 0.0f;
+        factor = total > 0.0f ? __fdiv_rn(-mean, total) : 0.0f;
+        if constexpr (E > 0) {
+            rescale *= factor;
+#pragma unroll
+            for (int i = 0; i < E; ++i) x[i] *= rescale;
+            if (vec) {
+#pragma unroll
+                for (int i = 0; i < E; i += V) {
+                    const int j = (i / V * TEAM + tid) * V;
+                    if (j < n) put16(j, x + i);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (i * TEAM + tid < n) out[i * TEAM + tid] = from_f32<L>(x[i]);
+            }
+        } else {
+            for (int j = tid; j < n; j += TEAM) out[j] = from_f32<L>(factor * exp_below(to_f32(__ldg(row + j)), m));
+        }
+    } else if (vec) {
+        for (int j = tid * V; j < n; j += TEAM * V) *reinterpret_cast<uint4*>(out + j) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+        for (int j = tid; j < n; j += TEAM) out[j] = L(0);
     }
-    for (int j = tid; j < n; j += TEAM) {
-        float d = 0.0f;
-        if (dense && total > 0.0f) d = -mean * __fdiv_rn(exp_below(to_f32(__ldg(row + j)), m), total);
-        out[j] = from_f32<L>(d);
+    // the chosen entries are written again, over what is there, by the team's first warp
+    float all = 1.0f, dot = 0.0f;
+    if (a.renorm && tid < 32) {
+        // scores, or exp(x - m) for a softmax, which is as good: the factor between them cancels
+        if (softmax) {
+            for (int i = lane; i < k; i += 32) {
+                float y, dw;
+                chosen(i, y, dw);
+                m = fmaxf(m, y);
+            }
+            m = warp_max(m);
+        }
+        all = 0.0f;
+        for (int i = lane; i < k; i += 32) {
+            float y, dw;
+            chosen(i, y, dw);
+            const float s = softmax ? exp_below(y, m) : sigmoid(y);
+            all += s;
+            dot += dw * s;
+        }
+        all = warp_sum(all);
+        dot = all > 0.0f ? __fdiv_rn(warp_sum(dot), all) : 0.0f;
     }
-    sync();  // the chosen entries are written again, over what is there
-    for (int i = tid; i < k; i += TEAM) {
-        if (at[i] < 0) continue;
-        out[at[i]] = from_f32<L>(!softmax ? u[i] * s[i] * (1.0f - s[i]) : dense ? s[i] * (u[i] - mean) : s[i] * u[i]);
+    sync();
+    if (tid >= 32) return;
+    for (int i = lane; i < k; i += 32) {
+        float y, dw;
+        const int j = chosen(i, y, dw);
+        if (j < 0) {
+            atomicOr(&g_route_status, SDM_DEV_BAD_INDEX);
+            continue;
+        }
+        float s = softmax ? exp_below(y, m) : sigmoid(y);
+        if (dense) s = total > 0.0f ? __fdiv_rn(s, total) : 0.0f;
+        const float u = !a.renorm ? dw : all > 0.0f ? __fdiv_rn(dw - dot, all) : 0.0f;
+        out[j] = from_f32<L>(!softmax ? u * s * (1.0f - s) : dense ? s * (u - mean) : s * u);
     }
-    (void)lane;
+}
+
+struct Team {
+    const void* fn;
+    int threads, teams;
+};
+
+// Teams with 8 to 32 logits a thread where the row is kept; without a row to keep, of 256 threads.
+template <typename L>
+Team backward_kernel(int n, bool dense) {
+    if (n <= 256) return {(const void*)route_backward_kernel<32, 8, L>, 128, 4};
+    if (n <= 1024) return {(const void*)route_backward_kernel<32, 32, L>, 128, 4};
+    if (!dense) return {(const void*)route_backward_kernel<256, 0, L>, 256, 1};
+    if (n <= 2048) return {(const void*)route_backward_kernel<256, 8, L>, 256, 1};
+    if (n <= 4096) return {(const void*)route_backward_kernel<256, 16, L>, 256, 1};
+    if (n <= 6144) return {(const void*)route_backward_kernel<256, 24, L>, 256, 1};
+    if (n <= 8192) return {(const void*)route_backward_kernel<256, 32, L>, 256, 1};
+    if (n <= 16384) return {(const void*)route_backward_kernel<512, 32, L>, 512, 1};
+    return {(const void*)route_backward_kernel<512, 0, L>, 512, 1};
 }
 
 template <typename L, bool SOFTMAX>
@@ -880,10 +1043,16 @@ const void* warp_kernel(int lanes, int e, int v) {
                      : (const void*)route_warp_kernel<32, 32, 2, SOFTMAX, L>;
 }
 
+template <typename L, bool PLAIN>
+const void* block_kernel(int threads) {
+    return threads == 512   ? (const void*)route_block_kernel<512, PLAIN, L>
+           : threads == 256 ? (const void*)route_block_kernel<256, PLAIN, L>
+                            : (const void*)route_block_kernel<128, PLAIN, L>;
+}
+
 template <typename L>
-const void* block_kernel(bool large, bool plain) {
-    if (large) return plain ? (const void*)route_block_kernel<512, true, L> : (const void*)route_block_kernel<512, false, L>;
-    return plain ? (const void*)route_block_kernel<128, true, L> : (const void*)route_block_kernel<128, false, L>;
+const void* block_kernel(int threads, bool plain) {
+    return plain ? block_kernel<L, true>(threads) : block_kernel<L, false>(threads);
 }
 
 }  // namespace
@@ -920,25 +1089,26 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     if (a.tokens > INT_MAX) return SDM_ECOUNT;
     int staged = (size_t)a.n * 4 <= kStagedBytes ? 1 : 0;
     const size_t smem = staged ? (size_t)a.n * 4 : 0;
-    const bool large = a.n > 4096;
+    // threads for 32 to 64 ranks each; blocks of 256 with 64 KB of ranks fit three times on an SM, so that
+    // one loads its row while others choose (1024 rows of 16384: two blocks of 512 threads 43 us)
+    const int threads = a.n > 16384 ? 512 : a.n > 4096 ? 256 : 128;
     const bool plain = a.score == SDM_SOFTMAX && a.bias == nullptr && !grouped;
-    const void* fn = a.logit_bf16 ? block_kernel<uint16_t>(large, plain) : block_kernel<float>(large, plain);
-    // the limit without a request counts the kernel's static arrays (16 KB) too
+    const void* fn = a.logit_bf16 ? block_kernel<uint16_t>(threads, plain) : block_kernel<float>(threads, plain);
+    // the limit without a request counts the kernel's static arrays (10 KB) too
     const int rc = allow_smem(fn, smem > 32 * 1024 ? std::max(smem, (size_t)48 * 1024 + 16) : smem);
     if (rc != 0) return rc;
     void* args[] = {&a, &staged};
-    return launch_pdl_raw(fn, dim3((unsigned)a.tokens), dim3(large ? 512 : 128), smem, stream, args);
+    return launch_pdl_raw(fn, dim3((unsigned)a.tokens), dim3(threads), smem, stream, args);
 }
 
 int launch_route_backward(const RouteArgs& a0, cudaStream_t stream) {
     RouteArgs a = a0;
-    const bool warp = a.n <= 1024;
-    const int64_t blocks = warp ? (a.tokens + 3) / 4 : a.tokens;
+    const bool dense = a.score == SDM_SOFTMAX && !a.renorm;
+    const Team team = a.logit_bf16 ? backward_kernel<uint16_t>(a.n, dense) : backward_kernel<float>(a.n, dense);
+    const int64_t blocks = (a.tokens + team.teams - 1) / team.teams;
     if (blocks > INT_MAX) return SDM_ECOUNT;
-    const void* fn = warp ? (a.logit_bf16 ? (const void*)route_backward_kernel<32, uint16_t> : (const void*)route_backward_kernel<32, float>)
-                          : (a.logit_bf16 ? (const void*)route_backward_kernel<256, uint16_t> : (const void*)route_backward_kernel<256, float>);
     void* args[] = {&a};
-    return launch_pdl_raw(fn, dim3((unsigned)blocks), dim3(warp ? 128 : 256), 0, stream, args);
+    return launch_pdl_raw(team.fn, dim3((unsigned)blocks), dim3(team.threads), 0, stream, args);
 }
 
 int route_status(unsigned int* word, bool clear) {
