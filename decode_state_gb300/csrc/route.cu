@@ -20,7 +20,7 @@
 // narrows the k-th rank down by histograms of its leading 11, then 11, then 10 bits.
 #include <algorithm>
 #include <climits>
-#include <cmath>
+#include <type_traits>
 
 #include "quant_device.cuh"
 #include "sdm_internal.h"
@@ -490,7 +490,7 @@ __device__ __forceinline__ float block_reduce(float x, bool sum, float* tmp, int
 template <int NT, bool PLAIN, typename L>
 __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_block_kernel(const RouteArgs a, int staged) {
     constexpr int WARPS = NT / 32;
-    extern __shared__ __align__(16) float ranks[];  // [n] when staged
+    extern __shared__ __align__(16) float staging[];  // [n + 4] when staged
     __shared__ __align__(16) int hist[kBins];
     // the histogram has been read when candidates are collected and chosen
     uint64_t* cand = reinterpret_cast<uint64_t*>(hist);                     // [kCandidates]
@@ -511,33 +511,35 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
     const bool grouped = !PLAIN && a.n_groups > 1 && a.top_groups < a.n_groups;
     const int per = n / a.n_groups;
     const L* row = static_cast<const L*>(a.logits) + t * a.row_stride;
-    const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
     constexpr int V = 16 / sizeof(L);  // logits of a 16-byte load
+    // the row's first logit at a 16-byte boundary; ranks + j is at one where row + j is
+    const int head = min(n, (int)((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16 / sizeof(L)));
+    float* ranks = staging + (4 - head % 4) % 4;
 
-    // f(j, x, count) for `count` logits x from j on, V of them where the row is aligned, all in all every one
+    // f(j, x, count) for `count` logits x from j on, V or one, all in all every one
     const auto each = [&](const auto& f) {
-        int first = 0;
-        if (vec) {
-            first = n / V * V;
-            const auto piece = [&](int j, const uint4& v) {
-                float x[V];
-                if constexpr (sizeof(L) == 2)
-                    unpack<Bf16>(v, x);
-                else
-                    unpack<F32>(v, x);
-                f(j, x, V);
-            };
-            int j = tid * V;
-            for (; j + 3 * NT * V < first; j += 4 * NT * V) {  // four loads on their way together
-                uint4 v[4];
+        const auto piece = [&](int j, const uint4& v) {
+            float x[V];
+            if constexpr (sizeof(L) == 2)
+                unpack<Bf16>(v, x);
+            else
+                unpack<F32>(v, x);
+            f(j, x, V);
+        };
+        const int end = head + (n - head) / V * V;
+        int j = head + tid * V;
+        for (; j + 3 * NT * V < end; j += 4 * NT * V) {  // four loads on their way together
+            uint4 v[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) v[u] = __ldg(reinterpret_cast<const uint4*>(row + j + u * NT * V));
+            for (int u = 0; u < 4; ++u) v[u] = __ldg(reinterpret_cast<const uint4*>(row + j + u * NT * V));
 #pragma unroll
-                for (int u = 0; u < 4; ++u) piece(j + u * NT * V, v[u]);
-            }
-            for (; j < first; j += NT * V) piece(j, __ldg(reinterpret_cast<const uint4*>(row + j)));
+            for (int u = 0; u < 4; ++u) piece(j + u * NT * V, v[u]);
         }
-        for (int j = first + tid; j < n; j += NT) {
+        for (; j < end; j += NT * V) piece(j, __ldg(reinterpret_cast<const uint4*>(row + j)));
+        // the few before the first boundary and behind the last one
+        const int rest = head + n - end;
+        if (tid < rest) {
+            j = tid < head ? tid : end + tid - head;
             float x[V] = {to_f32(__ldg(row + j))};
             f(j, x, 1);
         }
@@ -553,11 +555,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
         m = block_reduce(m, false, tmp, WARPS);
         if (biased || !a.renorm) {
             total = 0.0f;
-            each([&](int, const float* x, int count) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (i < count) total += exp_below(x[i], m);
-            });
+            for (int j = tid; j < n; j += NT) total += exp_below(to_f32(__ldg(row + j)), m);  // in one order, wherever the row starts
             total = block_reduce(total, true, tmp, WARPS);
         }
     }
@@ -612,7 +610,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
 #pragma unroll
         for (int i = 0; i < V; ++i) r[i] = i < count ? fmaxf(r[i], minus_inf()) : minus_inf();  // the number of the two
         if (grouped) {
-            if (per % V == 0) {  // a group, or none, for all of them
+            if (per % V == 0 && head == 0) {  // a group, or none, for all of them
                 const bool on = stays_at(j);
 #pragma unroll
                 for (int i = 0; i < V; ++i) r[i] = on ? r[i] : minus_inf();
@@ -653,11 +651,11 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
 
     // the bin of the need-th largest of the values counted in hist, from the top: found_bin (-1: there
     // are fewer), and found_above, those in higher bins; counts holds the warps' shares of all of them
-    const auto find_bin = [&](int need) {
-        constexpr int PER = kBins / NT;  // thread i owns the PER bins from i * PER on, counted from the top
+    const auto find_bin = [&](int need, auto bins) {
+        constexpr int BINS = decltype(bins)::value, PER = BINS / NT;  // thread i owns the PER bins from i * PER on, counted from the top
         int own = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) own += hist[kBins - 1 - (tid * PER + i)];
+        for (int i = 0; i < PER; ++i) own += hist[BINS - 1 - (tid * PER + i)];
         int all;
         int before = lanes_before<32>(own, &all);
         if (lane == 31) counts[warp] = all;
@@ -665,22 +663,23 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
         __syncthreads();
         for (int i = 0; i < warp; ++i) before += counts[i];
         if (before < need && before + own >= need) {
+#pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int b = kBins - 1 - (tid * PER + i), c = hist[b];
-                if (before + c >= need) {
+                const int b = BINS - 1 - (tid * PER + i), c = hist[b];
+                if (before < need && before + c >= need) {
                     found_bin = b;
                     found_above = before;
-                    break;
                 }
                 before += c;
             }
         }
         __syncthreads();
     };
-    const auto clear_bins = [&]() {
-        for (int b = tid; b < kBins; b += NT) hist[b] = 0;
+    const auto clear_bins = [&](int bins) {
+        for (int b = tid; b < bins; b += NT) hist[b] = 0;
         __syncthreads();
     };
+    constexpr int kFew = 2 * NT;  // bins for the threads' maxima
     // candidates: the live entries with a key from `lowest` on; those that fit are kept
     const auto collect = [&](uint32_t lowest) {
         if (tid == 0) n_cand = 0;
@@ -694,12 +693,16 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
             }
         };
         if (staged) {
-            const int whole = n / 4 * 4;
-            for (int j = tid * 4; j < whole; j += NT * 4) {
+            const int first = head % 4, whole = first + (n - first) / 4 * 4;
+            for (int j = first + tid * 4; j < whole; j += NT * 4) {
                 const float4 v = *reinterpret_cast<const float4*>(ranks + j);
                 if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= bound) keep(v.x, j), keep(v.y, j + 1), keep(v.z, j + 2), keep(v.w, j + 3);
             }
-            for (int j = whole + tid; j < n; j += NT) keep(ranks[j], j);
+            const int rest = first + n - whole;
+            if (tid < rest) {
+                const int j = tid < first ? tid : whole + tid - first;
+                keep(ranks[j], j);
+            }
         } else {
             for (int j = tid; j < n; j += NT) keep(rank_at(j), j);
         }
@@ -718,16 +721,16 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
         tmp[warp] = low;
         tmp[WARPS + warp] = high;
     }
-    clear_bins();
+    clear_bins(kFew);
     for (int i = 0; i < WARPS; ++i) {
         low = fminf(low, tmp[i]);
         high = fmaxf(high, tmp[WARPS + i]);
     }
-    const float width = (high - low) * (1.0f / kBins);
+    const float width = (high - low) * (1.0f / kFew);
     const bool spread = width > 0x1p-100f && width < 0x1p100f;
-    if (best > minus_inf()) atomicAdd(&hist[spread ? min(kBins - 1, (int)__fdividef(best - low, width)) : 0], 1);
+    if (best > minus_inf()) atomicAdd(&hist[spread ? min(kFew - 1, (int)__fdividef(best - low, width)) : 0], 1);
     __syncthreads();
-    find_bin(k);
+    find_bin(k, std::integral_constant<int, kFew>{});
     bool done = false, few = false, ties = false;
     uint32_t lowest = 0;
     int C = 0;
@@ -746,14 +749,14 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
         for (int level = 0; level < 3; ++level) {
             const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
             __syncthreads();
-            clear_bins();
+            clear_bins(kBins);
             for (int j = tid; j < n; j += NT) {
                 const uint32_t key = key_at(j);
                 if (key > kMasked && (level == 0 || key >> (shift + bits) == prefix))
                     atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1);
             }
             __syncthreads();
-            find_bin(need);
+            find_bin(need, std::integral_constant<int, kBins>{});
             if (found_bin < 0) {  // level 0 only: all live entries are taken
                 few = true;
                 lowest = kMasked + 1;
@@ -835,7 +838,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
 // read three times). All others get zeros there. The chosen entries are written over that.
 template <int TEAM, int E, typename L>
 __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel(const RouteArgs a) {
-    constexpr int NT = TEAM == 32 ? 128 : TEAM, TEAMS = NT / TEAM, WARPS = TEAM / 32, V = 16 / sizeof(L);
+    constexpr int NT = TEAM == 32 ? 128 : TEAM, TEAMS = NT / TEAM, WARPS = TEAM / 32, U = 4 / sizeof(L);
     __shared__ float largest[NT / 32], sums[NT / 32];
     grid_dependency_wait();
     grid_launch_dependents();
@@ -846,9 +849,9 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel
     const L* row = static_cast<const L*>(a.logits) + t * a.row_stride;
     L* out = static_cast<L*>(a.dlogits) + t * a.dlogits_stride;
     const bool softmax = a.score == SDM_SOFTMAX, dense = softmax && !a.renorm;
-    // thread tid has logits from (p * TEAM + tid) * V on, V of them, p = 0, 1, ...; or, in rows that are not
-    // 16-byte aligned, logits p * TEAM + tid
-    const bool vec = ((reinterpret_cast<uintptr_t>(row) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0 && n % V == 0;
+    // Thread tid works on the U logits of 4 bytes from (p * TEAM + tid) * U on, p = 0, 1, ...: runs of 128
+    // bytes for a warp, and one order of the sums wherever the row starts.
+    const bool words = U == 1 || ((reinterpret_cast<uintptr_t>(row) | reinterpret_cast<uintptr_t>(out)) & 3u) == 0;
 
     const auto sync = [] {
         if constexpr (TEAM == 32)
@@ -884,18 +887,48 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel
         dw = __ldg(a.dw + e) * a.scale;
         return in ? (int)j : -1;
     };
-    const auto put16 = [&](int j, const float* d) {  // V gradients from j on
-        uint32_t w[4];
+    const auto get = [&](int j, float* x) {  // U logits from j on; masked ones behind the end
+        if (U == 2 && words && j + U <= n) {
+            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(row + j));
+            x[0] = __uint_as_float(w << 16);
+            x[U - 1] = __uint_as_float(w & 0xffff0000u);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(L) == 2) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(d[2 * i], d[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            } else {
-                w[i] = __float_as_uint(d[i]);
-            }
+            for (int c = 0; c < U; ++c) x[c] = j + c < n ? to_f32(__ldg(row + j + c)) : minus_inf();
         }
-        *reinterpret_cast<uint4*>(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    const auto put = [&](int j, const float* d) {  // U gradients from j on
+        if (U == 2 && words && j + U <= n) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(d[0], d[U - 1]);
+            *reinterpret_cast<uint32_t*>(out + j) = *reinterpret_cast<const uint32_t*>(&b);
+        } else {
+#pragma unroll
+            for (int c = 0; c < U; ++c)
+                if (j + c < n) out[j + c] = from_f32<L>(d[c]);
+        }
+    };
+
+    // every warp has the first chosen entries at hand, loaded while the row is on its way
+    constexpr int KEPT = 2;
+    int kept_j[KEPT];
+    float kept_x[KEPT], kept_dw[KEPT];
+#pragma unroll
+    for (int q = 0; q < KEPT; ++q) {
+        kept_j[q] = -1;
+        kept_x[q] = minus_inf();
+        kept_dw[q] = 0.0f;
+        if (lane + 32 * q < k && (dense || tid < 32)) kept_j[q] = chosen(lane + 32 * q, kept_x[q], kept_dw[q]);
+    }
+    // f(j, x, dw) for this lane's chosen entries
+    const auto each_chosen = [&](const auto& f) {
+#pragma unroll
+        for (int q = 0; q < KEPT; ++q)
+            if (lane + 32 * q < k) f(kept_j[q], kept_x[q], kept_dw[q]);
+        for (int i = lane + 32 * KEPT; i < k; i += 32) {
+            float y, dw;
+            const int j = chosen(i, y, dw);
+            f(j, y, dw);
+        }
     };
 
     float m = minus_inf(), total = 0.0f, mean = 0.0f, factor = 0.0f;
@@ -903,35 +936,26 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel
     if (dense) {
         float own = 0.0f, rescale = 1.0f;
         if constexpr (E > 0) {
-            if (vec) {
 #pragma unroll
-                for (int i = 0; i < E; i += V) {
-                    const int j = (i / V * TEAM + tid) * V;
-                    if (j < n) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + j));
-                        if constexpr (sizeof(L) == 2)
-                            unpack<Bf16>(v, x + i);
-                        else
-                            unpack<F32>(v, x + i);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < V; ++c) x[i + c] = minus_inf();
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i) x[i] = i * TEAM + tid < n ? to_f32(__ldg(row + i * TEAM + tid)) : minus_inf();
-            }
+            for (int i = 0; i < E; i += U) get((i / U * TEAM + tid) * U, x + i);
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 x[i] = fmaxf(x[i], minus_inf());  // NaN is masked
                 m = fmaxf(m, x[i]);
             }
             const bool plain = fabsf(m) <= 3.402823466e38f;  // neither +inf nor masked throughout
+            if (plain) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                x[i] = plain ? expf(x[i] - m) : exp_below(x[i], m);
-                own += x[i];
+                for (int i = 0; i < E; ++i) {
+                    x[i] = expf(x[i] - m);
+                    own += x[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    x[i] = exp_below(x[i], m);
+                    own += x[i];
+                }
             }
             const float mine = m;
             join(m, own);
@@ -943,73 +967,55 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel
         }
         total = own;
         // every warp for itself: a barrier would cost more
-        for (int i = lane; i < k; i += 32) {
-            float y, dw;
-            chosen(i, y, dw);
-            mean += dw * exp_below(y, m);
-        }
+        each_chosen([&](int, float y, float dw) { mean += dw * exp_below(y, m); });
         mean = total > 0.0f ? __fdiv_rn(warp_sum(mean), total) : 0.0f;
         factor = total > 0.0f ? __fdiv_rn(-mean, total) : 0.0f;
         if constexpr (E > 0) {
             rescale *= factor;
 #pragma unroll
             for (int i = 0; i < E; ++i) x[i] *= rescale;
-            if (vec) {
 #pragma unroll
-                for (int i = 0; i < E; i += V) {
-                    const int j = (i / V * TEAM + tid) * V;
-                    if (j < n) put16(j, x + i);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (i * TEAM + tid < n) out[i * TEAM + tid] = from_f32<L>(x[i]);
-            }
+            for (int i = 0; i < E; i += U) put((i / U * TEAM + tid) * U, x + i);
         } else {
             for (int j = tid; j < n; j += TEAM) out[j] = from_f32<L>(factor * exp_below(to_f32(__ldg(row + j)), m));
         }
-    } else if (vec) {
-        for (int j = tid * V; j < n; j += TEAM * V) *reinterpret_cast<uint4*>(out + j) = make_uint4(0u, 0u, 0u, 0u);
     } else {
-        for (int j = tid; j < n; j += TEAM) out[j] = L(0);
+        // zeros, 16 bytes at a time between the boundaries in the row
+        constexpr int V = 16 / sizeof(L);
+        const int head = min(n, (int)((16 - reinterpret_cast<uintptr_t>(out) % 16) % 16 / sizeof(L)));
+        const int end = head + (n - head) / V * V, rest = head + n - end;
+        for (int j = head + tid * V; j < end; j += TEAM * V) *reinterpret_cast<uint4*>(out + j) = make_uint4(0u, 0u, 0u, 0u);
+        if (tid < rest) out[tid < head ? tid : end + tid - head] = L(0);
     }
     // the chosen entries are written again, over what is there, by the team's first warp
     float all = 1.0f, dot = 0.0f;
     if (a.renorm && tid < 32) {
         // scores, or exp(x - m) for a softmax, which is as good: the factor between them cancels
         if (softmax) {
-            for (int i = lane; i < k; i += 32) {
-                float y, dw;
-                chosen(i, y, dw);
-                m = fmaxf(m, y);
-            }
+            each_chosen([&](int, float y, float) { m = fmaxf(m, y); });
             m = warp_max(m);
         }
         all = 0.0f;
-        for (int i = lane; i < k; i += 32) {
-            float y, dw;
-            chosen(i, y, dw);
+        each_chosen([&](int, float y, float dw) {
             const float s = softmax ? exp_below(y, m) : sigmoid(y);
             all += s;
             dot += dw * s;
-        }
+        });
         all = warp_sum(all);
         dot = all > 0.0f ? __fdiv_rn(warp_sum(dot), all) : 0.0f;
     }
     sync();
     if (tid >= 32) return;
-    for (int i = lane; i < k; i += 32) {
-        float y, dw;
-        const int j = chosen(i, y, dw);
+    each_chosen([&](int j, float y, float dw) {
         if (j < 0) {
             atomicOr(&g_route_status, SDM_DEV_BAD_INDEX);
-            continue;
+            return;
         }
         float s = softmax ? exp_below(y, m) : sigmoid(y);
         if (dense) s = total > 0.0f ? __fdiv_rn(s, total) : 0.0f;
         const float u = !a.renorm ? dw : all > 0.0f ? __fdiv_rn(dw - dot, all) : 0.0f;
         out[j] = from_f32<L>(!softmax ? u * s * (1.0f - s) : dense ? s * (u - mean) : s * u);
-    }
+    });
 }
 
 struct Team {
@@ -1021,10 +1027,12 @@ struct Team {
 template <typename L>
 Team backward_kernel(int n, bool dense) {
     if (n <= 256) return {(const void*)route_backward_kernel<32, 8, L>, 128, 4};
+    if (n <= 512) return {(const void*)route_backward_kernel<32, 16, L>, 128, 4};
     if (n <= 1024) return {(const void*)route_backward_kernel<32, 32, L>, 128, 4};
     if (!dense) return {(const void*)route_backward_kernel<256, 0, L>, 256, 1};
     if (n <= 2048) return {(const void*)route_backward_kernel<256, 8, L>, 256, 1};
     if (n <= 4096) return {(const void*)route_backward_kernel<256, 16, L>, 256, 1};
+    if (n <= 5120) return {(const void*)route_backward_kernel<256, 20, L>, 256, 1};
     if (n <= 6144) return {(const void*)route_backward_kernel<256, 24, L>, 256, 1};
     if (n <= 8192) return {(const void*)route_backward_kernel<256, 32, L>, 256, 1};
     if (n <= 16384) return {(const void*)route_backward_kernel<512, 32, L>, 512, 1};
@@ -1088,7 +1096,7 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     }
     if (a.tokens > INT_MAX) return SDM_ECOUNT;
     int staged = (size_t)a.n * 4 <= kStagedBytes ? 1 : 0;
-    const size_t smem = staged ? (size_t)a.n * 4 : 0;
+    const size_t smem = staged ? (size_t)(a.n + 4) * 4 : 0;
     // threads for 32 to 64 ranks each; blocks of 256 with 64 KB of ranks fit three times on an SM, so that
     // one loads its row while others choose (1024 rows of 16384: two blocks of 512 threads 43 us)
     const int threads = a.n > 16384 ? 512 : a.n > 4096 ? 256 : 128;
