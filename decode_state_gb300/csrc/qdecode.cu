@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(NT, RPT == 8 ? 1 : 4) qdecode_kernel(const QDe
 #pragma unroll
         for (int j = 0; j < RPT; ++j) {
             new_row(j, x);
-            top[j] = piece_top<F>(x);
+            top[j] = piece_top<16>(x);
         }
         group_scales<F, RPT>(top, gl, new_scale, inv);
 #pragma unroll

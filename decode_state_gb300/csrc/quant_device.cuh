@@ -163,32 +163,30 @@ struct Int4 {
     static constexpr bool kQuantised = true;
     static constexpr float kLevels = 7.0f;
     static constexpr float kInvHigh = 0x1.24924ap-3f, kInvLow = -0x1.b6db6ep-28f;  // 1 / 7
-    static __device__ __forceinline__ void unpack2(const uint4& v, f32x2* x) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    static __device__ __forceinline__ void unpack_word(uint32_t w, f32x2* x) {  // 8 columns
         const f32x2 off = pair(-8388616.0f, -8388616.0f);  // -(2^23 + 8)
+        const uint32_t u = w ^ 0x88888888u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t u = w[i] ^ 0x88888888u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[4 * i + j] = add2(pair(__uint_as_float(((u >> (8 * j)) & 15u) | 0x4B000000u),
-                                         __uint_as_float(((u >> (8 * j + 4)) & 15u) | 0x4B000000u)),
-                                    off);
-        }
+        for (int j = 0; j < 4; ++j)
+            x[j] = add2(pair(__uint_as_float(((u >> (8 * j)) & 15u) | 0x4B000000u),
+                             __uint_as_float(((u >> (8 * j + 4)) & 15u) | 0x4B000000u)),
+                        off);
     }
-    static __device__ __forceinline__ uint4 pack2(const f32x2* y) {
-        uint32_t w[4];
+    static __device__ __forceinline__ uint32_t pack_word(const f32x2* y) {
+        uint32_t w = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float a, b;
-                split(y[4 * i + j], a, b);
-                w[i] |= (round_bits(a) & 15u) << (8 * j) | (round_bits(b) & 15u) << (8 * j + 4);
-            }
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            split(y[j], a, b);
+            w |= (round_bits(a) & 15u) << (8 * j) | (round_bits(b) & 15u) << (8 * j + 4);
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        return w;
+    }
+    static __device__ __forceinline__ void unpack2(const uint4& v, f32x2* x) {
+        unpack_word(v.x, x);
+        unpack_word(v.y, x + 4);
+        unpack_word(v.z, x + 8);
+        unpack_word(v.w, x + 12);
     }
 };
 
@@ -248,11 +246,11 @@ __device__ __forceinline__ float group_scale(float top, float* inv) {
 }
 
 // The largest magnitude of this lane's C columns.
-template <typename F>
+template <int C>
 __device__ __forceinline__ float piece_top(const f32x2* x) {
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < F::C / 2; ++i) {
+    for (int i = 0; i < C / 2; ++i) {
         float a, b;
         split(x[i], a, b);
         top = abs_max(top, a, b);

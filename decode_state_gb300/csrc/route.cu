@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
 // its exponentials stay in registers until the gradients are written (E 0: rows too long for that are
 // read three times). All others get zeros there. The chosen entries are written over that.
 template <int TEAM, int E, typename L>
-__global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, TEAM == 256 && E <= 24 ? 6 : 1) route_backward_kernel(const RouteArgs a) {
     constexpr int NT = TEAM == 32 ? 128 : TEAM, TEAMS = NT / TEAM, WARPS = TEAM / 32, U = 4 / sizeof(L);
     __shared__ float largest[NT / 32], sums[NT / 32];
     grid_dependency_wait();
@@ -909,7 +909,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM) route_backward_kernel
     };
 
     // every warp has the first chosen entries at hand, loaded while the row is on its way
-    constexpr int KEPT = 2;
+    constexpr int KEPT = 1;
     int kept_j[KEPT];
     float kept_x[KEPT], kept_dw[KEPT];
 #pragma unroll

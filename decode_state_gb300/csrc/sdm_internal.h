@@ -56,7 +56,8 @@ struct QuantRowsArgs {
     const void* slots;  // nullptr: row i is slot i
     int64_t n_slots, row_stride, n_rows;
     int hd, group, idx64;
-    int pieces, groups, lanes;  // 16-byte pieces and scale groups of a row; lanes that work on it
+    int pieces, groups, lanes;  // a lane's shares of a row of codes, scale groups of a row; lanes that work on it
+    int run_rows;               // rows of a block that takes them through shared memory
     int vec;    // the rows' pieces are 16-byte aligned
     int small;  // lane numbers fit 32 bits
 };
