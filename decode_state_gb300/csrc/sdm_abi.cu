@@ -549,7 +549,7 @@ int sdm_device_status(unsigned int* status, int clear) {
     int e = 0;
     unsigned int all = 0;
     for (const auto read : {sdm::decode_status, sdm::gather_status, sdm::quant_status, sdm::qgather_status,
-                            sdm::qdecode_status, sdm::route_status}) {
+                            sdm::gather_ring_status, sdm::qdecode_status, sdm::route_status}) {
         unsigned int word = 0;
         if (e == 0) e = read(&word, clear != 0);
         all |= word;

@@ -155,6 +155,11 @@ int run_gather(const GatherLaunch& L, cudaStream_t stream);
 int launch_quant_rows(const QuantRowsArgs& a, int format, int row_dtype, bool write, cudaStream_t stream);
 int launch_qgather(const QGatherArgs& a, int format, cudaStream_t stream);
 int launch_gather_dw(const QGatherArgs& a, int format, cudaStream_t stream);
+// The two of them for many tokens, 16-byte aligned rows (a.pieces, a.groups, a.row_bytes and a.vec_out set).
+int launch_gather_ring(const QGatherArgs& a, int format, bool grad, cudaStream_t stream);
+// Lanes that hold a row or a slice of it: the number that leaves the fewest lanes over, the larger of
+// equals (its rows come in longer runs); 4 to `most`.
+int row_lanes(int pieces, int most);
 int launch_qdecode(const QDecodeArgs& a, int format, cudaStream_t stream);
 int launch_route(const RouteArgs& a, cudaStream_t stream);
 int launch_route_backward(const RouteArgs& a, cudaStream_t stream);
@@ -164,6 +169,7 @@ int decode_status(unsigned int* word, bool clear);
 int gather_status(unsigned int* word, bool clear);
 int quant_status(unsigned int* word, bool clear);
 int qgather_status(unsigned int* word, bool clear);
+int gather_ring_status(unsigned int* word, bool clear);
 int qdecode_status(unsigned int* word, bool clear);
 int route_status(unsigned int* word, bool clear);
 
