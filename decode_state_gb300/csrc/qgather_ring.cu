@@ -51,14 +51,14 @@ __device__ __forceinline__ int turn(int r) {
     return LR == 4 ? (r >> 1) & 3 : r & 7;
 }
 
-// One step's share of shared memory: the rows' slices by 16-byte pieces, the entries' scales, and for
-// the gradient the slice of dout. ONE: a row's slice has one scale.
+// One step's share of shared memory: the rows' slices by 16-byte pieces, for the gradient the slice of
+// dout, and the entries' scales, unless (ONE) a row's slice has a single one.
 template <typename F, int LR, bool GRAD, bool ONE>
 struct RingStage {
     static constexpr int ENTRIES = LR <= 8 ? 32 : 256 / LR;  // of a step, so that its rows are 4 KB
     static constexpr int STEPS = ENTRIES * LR / 32;          // rows of a row slot
     static constexpr int COLS = LR * F::C;
-    static constexpr int GROUPS = !F::kQuantised ? 0 : ONE ? 1 : (COLS + 31) / 32;  // scales of a row's slice at most
+    static constexpr int GROUPS = !F::kQuantised || ONE ? 0 : (COLS + 31) / 32;  // scales of a row's slice at most
     uint4 rows[ENTRIES * LR];
     float dout[GRAD ? COLS : 4];
     float scale[GROUPS > 0 ? ENTRIES * GROUPS : 4];
@@ -277,9 +277,10 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
         if (a.idx64) raw_hi = __ldg(word + 1);
         if (!GRAD) raw_w = a.w_bf16 ? __ldg(static_cast<const uint16_t*>(a.w[at.op]) + i) : __ldg(static_cast<const uint32_t*>(a.w[at.op]) + i);
     };
-    // request the step's rows (one commit for every step, requested or not); returns the lane's weight
-    const auto request = [&](S& st) {
-        float weight = 0.0f;
+    // request the step's rows (one commit for every step, requested or not); gives the lane's weight and,
+    // where a row's slice has one, its scale
+    const auto request = [&](S& st, float& weight, float& scale) {
+        weight = scale = 0.0f;
         if (at.t >= 0) {
             const int n = a.width[at.op] - at.base;
             int slot = -1;
@@ -303,7 +304,9 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
             if constexpr (F::kQuantised) {
                 const float* scales = a.scales + (int64_t)slot * a.groups + g0;
                 if (ONE) {
-                    if (lane < ENTRIES) copy4_if(&st.scale[lane], scales, slot >= 0);
+                    // to a register, past L1: copies of 32 scattered words would each take a line of the little L1
+                    // that the stages leave
+                    scale = load4_if(scales, slot >= 0);
                 } else if (lane < ENTRIES) {
                     const int ng = min(a.groups - g0, (LR * C + a.group - 1) / a.group);
                     for (int g = 0; g < ng; ++g) copy4_if(&st.scale[lane * S::GROUPS + g], scales + g, slot >= 0);
@@ -320,18 +323,17 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        return weight;
     };
 
     Step steps[kAhead + 1];  // the steps of the ring, the oldest first, and their weights
-    float weights[kAhead + 1];
+    float weights[kAhead + 1], one_scale[kAhead + 1];
     int head = 0;  // the stage of the oldest
     advance();
     load_entries();
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
         steps[i] = at;
-        weights[i] = request(stages[i]);
+        request(stages[i], weights[i], one_scale[i]);
         if (at.t >= 0) advance();
         load_entries();
     }
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
     float dot[IS_F32 ? STEPS : 1];
     while (steps[0].t >= 0) {
         steps[kAhead] = at;
-        weights[kAhead] = request(stages[head == 0 ? kAhead : head - 1]);
+        request(stages[head == 0 ? kAhead : head - 1], weights[kAhead], one_scale[kAhead]);
         if (at.t >= 0) advance();
         load_entries();
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
@@ -488,9 +490,14 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
                     for (int m = 0; m < MATS / 2; ++m) {
                         float low = undo, high = undo;
                         if constexpr (F::kQuantised) {
-                            const bool there = ONE || g0 + g < a.groups;  // behind the row's end there are no scales
-                            low *= there ? st.scale[(16 * m + q) * S::GROUPS + g] : 0.0f;
-                            high *= there ? st.scale[(16 * m + 8 + q) * S::GROUPS + g] : 0.0f;
+                            if (ONE) {
+                                low *= __shfl_sync(kAll, one_scale[0], 16 * m + q);
+                                high *= __shfl_sync(kAll, one_scale[0], 16 * m + 8 + q);
+                            } else {
+                                const bool there = g0 + g < a.groups;  // behind the row's end there are no scales
+                                low *= there ? st.scale[(16 * m + q) * S::GROUPS + g] : 0.0f;
+                                high *= there ? st.scale[(16 * m + 8 + q) * S::GROUPS + g] : 0.0f;
+                            }
                         }
                         dots[m][0] = fmaf(part[m][0], low, dots[m][0]);
                         dots[m][1] = fmaf(part[m][1], low, dots[m][1]);
@@ -528,7 +535,7 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
                     // the entries' weights, with the scales of the columns that follow, as limbs
                     const int g = ONE ? 0 : p * C / a.group;
                     const bool there = lane < ENTRIES && (ONE || g0 + g < a.groups);
-                    const float w = there ? weights[0] * st.scale[lane * S::GROUPS + g] : 0.0f;
+                    const float w = there ? weights[0] * (ONE ? one_scale[0] : st.scale[lane * S::GROUPS + g]) : 0.0f;
                     const float f = limb_scale(__uint_as_float(__reduce_max_sync(kAll, __float_as_uint(fabsf(w)))), &undo);
                     uint16_t l[3];
                     limbs_f16(w * f, l);
@@ -589,6 +596,7 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
         for (int i = 0; i < kAhead; ++i) {
             steps[i] = steps[i + 1];
             weights[i] = weights[i + 1];
+            one_scale[i] = one_scale[i + 1];
         }
     }
 }
