@@ -5,8 +5,8 @@
 //
 // Design. Rows of 128 bytes at random places are what bounds both: at 7 TB/s every SM has to have
 // some 50 KB of them on their way all the time. One block an SM; its persistent warps walk over the live
-// tokens in steps of up to 32 entries. While a step is summed from shared memory, the rows of the next
-// two are on their way by cp.async, and the indices of the one behind them by plain loads. LR lanes copy
+// tokens in steps of up to 32 entries. While a step is summed from shared memory, the rows of the next are
+// on their way by cp.async, and the indices of the one behind it by plain loads. LR lanes copy
 // one row (or a slice of it), 16 bytes each. A block finds the live tokens by the prefix sums of
 // chunk_valid, so that every warp gets as many of them: by token number, warps whose tokens mostly lay at
 // the end of their chunks were done long before the others.
@@ -34,8 +34,12 @@ __device__ unsigned int g_ring_status;
 
 constexpr unsigned kAll = 0xffffffffu;
 
-constexpr int kRingWarps = 16;  // warps of a block at most
-constexpr int kAhead = 2;       // steps whose rows are on their way while one is summed
+// Warps of a block at most, and the steps whose rows are on their way while one is summed. More of
+// either is slower: the stages take shared memory from L1, whose lines the requests on their way need.
+// Gather / gradient of 65536 tokens, 64 and 64 rows of 128 bytes each: 16 warps 1 ahead 138 / 82 us, 2
+// ahead 173 / 101; 12 warps 1 ahead 146 / 93, 2 ahead 150 / 95; 20 warps 1 ahead 143 / 100.
+constexpr int kRingWarps = 16;
+constexpr int kAhead = 1;
 
 __device__ __forceinline__ void copy16_if(void* dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
@@ -77,15 +81,15 @@ struct RingScratch {
 
 constexpr float kLimb = 0x1p-11f;  // weight of the next f16 limb
 
-// The power of two that brings magnitudes of at most `most` below 2, and (undo) back; any magnitudes
+// The power of two that brings magnitudes of at most `most` below 4, and (undo) back; any magnitudes
 // where `most` is not finite.
 __device__ __forceinline__ float limb_scale(float most, float* undo) {
-    const uint32_t e = min(max(__float_as_uint(most) >> 23, 27u), 227u);
+    const uint32_t e = min(max(__float_as_uint(most) >> 23, 27u), 253u);
     *undo = __uint_as_float(e << 23);
     return __uint_as_float((254u - e) << 23);
 }
 
-// x as three f16 limbs, |x| < 2; an infinity or NaN is in the first alone
+// x as three f16 limbs, |x| < 4; an infinity or NaN is in the first alone
 __device__ __forceinline__ void limbs_f16(float x, uint16_t* l) {
     const __half a = __float2half_rn(x);
     float rest = (x - __half2float(a)) * 2048.0f;
@@ -337,23 +341,28 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
         if (at.t >= 0) advance();
         load_entries();
     }
-    // padding tokens: zeros, while the first rows are on their way
-    if (live < tokens) {
-        for (int64_t t0 = (int64_t)me * 32; t0 < tokens; t0 += (int64_t)stride * 32) {
-            for (uint32_t pads = __ballot_sync(kAll, t0 + lane < tokens && padding(a, t0 + lane)); pads; pads &= pads - 1) {
-                const int64_t t = t0 + __ffs(pads) - 1;
-                for (int op = 0; op < a.n_ops; ++op) {
-                    if (GRAD) {
-                        for (int i = lane; i < a.width[op]; i += 32) store_dw(a, op, t * a.width[op] + i, 0.0f);
-                    } else if (a.vec_out) {
-                        for (int c = 4 * lane; c < hd; c += 128) *reinterpret_cast<float4*>(a.out[op] + t * hd + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    } else {
-                        for (int c = lane; c < hd; c += 32) a.out[op][t * hd + c] = 0.0f;
-                    }
-                }
+    // padding tokens get zeros, one for every step, while rows are on their way
+    int64_t pad_at = live < tokens ? (int64_t)me * 32 : tokens;  // the 32 tokens that are looked at next
+    uint32_t pads = 0;                                           // padding among the 32 before
+    const auto zero_one = [&]() {
+        if (pads == 0) {
+            if (pad_at >= tokens) return;
+            pads = __ballot_sync(kAll, pad_at + lane < tokens && padding(a, pad_at + lane));
+            pad_at += (int64_t)stride * 32;
+            if (pads == 0) return;
+        }
+        const int64_t t = pad_at - (int64_t)stride * 32 + __ffs(pads) - 1;
+        pads &= pads - 1;
+        for (int op = 0; op < a.n_ops; ++op) {
+            if (GRAD) {
+                for (int i = lane; i < a.width[op]; i += 32) store_dw(a, op, t * a.width[op] + i, 0.0f);
+            } else if (a.vec_out) {
+                for (int c = 4 * lane; c < hd; c += 128) *reinterpret_cast<float4*>(a.out[op] + t * hd + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            } else {
+                for (int c = lane; c < hd; c += 32) a.out[op][t * hd + c] = 0.0f;
             }
         }
-    }
+    };
     const int q = lane >> 2, i4 = lane & 3;  // the lane's row (or column) and place in it of a matrix
     constexpr int MATS = ENTRIES / 8;         // matrices of a step's rows
     constexpr int TILES = IS_INT4 ? 2 * LR : LR;  // 16 columns of the sums each
@@ -365,6 +374,7 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
         request(stages[head == 0 ? kAhead : head - 1], weights[kAhead], one_scale[kAhead]);
         if (at.t >= 0) advance();
         load_entries();
+        zero_one();
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
         __syncwarp();
         const S& st = stages[head];
@@ -488,7 +498,7 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
                     const int g = ONE || !F::kQuantised ? 0 : p * C / a.group;
 #pragma unroll
                     for (int m = 0; m < MATS / 2; ++m) {
-                        float low = undo, high = undo;
+                        float low = 1.0f, high = 1.0f;
                         if constexpr (F::kQuantised) {
                             if (ONE) {
                                 low *= __shfl_sync(kAll, one_scale[0], 16 * m + q);
@@ -499,10 +509,10 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
                                 high *= there ? st.scale[(16 * m + 8 + q) * S::GROUPS + g] : 0.0f;
                             }
                         }
-                        dots[m][0] = fmaf(part[m][0], low, dots[m][0]);
-                        dots[m][1] = fmaf(part[m][1], low, dots[m][1]);
-                        dots[m][2] = fmaf(part[m][2], high, dots[m][2]);
-                        dots[m][3] = fmaf(part[m][3], high, dots[m][3]);
+                        dots[m][0] = fmaf(part[m][0] * low, undo, dots[m][0]);
+                        dots[m][1] = fmaf(part[m][1] * low, undo, dots[m][1]);
+                        dots[m][2] = fmaf(part[m][2] * high, undo, dots[m][2]);
+                        dots[m][3] = fmaf(part[m][3] * high, undo, dots[m][3]);
                     }
                 }
             }
@@ -599,6 +609,7 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
             one_scale[i] = one_scale[i + 1];
         }
     }
+    while (pads != 0 || pad_at < tokens) zero_one();
 }
 
 struct Kernel {
@@ -616,7 +627,7 @@ Kernel kernel_lr(bool one) {
     return {(const void*)gather_ring<F, LR, GRAD, true>, sizeof(RingStage<F, LR, GRAD, true>) * (kAhead + 1) + sizeof(RingScratch<F, LR, GRAD>)};
 }
 
-// MOST: lanes of a row at most (16 entries fill a matrix product, and the sums of more columns the registers)
+// MOST: lanes of a row at most
 template <typename F, bool GRAD, int MOST>
 Kernel kernel_of(int lr, bool one) {
     if constexpr (MOST == 32) {
@@ -632,16 +643,19 @@ Kernel kernel_of(int lr, bool one) {
 
 int launch_gather_ring(const QGatherArgs& a0, int format, bool grad, cudaStream_t stream) {
     QGatherArgs a = a0;
-    const int lr = row_lanes(a.pieces, format == SDM_F32 ? 32 : format == SDM_INT4 ? 8 : 16);
+    // Slices of codes have at most 128 bytes: 65536 tokens with 64 and 64 rows of 256 bytes take 311 us (gradient
+    // 171) in two slices and 392 (227) in one, whose 256 sums fill the registers. bf16 has half the columns in
+    // as many bytes: 107 us in one slice of 256 bytes, 125 in two.
+    const int lr = row_lanes(a.pieces, format == SDM_F32 ? 32 : format == SDM_BF16 ? 16 : 8);
     a.slices = (a.pieces + lr - 1) / lr;
     const bool one = a.groups <= 1;
-    const Kernel k = grad ? (format == SDM_INT8   ? kernel_of<Int8, true, 16>(lr, one)
-                             : format == SDM_FP8  ? kernel_of<Fp8, true, 16>(lr, one)
+    const Kernel k = grad ? (format == SDM_INT8   ? kernel_of<Int8, true, 8>(lr, one)
+                             : format == SDM_FP8  ? kernel_of<Fp8, true, 8>(lr, one)
                              : format == SDM_INT4 ? kernel_of<Int4, true, 8>(lr, one)
                              : format == SDM_BF16 ? kernel_of<Bf16, true, 16>(lr, one)
                                                   : kernel_of<F32, true, 32>(lr, one))
-                          : (format == SDM_INT8  ? kernel_of<Int8, false, 16>(lr, one)
-                             : format == SDM_FP8 ? kernel_of<Fp8, false, 16>(lr, one)
+                          : (format == SDM_INT8  ? kernel_of<Int8, false, 8>(lr, one)
+                             : format == SDM_FP8 ? kernel_of<Fp8, false, 8>(lr, one)
                                                  : kernel_of<Int4, false, 8>(lr, one));
     // one block for every SM, of as many warps as find room for their stages
     const size_t prefix = a.chunk_valid ? ((size_t)(a.tokens / a.chunk) + 4) / 4 * 16 : 0;
