@@ -8,11 +8,12 @@
 //
 // Both forward kernels find a lower bound of the k-th rank first: of the largest ranks of 32 lanes, or
 // of all threads of a block, the k-th largest is one, since k entries at least reach it. The entries
-// that reach it are few more than k; they are collected in shared memory and ranked by counting.
+// that reach it are few more than k; they are collected in shared memory and ranked by counting. With
+// too few lanes for that, a warp halves the range of the ranks until few enough reach its lower end.
 // Where they are too many (equal ranks), or fewer than k entries are not masked, a slower path
 // follows that takes any ranks.
 //
-// route_warp_kernel (n <= 1024, k <= 32): a warp for each token, its ranks in registers, lane l the
+// route_warp_kernel (n <= 1024, k <= 64): a warp for each token, its ranks in registers, lane l the
 // consecutive entries from l * E on, so that lane order is index order. Bound by instructions (an
 // exponential and a reciprocal for every entry of a biased sigmoid), not by its 2 or 4 bytes; small
 // rows get half a warp, which halves what is spent on a token rather than on its entries.
@@ -179,6 +180,56 @@ __device__ __forceinline__ float lanes_max(float x) {
     for (int o = LANES / 2; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, o));
     return x;
 }
+
+// A bound that at least k of a warp's ranks reach (E on each lane, -inf for masked ones; k <= 64), and at
+// most `most` unless too many are equal; that of all ranks where no more are live. Halves the range
+// between a bound that k reach and one that fewer do, by value and by the order of the floats in turn: the
+// first is quick for ranks of one size, the second needs no more than 32 steps for any. At most a rank of
+// each lane lies above all lanes' second largest, and at least two of each reach the least of those.
+template <int E>
+__device__ __forceinline__ float reached_by(const float* r, int k, int most) {
+    Top2 top;
+#pragma unroll
+    for (int i = 0; i < E; ++i) top.add(r[i]);
+    float low = k <= 32 ? top.a : top.b, high = low;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        low = fminf(low, __shfl_xor_sync(kAll, low, o));
+        high = fmaxf(high, __shfl_xor_sync(kAll, high, o));
+    }
+    if (low == minus_inf()) {  // some lanes have too few: the least live rank
+        low = 3.402823466e38f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) low = fminf(low, r[i] == minus_inf() ? low : r[i]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) low = fminf(low, __shfl_xor_sync(kAll, low, o));
+        high = lanes_max<32>(top.a);
+    }
+    const auto reaching = [&](float bound) {
+        float c = 0.0f;  // a comparison gives 1 or 0 as a float in one instruction
+#pragma unroll
+        for (int i = 0; i < E; ++i) c += r[i] >= bound ? 1.0f : 0.0f;
+        return __reduce_add_sync(kAll, (int)c);
+    };
+    int reach = reaching(low);
+    for (int step = 0; reach > most; ++step) {
+        float mid = 0.5f * low + 0.5f * high;
+        if (step & 1 || !(mid > low && mid < high)) {
+            const uint32_t a = ordered(low), b = ordered(high);
+            if (b <= a + 1) break;  // neighbours
+            mid = unordered(a + (b - a) / 2);
+        }
+        const int c = reaching(mid);
+        if (c >= k) {
+            low = mid;
+            reach = c;
+        } else {
+            high = mid;
+        }
+    }
+    return low;
+}
+
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float x) {
 #pragma unroll
@@ -203,7 +254,7 @@ __device__ __forceinline__ float rough_sigmoid(float x) {
 // are too close to call.
 template <int LANES, int E, int V, bool SOFTMAX, typename L>
 __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArgs a) {
-    constexpr int TEAMS = kWarpThreads / LANES, CANDS = 2 * LANES;
+    constexpr int TEAMS = kWarpThreads / LANES, Q = V == 0 ? 3 : 2, CANDS = Q * LANES;  // Q: candidates of a lane at most
     extern __shared__ float staged[];  // groups that are no whole lanes: every team's group values [n] and scores [n_groups]
     __shared__ uint16_t found[TEAMS][CANDS];
     grid_dependency_wait();
@@ -327,20 +378,28 @@ __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArg
             for (int i = 0; i < E; ++i) r[i] = minus_inf();
         }
     } else if (grouped) {
-        float* value = staged + (size_t)team * (n + a.n_groups);
-        float* scores = value + n;
+        float* value = staged + (size_t)team * (n + LANES + a.n_groups);
+        float* scores = value + n + LANES;
+        const auto place = [](int j) { return j + j / E; };  // lanes' entries are one bank apart
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            if (j0 + i < n) value[j0 + i] = by_exp ? (r[i] == minus_inf() ? minus_inf() : exp_below(x[i], m)) : r[i];
+            if (j0 + i < n) value[place(j0 + i)] = by_exp ? (r[i] == minus_inf() ? minus_inf() : exp_below(x[i], m)) : r[i];
         __syncwarp();
-        for (int g = l; g < a.n_groups; g += LANES) {
+        int share = 1;  // lanes of a group
+        while (2 * share * a.n_groups <= LANES && 2 * share <= per) share *= 2;
+        for (int g0 = 0; g0 < a.n_groups; g0 += LANES / share) {
+            const int g = g0 + l / share, from = l % share;
             Top2 top;
-            int at = l % per;  // lanes start apart, since groups are often a multiple of the banks
-            for (int i = 0; i < per; ++i) {
-                top.add(value[g * per + at]);
-                at = at + 1 == per ? 0 : at + 1;
+            if (g < a.n_groups) {
+                const int own = (per - from + share - 1) / share;
+                int i = g % own;  // groups start apart, since they are often a multiple of the banks long
+                for (int left = own; left > 0; --left) {
+                    top.add(value[place(g * per + from + i * share)]);
+                    i = i + 1 == own ? 0 : i + 1;
+                }
             }
-            scores[g] = top.value(a.group_top);
+            for (int o = 1; o < share; o <<= 1) top.join(__shfl_xor_sync(kAll, top.a, o), __shfl_xor_sync(kAll, top.b, o));
+            if (g < a.n_groups && from == 0) scores[g] = top.value(a.group_top);
         }
         __syncwarp();
         uint32_t* stays = reinterpret_cast<uint32_t*>(value);  // the values have been read
@@ -357,15 +416,22 @@ __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArg
         }
     }
 
-    // the entries that reach the k-th largest of the maxima of the lanes' entries (V 2: of both halves of them)
-    float best[V];
+    // a bound that k entries reach at least, and few more
+    float bound;
+    if constexpr (V == 0) {
+        static_assert(LANES == 32, "a warp for each token");
+        bound = reached_by<E>(r, k, CANDS);
+    } else {
+        // the k-th largest of the maxima of the lanes' entries (V 2: of both halves of them)
+        float best[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        best[v] = r[v * (E / V)];
+        for (int v = 0; v < V; ++v) {
+            best[v] = r[v * (E / V)];
 #pragma unroll
-        for (int i = 1; i < E / V; ++i) best[v] = fmaxf(best[v], r[v * (E / V) + i]);
+            for (int i = 1; i < E / V; ++i) best[v] = fmaxf(best[v], r[v * (E / V) + i]);
+        }
+        bound = kth_of_lanes<LANES, V>(best, k);
     }
-    float bound = kth_of_lanes<LANES, V>(best, k);
     if (rough && bound > minus_inf()) bound -= margin(bound);
     bound = fmaxf(bound, -3.402823466e38f);  // masked entries never reach it
     uint32_t reach = 0;  // bit i: entry i does
@@ -412,49 +478,55 @@ __global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArg
     __syncwarp();
     // exact ranks of the candidates; where they were collected their order is that of the indices,
     // and where they were taken in rounds it is that of the ranks: equal ranks go by the place
-    int j[2], rank[2] = {0, 0};
-    float score[2] = {0.0f, 0.0f}, key[2] = {minus_inf(), minus_inf()};
-    const bool two = __any_sync(kAll, count > LANES);  // a second candidate for some lanes
-    const auto rate = [&](int q) {
-        if (l + LANES * q < count) {
+    int j[Q], rank[Q];
+    float score[Q], key[Q];
+    bool some[Q];  // whether a lane has a candidate q
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        rank[q] = 0;
+        score[q] = 0.0f;
+        key[q] = minus_inf();
+        some[q] = q == 0 || __any_sync(kAll, count > LANES * q);
+        if (some[q] && l + LANES * q < count) {
             j[q] = cand[l + LANES * q];
             const float y = to_f32(__ldg(row + j[q]));
             score[q] = softmax ? exp_below(y, m) : sigmoid(y);
             key[q] = !softmax ? score[q] : biased ? __fdiv_rn(score[q], total) : y;
             if (biased) key[q] += __ldg(a.bias + j[q]);
         }
-    };
-    rate(0);
-    if (two) rate(1);
-    const int most = min(LANES, LANES == 32 ? count : max(count, __shfl_xor_sync(kAll, count, 16)));
-    for (int o0 = 0; o0 < most; o0 += 4) {
+    }
+    const int most = LANES == 32 ? count : max(count, __shfl_xor_sync(kAll, count, 16));
 #pragma unroll
-        for (int o = o0; o < o0 + 4; ++o) {
-            const float other = __shfl_sync(kAll, key[0], o, LANES);  // -inf behind the last one: better than none
-            rank[0] += other > key[0] || (other == key[0] && o < l);
-            if (two) rank[1] += other >= key[1];
+    for (int p = 0; p < Q; ++p) {
+        const int end = min(LANES, most - LANES * p);
+        for (int o0 = 0; o0 < end; o0 += 4) {
+#pragma unroll
+            for (int o = o0; o < o0 + 4; ++o) {
+                const float other = __shfl_sync(kAll, key[p], o, LANES);  // -inf behind the last one: better than none
+#pragma unroll
+                for (int q = 0; q < Q; ++q)
+                    if (some[q]) rank[q] += other > key[q] || (other == key[q] && (p == q ? o < l : p < q));
+            }
         }
     }
-    if (two) {
-        for (int o = 0; o < LANES; ++o) {
-            const float other = __shfl_sync(kAll, key[1], o, LANES);
-            rank[0] += other > key[0];
-            rank[1] += other > key[1] || (other == key[1] && o < l);
-        }
+    bool mine[Q];
+    float chosen = 0.0f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        mine[q] = some[q] && l + LANES * q < count && rank[q] < k;
+        if (mine[q]) chosen += score[q];
     }
-    const bool mine[2] = {l < count && rank[0] < k, two && l + LANES < count && rank[1] < k};
-    if (a.renorm) total = lanes_sum<LANES>((mine[0] ? score[0] : 0.0f) + (mine[1] ? score[1] : 0.0f));
+    if (a.renorm) total = lanes_sum<LANES>(chosen);
     const float factor = (softmax || a.renorm) && total > 0.0f ? __fdividef(a.scale, total) : a.scale;
     if (!there) return;
     const int64_t to = t * k;
-    const auto put = [&](int q) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
         if (mine[q]) {
             put_index(a, t, rank[q], j[q]);
             a.w[to + rank[q]] = score[q] * factor;
         }
-    };
-    put(0);
-    if (two) put(1);
+    }
     if (count < k) {  // fill up with masked entries, in index order
         uint32_t gone = 0;
 #pragma unroll
@@ -1042,6 +1114,10 @@ Team backward_kernel(int n, bool dense) {
 template <typename L, bool SOFTMAX>
 const void* warp_kernel(int lanes, int e, int v) {
     if (lanes == 16) return e == 8 ? (const void*)route_warp_kernel<16, 8, 2, SOFTMAX, L> : (const void*)route_warp_kernel<16, 16, 2, SOFTMAX, L>;
+    if (v == 0)
+        return e == 8    ? (const void*)route_warp_kernel<32, 8, 0, SOFTMAX, L>
+               : e == 16 ? (const void*)route_warp_kernel<32, 16, 0, SOFTMAX, L>
+                         : (const void*)route_warp_kernel<32, 32, 0, SOFTMAX, L>;
     if (v == 1)
         return e == 8    ? (const void*)route_warp_kernel<32, 8, 1, SOFTMAX, L>
                : e == 16 ? (const void*)route_warp_kernel<32, 16, 1, SOFTMAX, L>
@@ -1070,29 +1146,31 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     // The warp kernel, with as few lanes and maxima as leave twice k maxima among the entries whose groups
     // stay: the k-th largest of them is then a close bound. Half a warp and two maxima a lane for 65536 rows
     // of 256 with 8 of 4 groups of 32: 48 us, a whole one and one each: 62; without two k of them (one
-    // maximum each for half a warp, 8 in all) 76.
+    // maximum each for half a warp, 8 in all) 76. Where no such choice is left, and for more than 32 entries, a
+    // bound by halving; 32768 float32 rows of 200, 500, 1000 with k = 64: 110, 123, 228 us, the block kernel 273, 211,
+    // 266; of 500 with k = 8 the maxima take 44 us, halving 88.
     const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups;
     const int live = grouped ? a.n / a.n_groups * a.top_groups : a.n;
-    if (a.n <= 1024 && a.k <= 32) {
+    if (a.n <= 1024 && a.k <= 64) {
         const int e32 = a.n <= 256 ? 8 : a.n <= 512 ? 16 : 32, e16 = a.n <= 128 ? 8 : 16;
         int lanes = 0, e = 0, v = 0;
         if (a.n <= 256 && 2 * a.k <= live / (e16 / 2))
             lanes = 16, e = e16, v = 2;
         else if (2 * a.k <= live / e32)
             lanes = 32, e = e32, v = 1;
-        else if (3 * a.k <= 2 * (live / (e32 / 2)) || a.n <= 256)
+        else if (a.k <= 32 && (3 * a.k <= 2 * (live / (e32 / 2)) || a.n <= 256))
             lanes = 32, e = e32, v = 2;
-        if (lanes != 0) {
-            const int teams = kWarpThreads / lanes;
-            const int64_t blocks = (a.tokens + teams - 1) / teams;
-            if (blocks > INT_MAX) return SDM_ECOUNT;
-            const size_t smem = grouped ? (size_t)teams * (a.n + a.n_groups) * 4 : 0;
-            const bool softmax = a.score == SDM_SOFTMAX;
-            const void* fn = a.logit_bf16 ? (softmax ? warp_kernel<uint16_t, true>(lanes, e, v) : warp_kernel<uint16_t, false>(lanes, e, v))
-                                          : (softmax ? warp_kernel<float, true>(lanes, e, v) : warp_kernel<float, false>(lanes, e, v));
-            void* args[] = {&a};
-            return launch_pdl_raw(fn, dim3((unsigned)blocks), dim3(kWarpThreads), smem, stream, args);
-        }
+        else
+            lanes = 32, e = e32, v = 0;
+        const int teams = kWarpThreads / lanes;
+        const int64_t blocks = (a.tokens + teams - 1) / teams;
+        if (blocks > INT_MAX) return SDM_ECOUNT;
+        const size_t smem = grouped ? (size_t)teams * (a.n + lanes + a.n_groups) * 4 : 0;
+        const bool softmax = a.score == SDM_SOFTMAX;
+        const void* fn = a.logit_bf16 ? (softmax ? warp_kernel<uint16_t, true>(lanes, e, v) : warp_kernel<uint16_t, false>(lanes, e, v))
+                                      : (softmax ? warp_kernel<float, true>(lanes, e, v) : warp_kernel<float, false>(lanes, e, v));
+        void* args[] = {&a};
+        return launch_pdl_raw(fn, dim3((unsigned)blocks), dim3(kWarpThreads), smem, stream, args);
     }
     if (a.tokens > INT_MAX) return SDM_ECOUNT;
     int staged = (size_t)a.n * 4 <= kStagedBytes ? 1 : 0;
