@@ -82,6 +82,7 @@ struct QGatherArgs {
     int64_t row_bytes;     // from one row to the next
     int slices;            // column slices of a row, each the lanes of one row slot
     int vec_out;           // out / dout rows are 16-byte aligned
+    int scale_words;       // 1, 2 or 4: scales of a row's slice that are copied together
 };
 
 // Write-then-read tokens on a quantised bank.
