@@ -17,6 +17,12 @@
 // record in shared memory and warms the row in L2; a value column's thread does the same with v. And
 // behind the barrier that ends a token's writes its read rows and the next token's write rows are
 // requested together, without branches between the requests, so a token waits once, for L2.
+//
+// What bounds it: instructions. 512 streams of 64 and 64 rows of 128 columns take 4.6 us a token (3.1 TB/s
+// through L2, where the state of a chunk of tokens stays); a warp spends 1326 instructions on its 16 and 16
+// rows, at 0.55 a cycle and scheduler, 876 of them on the rows written: their 8-bit codes are unpacked for the
+// retrieval, for the scale and for the new codes, since the columns of four rows do not fit the registers.
+// Keeping them two rows at a time spills (4.8 us). So 8-bit rows halve the bytes of a bf16 bank, not its time.
 #include <algorithm>
 #include <climits>
 
@@ -60,8 +66,10 @@ __device__ __forceinline__ int reduce_rows(float* x, int lane) {
 
 // F: Int8 or Fp8. LR: lanes of a row slice (its columns: 16 * LR). NT: threads. RPT: rows a thread
 // holds. ITEMS: entries (W + R of them) that a thread prepares.
+// The registers are bounded for four blocks of 128 threads an SM, or two of 256: 512 streams of 64 rows take
+// 4.6 us a token with 128 registers, 12 with the 153 it would use, in two waves.
 template <typename F, int LR, int NT, int RPT, int ITEMS>
-__global__ void __launch_bounds__(NT, RPT == 8 ? 1 : 4) qdecode_kernel(const QDecodeArgs a) {
+__global__ void __launch_bounds__(NT, RPT == 8 ? 1 : NT == 256 ? 2 : 4) qdecode_kernel(const QDecodeArgs a) {
     static_assert(F::C == 16, "pieces of 16 columns");
     constexpr int COLS = 16 * LR, RS = NT / LR, WARPS = NT / 32, KEEP = 16 * LR / 32;
     static_assert(COLS <= NT, "a thread for every column");
@@ -290,12 +298,20 @@ Chosen with_items(int entries) {
     return {(const void*)qdecode_kernel<F, LR, NT, RPT, 512 / NT>, NT};
 }
 
+// Blocks that fit the GPU at once as two of 256 threads on each of 152 SMs.
+constexpr int64_t kFewBlocks = 304;
+
+// Threads and rows of each. Few blocks get 256 threads, since a token's chain of steps is then all the
+// time there is, and more blocks 128, whose warps spend fewer instructions on a token. us a token, 128
+// / 256 threads: 64 streams of 64 rows 3.00 / 2.51, 304 streams 3.37 / 3.08, 512 streams 4.59 / 5.91;
+// of 32 rows 2.19 / 1.81, 2.36 / 2.23, 2.99 / 4.12. Eight rows a thread lose even to that: 128 rows a
+// stream 5.28 / 3.80 for 64 streams and 10.9 / 9.5 for 512.
 template <typename F, int LR>
-Chosen choose(int W, int R) {
+Chosen choose(int W, int R, bool few) {
     constexpr int S = 128 / LR;  // row slots of 128 threads
-    if (W <= 2 * S) return with_items<F, LR, 128, 2>(W + R);
-    if (W <= 4 * S) return with_items<F, LR, 128, 4>(W + R);
-    if (W <= 8 * S) return with_items<F, LR, 128, 8>(W + R);
+    if (W <= 2 * S) return few ? with_items<F, LR, 256, 1>(W + R) : with_items<F, LR, 128, 2>(W + R);
+    if (W <= 4 * S) return few ? with_items<F, LR, 256, 2>(W + R) : with_items<F, LR, 128, 4>(W + R);
+    if (W <= 8 * S) return with_items<F, LR, 256, 4>(W + R);
     return with_items<F, LR, 256, 8>(W + R);
 }
 
@@ -309,8 +325,9 @@ int launch_qdecode(const QDecodeArgs& a0, int format, cudaStream_t stream) {
     a.slices = narrow ? 1 : (a.pieces + 7) / 8;
     const int64_t blocks = a.n_streams * a.slices;
     if (blocks > INT_MAX) return SDM_ECOUNT;
-    const Chosen c = format == SDM_INT8 ? (narrow ? choose<Int8, 4>(a.W, a.R) : choose<Int8, 8>(a.W, a.R))
-                                        : (narrow ? choose<Fp8, 4>(a.W, a.R) : choose<Fp8, 8>(a.W, a.R));
+    const bool few = blocks <= kFewBlocks;
+    const Chosen c = format == SDM_INT8 ? (narrow ? choose<Int8, 4>(a.W, a.R, few) : choose<Int8, 8>(a.W, a.R, few))
+                                        : (narrow ? choose<Fp8, 4>(a.W, a.R, few) : choose<Fp8, 8>(a.W, a.R, few));
     const size_t smem = (size_t)kRing * (a.W + a.R) * sizeof(Entry);
     void* args[] = {&a};
     return launch_pdl_raw(c.fn, dim3((unsigned)blocks), dim3((unsigned)c.threads), smem, stream, args);
