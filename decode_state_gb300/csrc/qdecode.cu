@@ -69,7 +69,7 @@ __device__ __forceinline__ int reduce_rows(float* x, int lane) {
 // The registers are bounded for four blocks of 128 threads an SM, or two of 256: 512 streams of 64 rows take
 // 4.6 us a token with 128 registers, 12 with the 153 it would use, in two waves.
 template <typename F, int LR, int NT, int RPT, int ITEMS>
-__global__ void __launch_bounds__(NT, RPT == 8 ? 1 : NT == 256 ? 2 : 4) qdecode_kernel(const QDecodeArgs a) {
+__global__ void __launch_bounds__(NT, NT == 512 ? 1 : NT == 256 ? 2 : 4) qdecode_kernel(const QDecodeArgs a) {
     static_assert(F::C == 16, "pieces of 16 columns");
     constexpr int COLS = 16 * LR, RS = NT / LR, WARPS = NT / 32, KEEP = 16 * LR / 32;
     static_assert(COLS <= NT, "a thread for every column");
@@ -294,8 +294,10 @@ struct Chosen {
 
 template <typename F, int LR, int NT, int RPT>
 Chosen with_items(int entries) {
-    if (entries <= NT) return {(const void*)qdecode_kernel<F, LR, NT, RPT, 1>, NT};
-    return {(const void*)qdecode_kernel<F, LR, NT, RPT, 512 / NT>, NT};
+    if constexpr (NT < 512) {  // of the 512 entries at most
+        if (entries > NT) return {(const void*)qdecode_kernel<F, LR, NT, RPT, 512 / NT>, NT};
+    }
+    return {(const void*)qdecode_kernel<F, LR, NT, RPT, 1>, NT};
 }
 
 // Blocks that fit the GPU at once as two of 256 threads on each of 152 SMs.
@@ -305,14 +307,16 @@ constexpr int64_t kFewBlocks = 304;
 // time there is, and more blocks 128, whose warps spend fewer instructions on a token. us a token, 128
 // / 256 threads: 64 streams of 64 rows 3.00 / 2.51, 304 streams 3.37 / 3.08, 512 streams 4.59 / 5.91;
 // of 32 rows 2.19 / 1.81, 2.36 / 2.23, 2.99 / 4.12. Eight rows a thread lose even to that: 128 rows a
-// stream 5.28 / 3.80 for 64 streams and 10.9 / 9.5 for 512.
+// stream 5.28 / 3.80 for 64 streams and 10.9 / 9.5 for 512; 256 rows on 256 / 512 threads 6.12 / 5.78 and 22.0 / 20.4.
 template <typename F, int LR>
 Chosen choose(int W, int R, bool few) {
     constexpr int S = 128 / LR;  // row slots of 128 threads
     if (W <= 2 * S) return few ? with_items<F, LR, 256, 1>(W + R) : with_items<F, LR, 128, 2>(W + R);
     if (W <= 4 * S) return few ? with_items<F, LR, 256, 2>(W + R) : with_items<F, LR, 128, 4>(W + R);
-    if (W <= 8 * S) return with_items<F, LR, 256, 4>(W + R);
-    return with_items<F, LR, 256, 8>(W + R);
+    if constexpr (LR == 8) {  // the 256 rows of a token at most fit 256 threads of 4 lanes a row
+        if (W > 8 * S) return with_items<F, LR, 512, 4>(W + R);
+    }
+    return with_items<F, LR, 256, 4>(W + R);
 }
 
 }  // namespace
