@@ -559,8 +559,11 @@ __device__ __forceinline__ float block_reduce(float x, bool sum, float* tmp, int
 }
 
 // PLAIN: a softmax without bias and groups, whose ranks are the logits.
+// The steps of a block wait for one another, so blocks are many: the registers are bounded for 12 of 128
+// threads, 5 of 256, or 3 of 512 (16384 rows of 1500, k = 8: 102 us with 4 blocks as the bound, 54 with 12; 2048 of
+// 8000 33 with 3, 26 with 5). What is left is latency and instructions, of the candidates' ranking by counting most.
 template <int NT, bool PLAIN, typename L>
-__global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_block_kernel(const RouteArgs a, int staged) {
+__global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_block_kernel(const RouteArgs a, int staged) {
     constexpr int WARPS = NT / 32;
     extern __shared__ __align__(16) float staging[];  // [n + 4] when staged
     __shared__ __align__(16) int hist[kBins];
@@ -607,7 +610,14 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 3 : 4) route_b
 #pragma unroll
             for (int u = 0; u < 4; ++u) piece(j + u * NT * V, v[u]);
         }
-        for (; j < end; j += NT * V) piece(j, __ldg(reinterpret_cast<const uint4*>(row + j)));
+        {  // and the up to four that are left
+            uint4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = load16_if(row + j + u * NT * V, j + u * NT * V < end);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (j + u * NT * V < end) piece(j + u * NT * V, v[u]);
+        }
         // the few before the first boundary and behind the last one
         const int rest = head + n - end;
         if (tid < rest) {
@@ -1173,12 +1183,15 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
         return launch_pdl_raw(fn, dim3((unsigned)blocks), dim3(kWarpThreads), smem, stream, args);
     }
     if (a.tokens > INT_MAX) return SDM_ECOUNT;
-    int staged = (size_t)a.n * 4 <= kStagedBytes ? 1 : 0;
-    const size_t smem = staged ? (size_t)(a.n + 4) * 4 : 0;
-    // threads for 32 to 64 ranks each; blocks of 256 with 64 KB of ranks fit three times on an SM, so that
-    // one loads its row while others choose (1024 rows of 16384: two blocks of 512 threads 43 us)
-    const int threads = a.n > 16384 ? 512 : a.n > 4096 ? 256 : 128;
+    // Ranks that are the logits themselves are read again, out of L2, when a row of them is long, since the
+    // shared memory to keep them is room for blocks: 1024 rows of 16384 bf16 logits, k = 64, 30 us and staged 34, 512
+    // of 32768 26 and 36. Sigmoid ranks would be computed again: 68 us and staged 43.
     const bool plain = a.score == SDM_SOFTMAX && a.bias == nullptr && !grouped;
+    int staged = (size_t)a.n * 4 <= kStagedBytes && !(plain && a.n > 8192) ? 1 : 0;
+    const size_t smem = staged ? (size_t)(a.n + 4) * 4 : 0;
+    // Threads for 16 to 64 ranks each. 1024 rows of 16384, k = 64: 128 threads 44 us, 256 34, 512 34; 4096 of 4096
+    // 55, 59, 75; 16384 of 1500 161, 201, 246; 256 of 65536 53, 33, 25.
+    const int threads = a.n > 16384 ? 512 : a.n > 4096 ? 256 : 128;
     const void* fn = a.logit_bf16 ? block_kernel<uint16_t>(threads, plain) : block_kernel<float>(threads, plain);
     // the limit without a request counts the kernel's static arrays (10 KB) too
     const int rc = allow_smem(fn, smem > 32 * 1024 ? std::max(smem, (size_t)48 * 1024 + 16) : smem);
