@@ -252,8 +252,12 @@ __device__ __forceinline__ float rough_sigmoid(float x) {
 // The ranks of a sigmoid are first computed roughly, with a margin, at a third of the instructions;
 // what is near enough to matter is computed exactly: the candidates, and all entries where two groups
 // are too close to call.
+//
+// Bound by instructions and the latencies between them: 65536 rows of 256 by sigmoid, bias and groups, k = 8, take
+// some 1000 instructions for two tokens, 0.6 a cycle and scheduler, at a tenth of the DRAM's rate. So the registers are bounded for
+// 4 to 6 blocks an SM: 52 -> 45 us; 32768 rows of 1000 float32, k = 64, 228 -> 148 (4 blocks; 6: 163).
 template <int LANES, int E, int V, bool SOFTMAX, typename L>
-__global__ void __launch_bounds__(kWarpThreads) route_warp_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kWarpThreads, E == 32 ? 4 : E == 16 ? 5 : 6) route_warp_kernel(const RouteArgs a) {
     constexpr int TEAMS = kWarpThreads / LANES, Q = V == 0 ? 3 : 2, CANDS = Q * LANES;  // Q: candidates of a lane at most
     extern __shared__ float staged[];  // groups that are no whole lanes: every team's group values [n] and scores [n_groups]
     __shared__ uint16_t found[TEAMS][CANDS];
@@ -1157,7 +1161,7 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     // stay: the k-th largest of them is then a close bound. Half a warp and two maxima a lane for 65536 rows
     // of 256 with 8 of 4 groups of 32: 48 us, a whole one and one each: 62; without two k of them (one
     // maximum each for half a warp, 8 in all) 76. Where no such choice is left, and for more than 32 entries, a
-    // bound by halving; 32768 float32 rows of 200, 500, 1000 with k = 64: 110, 123, 228 us, the block kernel 273, 211,
+    // bound by halving; 32768 float32 rows of 200, 500, 1000 with k = 64: 104, 113, 148 us, the block kernel 273, 211,
     // 266; of 500 with k = 8 the maxima take 44 us, halving 88.
     const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups;
     const int live = grouped ? a.n / a.n_groups * a.top_groups : a.n;
@@ -1168,7 +1172,7 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
             lanes = 16, e = e16, v = 2;
         else if (2 * a.k <= live / e32)
             lanes = 32, e = e32, v = 1;
-        else if (a.k <= 32 && (3 * a.k <= 2 * (live / (e32 / 2)) || a.n <= 256))
+        else if (a.k <= 32 && (a.n <= 256 ? a.k <= live / (e32 / 2) : 3 * a.k <= 2 * (live / (e32 / 2))))
             lanes = 32, e = e32, v = 2;
         else
             lanes = 32, e = e32, v = 0;
