@@ -918,12 +918,20 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_
 
 // ---------------------------------------------------------------- the gradient
 
+// Blocks an SM that the registers are bounded for: a token's steps wait for memory and for one another, so
+// tokens have to be many, as long as their rows fit the registers. Softmax without renormalisation, k = 8:
+// 65536 rows of 256 float32 42 us with 12 blocks, 52 with 8, 54 unbounded; 32768 of 500 33, 36, 42; 16384 of 1000 40, 29, 38
+// (it spills with 12); 2048 of 8000 33 with 4 blocks, 45 unbounded; 1024 of 16384 39 with 2, 53 unbounded.
+constexpr int backward_blocks(int team, int e) {
+    return team == 32 ? (e <= 16 ? 12 : 8) : team == 256 ? (e <= 24 ? 6 : 4) : 2;
+}
+
 // A team of TEAM threads (a warp, or a block) for each token. Only a softmax that is not
 // renormalised has gradients outside the chosen entries: its row is read once, E logits a thread, and
 // its exponentials stay in registers until the gradients are written (E 0: rows too long for that are
 // read three times). All others get zeros there. The chosen entries are written over that.
 template <int TEAM, int E, typename L>
-__global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, TEAM == 256 && E <= 24 ? 6 : 1) route_backward_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM, E)) route_backward_kernel(const RouteArgs a) {
     constexpr int NT = TEAM == 32 ? 128 : TEAM, TEAMS = NT / TEAM, WARPS = TEAM / 32, U = 4 / sizeof(L);
     __shared__ float largest[NT / 32], sums[NT / 32];
     grid_dependency_wait();
