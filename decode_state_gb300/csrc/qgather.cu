@@ -8,7 +8,8 @@
 // bytes each, so a warp reads 32 / LR rows at once. A block of four warps shares a token's entries, rows
 // go straight to registers, and the sums are joined through shared memory; with few tokens the machine
 // is idle otherwise, and a ring has nothing to run ahead of. The rule between them looks at the sizes
-// only, so that results do not depend on the GPU.
+// only, so that results do not depend on the GPU. Bound by latency: 256 tokens with 64 int8 rows of 128
+// columns take 2.6 us from a graph, a launch and two loads that wait for one another, the index and the row.
 #include <algorithm>
 #include <climits>
 
