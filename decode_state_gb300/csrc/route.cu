@@ -922,9 +922,9 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_
 // tokens have to be many, as long as their rows fit the registers. Softmax without renormalisation, k = 8:
 // 65536 rows of 256 float32 42 us with 12 blocks, 52 with 8, 54 unbounded; 32768 of 500 33, 36, 42; 16384 of 1000 40, 29, 38
 // (it spills with 12); 2048 of 8000 33 with 4 blocks, 45 unbounded; 1024 of 16384 39 with 2, 53 unbounded.
-// Teams of 128 threads for rows up to 4096: 8192 rows of 1500 30 us, on 256 threads 45; 4096 of 4096 31 and 37.
+// Teams of 128 threads for rows up to 6144: 8192 rows of 1500 30 us, on 256 threads 45; 4097 of 4099 34 and 41.
 constexpr int backward_blocks(int team, int e) {
-    return team <= 128 ? (e <= 16 ? 12 : 8) : team == 256 ? (e <= 24 ? 6 : 4) : 2;
+    return team <= 128 ? (e <= 16 ? 12 : 8) : team == 256 ? (e == 0 ? 6 : 4) : 2;
 }
 
 // A team of TEAM threads (a warp, or a block) for each token. Only a softmax that is not
@@ -1128,8 +1128,8 @@ Team backward_kernel(int n, bool dense) {
     if (!dense) return {(const void*)route_backward_kernel<256, 0, L>, 256, 1};
     if (n <= 2048) return {(const void*)route_backward_kernel<128, 16, L>, 128, 1};
     if (n <= 4096) return {(const void*)route_backward_kernel<128, 32, L>, 128, 1};
-    if (n <= 5120) return {(const void*)route_backward_kernel<256, 20, L>, 256, 1};
-    if (n <= 6144) return {(const void*)route_backward_kernel<256, 24, L>, 256, 1};
+    if (n <= 5120) return {(const void*)route_backward_kernel<128, 40, L>, 128, 1};
+    if (n <= 6144) return {(const void*)route_backward_kernel<128, 48, L>, 128, 1};
     if (n <= 8192) return {(const void*)route_backward_kernel<256, 32, L>, 256, 1};
     if (n <= 16384) return {(const void*)route_backward_kernel<512, 32, L>, 512, 1};
     return {(const void*)route_backward_kernel<512, 0, L>, 512, 1};
