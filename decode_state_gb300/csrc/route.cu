@@ -1169,10 +1169,9 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     RouteArgs a = a0;
     // The warp kernel, with as few lanes and maxima as leave twice k maxima among the entries whose groups
     // stay: the k-th largest of them is then a close bound. Half a warp and two maxima a lane for 65536 rows
-    // of 256 with 8 of 4 groups of 32: 48 us, a whole one and one each: 62; without two k of them (one
-    // maximum each for half a warp, 8 in all) 76. Where no such choice is left, and for more than 32 entries, a
-    // bound by halving; 32768 float32 rows of 200, 500, 1000 with k = 64: 104, 113, 148 us, the block kernel 273, 211,
-    // 266; of 500 with k = 8 the maxima take 44 us, halving 88.
+    // of 256, k = 8, 4 of 8 groups of 32: 46 us, a whole one and one each: 57. Where no such choice is left, and
+    // for more than 32 entries, a bound by halving: 32768 float32 rows of 200, 500, 1000 with k = 64 take 106, 114,
+    // 149 us, the block kernel 189, 151, 174; of 500 with k = 8 the maxima take 37 us, halving 77.
     const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups;
     const int live = grouped ? a.n / a.n_groups * a.top_groups : a.n;
     if (a.n <= 1024 && a.k <= 64) {
@@ -1203,8 +1202,8 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     const bool plain = a.score == SDM_SOFTMAX && a.bias == nullptr && !grouped;
     int staged = (size_t)a.n * 4 <= kStagedBytes && !(plain && a.n > 8192) ? 1 : 0;
     const size_t smem = staged ? (size_t)(a.n + 4) * 4 : 0;
-    // Threads for 16 to 64 ranks each. 1024 rows of 16384, k = 64: 128 threads 44 us, 256 34, 512 34; 4096 of 4096
-    // 55, 59, 75; 16384 of 1500 161, 201, 246; 256 of 65536 53, 33, 25.
+    // Threads for 16 to 64 ranks each. 16384 rows of 1500, k = 64: 128 threads 101 us, 256 142, 512 201; 4096 of 4096
+    // 45, 49, 62; 1024 of 16384 30, 31, 32 (by sigmoid 65, 45, 42); 256 of 65536 53, 33, 24.
     const int threads = a.n > 16384 ? 512 : a.n > 4096 ? 256 : 128;
     const void* fn = a.logit_bf16 ? block_kernel<uint16_t>(threads, plain) : block_kernel<float>(threads, plain);
     // the limit without a request counts the kernel's static arrays (10 KB) too
