@@ -578,7 +578,8 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_
     static_assert(2 * kCandidates + 2 * kMaxK <= kBins, "they fit the histogram");
     __shared__ float scores[kMaxGroups];
     __shared__ uint32_t stays[kMaxGroups / 32];
-    __shared__ float tmp[2 * WARPS];
+    __shared__ float tmp[WARPS];
+    __shared__ float ends[2 * WARPS];  // not in tmp: no barrier is behind the last reads of a sum there
     __shared__ int counts[WARPS];
     __shared__ int found_bin, found_above, n_cand;
     grid_dependency_wait();
@@ -804,13 +805,13 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_
         high = fmaxf(high, __shfl_xor_sync(kAll, high, o));
     }
     if (lane == 0) {
-        tmp[warp] = low;
-        tmp[WARPS + warp] = high;
+        ends[warp] = low;
+        ends[WARPS + warp] = high;
     }
     clear_bins(kFew);
     for (int i = 0; i < WARPS; ++i) {
-        low = fminf(low, tmp[i]);
-        high = fmaxf(high, tmp[WARPS + i]);
+        low = fminf(low, ends[i]);
+        high = fmaxf(high, ends[WARPS + i]);
     }
     const float width = (high - low) * (1.0f / kFew);
     const bool spread = width > 0x1p-100f && width < 0x1p100f;
