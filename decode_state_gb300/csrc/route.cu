@@ -118,7 +118,7 @@ __device__ __forceinline__ bool group_stays(const float* scores, int groups, int
     return better < top;
 }
 
-// The float of an ordered integer above kMasked; NaN beyond +inf.
+// The float of an ordered integer from that of -inf to that of +inf; a NaN outside them.
 __device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); }
 
 // A candidate as 64 bits that order first by rank, then by the lower index.
@@ -767,14 +767,14 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_
         __syncthreads();
     };
     constexpr int kFew = 2 * NT;  // bins for the threads' maxima
-    // candidates: the live entries with a key from `lowest` on; those that fit are kept
-    const auto collect = [&](uint32_t lowest) {
+    // candidates: the live entries with a rank from `bound` on, or above it; those that fit are kept
+    // (the key behind that of +inf is no rank's: what lies above a rank is asked of the rank itself)
+    const auto collect = [&](float bound, bool above) {
         if (tid == 0) n_cand = 0;
         __syncthreads();
-        // keys and ranks have the same order, and -inf is no live entry's rank
-        const float bound = fmaxf(unordered(lowest), -3.402823466e38f);
+        bound = fmaxf(bound, -3.402823466e38f);  // -inf is no live entry's rank
         const auto keep = [&](float r, int j) {
-            if (r >= bound) {
+            if (above ? r > bound : r >= bound) {
                 const int c = atomicAdd(&n_cand, 1);
                 if (c < kCandidates) cand[c] = candidate(ordered(r), j);
             }
@@ -823,7 +823,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_
     int C = 0;
     if (found_bin >= 0) {
         // one bin lower, for the roundings
-        collect(ordered(spread && found_bin > 0 ? fmaf((float)(found_bin - 1), width, low) : low));
+        collect(spread && found_bin > 0 ? fmaf((float)(found_bin - 1), width, low) : low, false);
         C = n_cand;
         done = C <= kCandidates;
     }
@@ -846,7 +846,6 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_
             find_bin(need, std::integral_constant<int, kBins>{});
             if (found_bin < 0) {  // level 0 only: all live entries are taken
                 few = true;
-                lowest = kMasked + 1;
                 break;
             }
             above += found_above;
@@ -859,8 +858,8 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_
         }
         // only what lies above the last rank when too many share it
         ties = !few && exact && above + inside > kCandidates;
-        collect(ties ? lowest + 1 : lowest);
-        C = n_cand;
+        collect(few ? minus_inf() : unordered(lowest), ties);
+        C = min(n_cand, kCandidates);
     }
     // rank the candidates by counting, four threads for each
     for (int c0 = 0; c0 < C; c0 += NT / 4) {
