@@ -521,14 +521,15 @@ __global__ void __launch_bounds__(kWarpThreads, E == 32 ? 4 : E == 16 ? 5 : 6) r
         if (mine[q]) chosen += score[q];
     }
     if (a.renorm) total = lanes_sum<LANES>(chosen);
-    const float factor = (softmax || a.renorm) && total > 0.0f ? __fdividef(a.scale, total) : a.scale;
+    // a share of the total first: scale / total overflows where all that are chosen have tiny scores
+    const bool shares = (softmax || a.renorm) && total > 0.0f;
     if (!there) return;
     const int64_t to = t * k;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         if (mine[q]) {
             put_index(a, t, rank[q], j[q]);
-            a.w[to + rank[q]] = score[q] * factor;
+            a.w[to + rank[q]] = (shares ? __fdiv_rn(score[q], total) : score[q]) * a.scale;
         }
     }
     if (count < k) {  // fill up with masked entries, in index order
