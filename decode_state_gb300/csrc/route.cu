@@ -1085,6 +1085,9 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
     }
     // the chosen entries are written again, over what is there, by the team's first warp
     float all = 1.0f, dot = 0.0f;
+    const auto score_of = [&](float y) { return softmax ? exp_below(y, m) : sigmoid(y); };
+    // shares of the sum, not its reciprocal, which overflows where all that are chosen have tiny scores
+    const auto share_of = [&](float s) { return all > 0.0f ? __fdiv_rn(s, all) : 0.0f; };
     if (a.renorm && tid < 32) {
         // scores, or exp(x - m) for a softmax, which is as good: the factor between them cancels
         if (softmax) {
@@ -1092,13 +1095,10 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
             m = warp_max(m);
         }
         all = 0.0f;
-        each_chosen([&](int, float y, float dw) {
-            const float s = softmax ? exp_below(y, m) : sigmoid(y);
-            all += s;
-            dot += dw * s;
-        });
+        each_chosen([&](int, float y, float) { all += score_of(y); });
         all = warp_sum(all);
-        dot = all > 0.0f ? __fdiv_rn(warp_sum(dot), all) : 0.0f;
+        each_chosen([&](int, float y, float dw) { dot += dw * share_of(score_of(y)); });
+        dot = warp_sum(dot);
     }
     sync();
     if (tid >= 32) return;
@@ -1107,10 +1107,13 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
             atomicOr(&g_route_status, SDM_DEV_BAD_INDEX);
             return;
         }
-        float s = softmax ? exp_below(y, m) : sigmoid(y);
-        if (dense) s = total > 0.0f ? __fdiv_rn(s, total) : 0.0f;
-        const float u = !a.renorm ? dw : all > 0.0f ? __fdiv_rn(dw - dot, all) : 0.0f;
-        out[j] = from_f32<L>(!softmax ? u * s * (1.0f - s) : dense ? s * (u - mean) : s * u);
+        const float s = score_of(y);
+        float d;
+        if (dense)
+            d = total > 0.0f ? __fdiv_rn(s, total) * (dw - mean) : 0.0f;
+        else
+            d = (a.renorm ? (dw - dot) * share_of(s) : dw * s) * (softmax ? 1.0f : 1.0f - s);
+        out[j] = from_f32<L>(d);
     });
 }
 

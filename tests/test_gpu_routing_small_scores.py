@@ -1,4 +1,4 @@
-"""Renormalised weights where all chosen scores are tiny: their sum is subnormal or so
+"""Renormalised weights, and their gradient, where all chosen scores are tiny: their sum is subnormal or so
 small that its reciprocal overflows, while the weights themselves are ordinary numbers.
 
 Tolerance: a float32 score s has an error of half the least float (2^-150) more than its 20 eps (exp of an
@@ -41,6 +41,19 @@ def test_sigmoid_weights(n, k, scale):
     _, _, w, s = _sigmoid_rows(n, k, scale, torch.Generator().manual_seed(n + k))
     want = s / s.sum(1, keepdims=True) * scale
     assert (np.abs(w.cpu().double().numpy() - want) <= _tolerance(s, want, k)).all()
+
+
+@pytest.mark.parametrize("n,k", SIZES)
+@pytest.mark.parametrize("scale", (1.0, 2.5, 100.0))
+def test_sigmoid_gradient(n, k, scale):
+    gen = torch.Generator().manual_seed(n + k)
+    x, idx, _, s = _sigmoid_rows(n, k, scale, gen)
+    at, xn = idx.cpu().numpy(), x.numpy()
+    dw = torch.randn((4, k), generator=gen)
+    d = routing.route_backward(x.cuda(), idx, dw.cuda(), score="sigmoid", scale=scale).cpu().double().numpy()
+    grad, size = ref.route_backward(xn, at, dw.numpy(), "sigmoid", True, scale)
+    rel = (2 * (20 * EPS + 2.0 ** -150 / s) + (8 + k) * EPS).max(1, keepdims=True)
+    assert (np.abs(d - grad) <= 2 * rel * size).all()
 
 
 @pytest.mark.parametrize("n,k", SIZES)
