@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(kWarpThreads, E == 32 ? 4 : E == 16 ? 5 : 6) r
         float mine = judge();
         int better = 0, near = 0;  // groups that are surely better; and those that may be
         if (rough) {
-            const float d = mine == minus_inf() ? 0.0f : margin(mine), high = mine + d, low = mine - d;
+            // an infinite score (a bias) is exact: no margin, so that equal ones are near
+            const float d = fabsf(mine) <= 3.402823466e38f ? margin(mine) : 0.0f, high = mine + d, low = mine - d;
             for (int q = 0, from = 0; q < a.n_groups; ++q, from += group_lanes) {
                 const float other = __shfl_sync(kAll, mine, from, LANES);
                 better += other > high;
