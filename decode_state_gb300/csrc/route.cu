@@ -974,15 +974,19 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
             for (int w = 0; w < WARPS; ++w) own += sums[w] * exp_below(largest[w], m);
         }
     };
-    // chosen entry i: its column (-1: outside the row), its logit and the gradient of its weight
+    // chosen entry i: its column, its logit and the gradient of its weight. A weight that is 0 whatever the
+    // logits are has no gradient, and its dw, which may be anything, takes no part: kNone for a masked entry,
+    // kOutside for an index outside the row.
+    constexpr int kNone = -2, kOutside = -1;
     const auto chosen = [&](int i, float& x, float& dw) {
         const int64_t e = t * k + i;
+        const float given = __ldg(a.dw + e) * a.scale;  // on its way beside the index
         const int64_t j = (a.idx64 ? __ldg(static_cast<const int64_t*>(a.idx) + e) : __ldg(static_cast<const int32_t*>(a.idx) + e)) -
                           (a.base == nullptr ? 0 : a.idx64 ? __ldg(static_cast<const int64_t*>(a.base) + t) : __ldg(static_cast<const int32_t*>(a.base) + t));
         const bool in = j >= 0 && j < n;
         x = in ? to_f32(__ldg(row + j)) : minus_inf();
-        dw = __ldg(a.dw + e) * a.scale;
-        return in ? (int)j : -1;
+        dw = masked(x) ? 0.0f : given;
+        return !in ? kOutside : masked(x) ? kNone : (int)j;
     };
     const auto get = [&](int j, float* x) {  // U logits from j on; masked ones behind the end
         if (U == 2 && words && j + U <= n) {
@@ -1011,7 +1015,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
     float kept_x[KEPT], kept_dw[KEPT];
 #pragma unroll
     for (int q = 0; q < KEPT; ++q) {
-        kept_j[q] = -1;
+        kept_j[q] = kNone;
         kept_x[q] = minus_inf();
         kept_dw[q] = 0.0f;
         if (lane + 32 * q < k && (dense || tid < 32)) kept_j[q] = chosen(lane + 32 * q, kept_x[q], kept_dw[q]);
@@ -1104,8 +1108,8 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
     sync();
     if (tid >= 32) return;
     each_chosen([&](int j, float y, float dw) {
-        if (j < 0) {
-            atomicOr(&g_route_status, SDM_DEV_BAD_INDEX);
+        if (j < 0) {  // what is there stays: 0, or in a dense row that of an entry not chosen
+            if (j == kOutside) atomicOr(&g_route_status, SDM_DEV_BAD_INDEX);
             return;
         }
         const float s = score_of(y);
