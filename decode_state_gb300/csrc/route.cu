@@ -975,8 +975,8 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
         }
     };
     // chosen entry i: its column, its logit and the gradient of its weight. A weight that is 0 whatever the
-    // logits are has no gradient, and its dw, which may be anything, takes no part: kNone for a masked entry,
-    // kOutside for an index outside the row.
+    // logits are has no gradient, and its dw, which may be anything, takes no part: kNone for a masked entry
+    // and, with the forward's weights, for one of weight 0; kOutside for an index outside the row.
     constexpr int kNone = -2, kOutside = -1;
     const auto chosen = [&](int i, float& x, float& dw) {
         const int64_t e = t * k + i;
@@ -984,7 +984,8 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
         const int64_t j = (a.idx64 ? __ldg(static_cast<const int64_t*>(a.idx) + e) : __ldg(static_cast<const int32_t*>(a.idx) + e)) -
                           (a.base == nullptr ? 0 : a.idx64 ? __ldg(static_cast<const int64_t*>(a.base) + t) : __ldg(static_cast<const int32_t*>(a.base) + t));
         const bool in = j >= 0 && j < n;
-        x = in ? to_f32(__ldg(row + j)) : minus_inf();
+        const bool filled = a.w != nullptr && __ldg(a.w + e) == 0.0f;
+        x = in && !filled ? to_f32(__ldg(row + j)) : minus_inf();
         dw = masked(x) ? 0.0f : given;
         return !in ? kOutside : masked(x) ? kNone : (int)j;
     };

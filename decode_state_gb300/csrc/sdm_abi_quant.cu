@@ -282,14 +282,14 @@ int sdm_route(const void* logits, int64_t row_stride, int logit_dtype, const flo
     return sdm::launch_route(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
-int sdm_route_backward(const void* logits, int64_t row_stride, int logit_dtype, const void* base, const void* idx,
-                       const float* dw, void* dlogits, int64_t dlogits_stride, int64_t tokens, int n, int k, int score,
-                       float scale, unsigned flags, int idx_dtype, sdm_stream_t stream) {
+int sdm_route_backward_ex(const void* logits, int64_t row_stride, int logit_dtype, const void* base, const void* idx,
+                          const float* w, const float* dw, void* dlogits, int64_t dlogits_stride, int64_t tokens, int n,
+                          int k, int score, float scale, unsigned flags, int idx_dtype, sdm_stream_t stream) {
     const int rc = check_route(logits, row_stride, logit_dtype, base, idx, tokens, n, k, score, flags, idx_dtype);
     if (rc != SDM_OK || tokens == 0) return rc;
     if (!dw || !dlogits) return SDM_ENULL;
     if (dlogits_stride < n) return SDM_ESTRIDE;
-    if (!aligned(dw, 4) || !aligned(dlogits, float_size(logit_dtype))) return SDM_EALIGN;
+    if (!aligned(w, 4) || !aligned(dw, 4) || !aligned(dlogits, float_size(logit_dtype))) return SDM_EALIGN;
     sdm::RouteArgs a{};
     a.logits = logits;
     a.row_stride = row_stride;
@@ -303,10 +303,18 @@ int sdm_route_backward(const void* logits, int64_t row_stride, int logit_dtype, 
     a.renorm = (flags & SDM_RENORM) != 0;
     a.idx64 = idx_dtype == SDM_I64;
     a.logit_bf16 = logit_dtype == SDM_BF16;
+    a.w = const_cast<float*>(w);
     a.dw = dw;
     a.dlogits = dlogits;
     a.dlogits_stride = dlogits_stride;
     return sdm::launch_route_backward(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int sdm_route_backward(const void* logits, int64_t row_stride, int logit_dtype, const void* base, const void* idx,
+                       const float* dw, void* dlogits, int64_t dlogits_stride, int64_t tokens, int n, int k, int score,
+                       float scale, unsigned flags, int idx_dtype, sdm_stream_t stream) {
+    return sdm_route_backward_ex(logits, row_stride, logit_dtype, base, idx, nullptr, dw, dlogits, dlogits_stride, tokens,
+                                 n, k, score, scale, flags, idx_dtype, stream);
 }
 
 }  // extern "C"

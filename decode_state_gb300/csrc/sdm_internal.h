@@ -117,7 +117,7 @@ struct RouteArgs {
     int n, k, score, n_groups, top_groups, group_top;
     float scale;
     int renorm, idx64, logit_bf16;
-    // the gradient's: idx is read
+    // the gradient's: idx and w (nullptr: all are taken as chosen) are read
     const float* dw;
     void* dlogits;
     int64_t dlogits_stride;

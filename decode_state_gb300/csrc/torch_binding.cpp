@@ -453,11 +453,11 @@ PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// route_backward(logits, idx, dw, score, renorm, scale, base or None, out or None, stream)
+// route_backward(logits, idx, dw, score, renorm, scale, base or None, w or None, out or None, stream)
 PyObject* route_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     const Args a{args, n};
-    expect(a, 9, "route_backward");
+    expect(a, 10, "route_backward");
     const Logits x(a.tensor(0, "logits"), "logits");
     const at::Device dev = x.t.device();
     const Tensor &idx = a.tensor(1, "idx"), &dw = a.tensor(2, "dw");
@@ -467,17 +467,22 @@ PyObject* route_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     need(idx, "idx", dev, {x.tokens, k});
     need_f32(dw, "dw", dev, {x.tokens, k});
     const void* base = base_of(a, 6, x.tokens, idx.scalar_type(), dev);
-    Launch l(dev, a.a[8]);
+    const float* w = nullptr;
+    if (!a.none(7)) {
+        need_f32(a.tensor(7, "w"), "w", dev, {x.tokens, k});
+        w = static_cast<const float*>(a.tensor(7, "w").data_ptr());
+    }
+    Launch l(dev, a.a[9]);
     Tensor made;
-    if (a.none(7)) made = empty(x.t.sizes(), x.t.scalar_type(), dev);
-    const Logits out(a.none(7) ? made : a.tensor(7, "out"), "out");
+    if (a.none(8)) made = empty(x.t.sizes(), x.t.scalar_type(), dev);
+    const Logits out(a.none(8) ? made : a.tensor(8, "out"), "out");
     TORCH_CHECK_TYPE(out.type == x.type && out.t.device() == dev, "out must have the dtype and the device of the logits");
     TORCH_CHECK_VALUE(out.t.sizes() == x.t.sizes(), "out has shape ", out.t.sizes(), ", expected ", x.t.sizes());
-    check("sdm_route_backward",
-          sdm_route_backward(x.t.data_ptr(), x.stride, x.type, base, idx.data_ptr(), static_cast<const float*>(dw.data_ptr()),
-                             out.t.data_ptr(), out.stride, x.tokens, static_cast<int>(x.n), k > 256 ? 257 : static_cast<int>(k),
-                             a.small(3), a.real(5), a.truth(4) ? SDM_RENORM : 0u, it, l.stream));
-    return give(a.a[7], made);
+    check("sdm_route_backward_ex",
+          sdm_route_backward_ex(x.t.data_ptr(), x.stride, x.type, base, idx.data_ptr(), w, static_cast<const float*>(dw.data_ptr()),
+                                out.t.data_ptr(), out.stride, x.tokens, static_cast<int>(x.n), k > 256 ? 257 : static_cast<int>(k),
+                                a.small(3), a.real(5), a.truth(4) ? SDM_RENORM : 0u, it, l.stream));
+    return give(a.a[8], made);
     END_HANDLE_TH_ERRORS
 }
 

@@ -36,8 +36,12 @@ def route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias=None, gr
 
 
 def route_backward(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor, *, score: str = "softmax",
-                   renorm: bool = True, scale: float = 1.0, base=None, out=None, stream=None) -> torch.Tensor:
+                   renorm: bool = True, scale: float = 1.0, base=None, w=None, out=None, stream=None) -> torch.Tensor:
     """Gradient of the logits from the gradient ``dw`` [tokens, k] (float32) of the weights, for the
     ``idx`` that ``route`` returned with the same ``score``, ``renorm``, ``scale`` and ``base``
-    (sdm_route_backward). Returns [tokens, n] in the dtype of the logits."""
-    return binding().route_backward(logits, idx, dw, _score(score), renorm, scale, base, out, stream)
+    (sdm_route_backward_ex). Returns [tokens, n] in the dtype of the logits.
+
+    ``w``, the weights that ``route`` returned, tells which entries only filled up: those of weight 0
+    have no gradient. It is needed wherever ``groups`` or a ``bias`` of -inf may leave fewer than k
+    entries; without it every entry with a live logit is taken as chosen."""
+    return binding().route_backward(logits, idx, dw, _score(score), renorm, scale, base, w, out, stream)

@@ -26,7 +26,7 @@ ENTRY_POINTS = ("sdm_decode_step", "sdm_decode_step_ex", "sdm_decode_seq", "sdm_
                 "sdm_gather_kpos",
                 "sdm_gather_plan_init", "sdm_gather_plan_launch", "sdm_gather_plan_launch_ex", "sdm_gather_plan_walk",
                 "sdm_quant_row_bytes", "sdm_quantize_rows", "sdm_dequantize_rows", "sdm_qgather", "sdm_gather_dw",
-                "sdm_qdecode_step", "sdm_qdecode_seq", "sdm_route", "sdm_route_backward",
+                "sdm_qdecode_step", "sdm_qdecode_seq", "sdm_route", "sdm_route_backward", "sdm_route_backward_ex",
                 "sdm_status_string",
                 "sdm_device_status", "sdm_version")
 SDM_INPUTS_READY = 1  # flag of the _ex calls: the inputs predate the kernel launched just before
@@ -105,6 +105,8 @@ def library() -> ctypes.CDLL:
                                       u32, i32, vp]
             lib.sdm_route_backward.argtypes = [vp, i64, i32, vp, vp, vp, vp, i64, i64, i32, i32, i32, ctypes.c_float,
                                                u32, i32, vp]
+            lib.sdm_route_backward_ex.argtypes = [vp, i64, i32, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, ctypes.c_float,
+                                                  u32, i32, vp]
             for name in ENTRY_POINTS[ENTRY_POINTS.index("sdm_quant_row_bytes"):ENTRY_POINTS.index("sdm_status_string")]:
                 getattr(lib, name).restype = i32
             lib.sdm_status_string.argtypes = [i32]

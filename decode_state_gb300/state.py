@@ -136,9 +136,13 @@ class RoutedLayerState:
         out, = quant.gather(self.memory, [(idx, w)])
         return out, idx, w
 
-    def read_backward(self, q_logits: torch.Tensor, idx: torch.Tensor, dout: torch.Tensor) -> torch.Tensor:
-        """Gradient of the logits of ``read`` from that of its readings (float32 [S, hd]); ``idx`` as it
-        returned them. The choice itself has no gradient, as in any top-k router."""
+    def read_backward(self, q_logits: torch.Tensor, idx: torch.Tensor, dout: torch.Tensor, w=None) -> torch.Tensor:
+        """Gradient of the logits of ``read`` from that of its readings (float32 [S, hd]); ``idx`` and ``w`` as
+        it returned them. The choice itself has no gradient, as in any top-k router. Where groups or a bias can
+        leave too few slots, the weights tell which only filled up; they are computed again when not given."""
+        groups = self.router.get("groups", 1)
+        if w is None and (self.router.get("bias") is not None or (self.router.get("top_groups") or groups) < groups):
+            _, w = self.choose(q_logits, self.reads)
         dw, = quant.gather_dw(self.memory, [(idx, dout)])
         given = {n: self.router[n] for n in ("score", "renorm", "scale") if n in self.router}
-        return routing.route_backward(q_logits, idx, dw, base=self._first, **given)
+        return routing.route_backward(q_logits, idx, dw, base=self._first, w=w, **given)

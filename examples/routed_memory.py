@@ -46,10 +46,10 @@ def main(streams: int = 64, slots: int = 512, hd: int = 128, prompt: int = 32, t
     losses = []
     for _ in range(rounds):
         logits = features @ router
-        out, idx, _ = state.read(logits)
+        out, idx, w = state.read(logits)
         err = out - target
         losses.append(float((err * err).mean()))
-        dlogits = state.read_backward(logits, idx, 2 * err)
+        dlogits = state.read_backward(logits, idx, 2 * err, w)
         router -= 0.1 * (features.T @ dlogits)
     if sdm.device_status() != 0:
         raise RuntimeError("a kernel raised the device status word")

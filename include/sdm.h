@@ -12,7 +12,8 @@
  *
  *
  * and the operators around them (routing and quantised banks, at the end of this file):
- *   sdm_route          scores to slots and weights (top-k), sdm_route_backward its gradient
+ *   sdm_route          scores to slots and weights (top-k), sdm_route_backward its gradient (_ex: with
+ *                      the weights, by which entries that filled up are known)
  *   sdm_quantize_rows  rows into a quantised bank, sdm_dequantize_rows back out of it
  *   sdm_qgather        weighted sums of quantised rows, sdm_gather_dw the weights' gradient
  *   sdm_qdecode_step   write-then-read tokens on a quantised bank (sdm_qdecode_seq: T tokens)
@@ -475,13 +476,23 @@ int sdm_route(const void* logits, int64_t row_stride, int logit_dtype, const flo
  *     dlogits_j = s_j * (u_j [chosen] - sum_i u_i * s_i)       (SDM_SOFTMAX)
  * The choice itself, and the bias, have no gradient. idx is what sdm_route returned (base added);
  * an index outside the row is skipped and raises SDM_DEV_BAD_INDEX; the k indices of a token are
- * distinct. Masked logits get 0.
+ * distinct. Masked logits get 0, and the dw of masked entries, which may be anything, takes no part.
  *
+ * Where sdm_route filled up with masked entries whose logits are live (of groups that did not stay, or
+ * with a rank of -inf by their bias) it has to be known which these are: sdm_route_backward_ex takes
+ * the weights that sdm_route returned, and an entry of weight 0 counts as not chosen. sdm_route_backward
+ * is the call without them (w NULL): it takes every entry with a live logit as chosen, which is so
+ * wherever k entries at least are not masked, and without groups and biases always.
+ *
+ *   w           [tokens, k] float32, or NULL
  *   dlogits     row t at dlogits + t * dlogits_stride elements, logit dtype; all n columns written
  */
 int sdm_route_backward(const void* logits, int64_t row_stride, int logit_dtype, const void* base, const void* idx,
                        const float* dw, void* dlogits, int64_t dlogits_stride, int64_t tokens, int n, int k, int score,
                        float scale, unsigned flags, int idx_dtype, sdm_stream_t stream);
+int sdm_route_backward_ex(const void* logits, int64_t row_stride, int logit_dtype, const void* base, const void* idx,
+                          const float* w, const float* dw, void* dlogits, int64_t dlogits_stride, int64_t tokens, int n,
+                          int k, int score, float scale, unsigned flags, int idx_dtype, sdm_stream_t stream);
 
 /* A static string naming a return code of the calls above. */
 const char* sdm_status_string(int status);
