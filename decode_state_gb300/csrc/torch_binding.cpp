@@ -107,9 +107,12 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType t, const at::Device& dev) {
     return Tensor(at::detail::empty_cuda(shape, t, dev, std::nullopt));
 }
 
-// The device of the work made current, and the stream it goes to.
+// The device of the work made current, and the stream it goes to. Outputs made while a given stream is
+// current come from that stream's memory: what else is free may still be in use by the current stream,
+// whose work the given one does not wait for.
 struct Launch {
     c10::cuda::OptionalCUDAGuard guard;
+    c10::cuda::OptionalCUDAStreamGuard stream_guard;
     sdm_stream_t stream;
 
     Launch(const at::Device& dev, PyObject* s) {
@@ -122,6 +125,9 @@ struct Launch {
         THPObjectPtr handle = PyLong_Check(s) ? THPObjectPtr(Py_NewRef(s)) : attribute(s, name);
         stream = static_cast<sdm_stream_t>(PyLong_AsVoidPtr(handle.get()));
         if (stream == nullptr && PyErr_Occurred()) throw python_error();
+        // the handles 1 (the legacy default stream) and 2 (a thread's) are names, not streams of their own
+        const cudaStream_t own = stream == reinterpret_cast<sdm_stream_t>(cudaStreamLegacy) ? nullptr : reinterpret_cast<cudaStream_t>(stream);
+        if (own != cudaStreamPerThread) stream_guard.reset_stream(c10::cuda::getStreamFromExternal(own, dev.index()));
     }
 };
 

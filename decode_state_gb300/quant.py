@@ -6,7 +6,9 @@ slots, ``dequantize_rows`` reads them back, ``gather`` sums rows with weights, `
 gradient of those weights (also over bfloat16 and float32 banks), and ``decode_step`` /
 ``decode_seq`` advance streams on it as ``sdm.decode_step`` / ``sdm.decode_seq`` do on a
 floating-point bank. Everything runs in the CUDA library; the native binding checks arguments and
-passes pointers. Work goes to the current stream of the bank's device unless ``stream`` is given.
+passes pointers. Work goes to the current stream of the bank's device unless ``stream`` is given (a
+``torch.cuda.Stream`` or a handle); outputs are then made in that stream's memory, and whoever uses
+them on another stream waits for it first, and records its use (``Tensor.record_stream``) before they go.
 
 A user's choice of format: int8 rounds a row's values by about as much as bfloat16 does (1/254 of
 the group's largest value at most) and suits rows that are written again and again; fp8 keeps three
@@ -63,8 +65,10 @@ class QuantBank:
     def from_rows(cls, rows: torch.Tensor, *, group: int = 128, format: str = "int8", stream=None) -> "QuantBank":
         """The bank [n_slots, hd] (bfloat16 or float32) quantised, e.g. to go on decoding on 8 bits."""
         n, hd = rows.shape
-        codes = torch.empty((n, row_bytes(hd, format)), dtype=torch.uint8, device=rows.device)
-        scales = torch.empty((n, -(-hd // group)), dtype=torch.float32, device=rows.device)
+        given = stream if stream is None or hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, rows.device)
+        with torch.cuda.stream(given):  # memory that is free for the stream that writes it
+            codes = torch.empty((n, row_bytes(hd, format)), dtype=torch.uint8, device=rows.device)
+            scales = torch.empty((n, -(-hd // group)), dtype=torch.float32, device=rows.device)
         bank = cls(codes, scales, hd, group=group, format=format)
         quantize_rows(bank, rows, stream=stream)
         return bank

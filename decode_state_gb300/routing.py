@@ -2,7 +2,8 @@
 
 The entries are a stream's memory slots (the results are then ``k_idx`` / ``k_val`` or ``q_idx`` /
 ``q_val`` of a decode, or an operand of a gather) or experts (whose outputs a gather joins). The
-definition, with ties, masks and groups, stands at ``sdm_route`` in ``include/sdm.h``.
+definition, with ties, masks and groups, stands at ``sdm_route`` in ``include/sdm.h``. Work goes to the
+current stream unless ``stream`` is given; outputs are then made in that stream's memory.
 """
 
 from __future__ import annotations
