@@ -518,7 +518,7 @@ const char* sdm_status_string(int status) {
         case SDM_ECOUNT: return "a count is negative or too large for one launch, or n_slots is outside 1..2^31-1";
         case SDM_ECHUNK: return "need chunk >= 1, tokens a multiple of chunk and 0 <= valid <= chunk";
         case SDM_EALIGN: return "a pointer is not aligned to its element size";
-        case SDM_EOVERLAP: return "a gather output or the stash overlaps the bank";
+        case SDM_EOVERLAP: return "an output overlaps memory that the call reads (a gather's: its bank), or another output";
         case SDM_ENOPS: return "the gather takes one or two operands";
         case SDM_EPLAN: return "not a plan made by sdm_gather_plan_init / sdm_decode_plan_init in this process";
         case SDM_EROW: return "row0 outside 0..row0_max, row0_max + tokens beyond the index rows, or a plan step outside 0..T-1";

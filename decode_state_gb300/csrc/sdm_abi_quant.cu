@@ -15,6 +15,37 @@ bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
     return x < y + bn && y < x + an;
 }
 
+// Rows of `cols` elements, `stride` elements from one to the next; an array is one row of all its elements.
+struct Rows {
+    const void* p;
+    int64_t rows, stride, cols;
+    size_t es;
+
+    uintptr_t at() const { return reinterpret_cast<uintptr_t>(p); }
+    unsigned __int128 pitch() const { return (unsigned __int128)stride * es; }
+    unsigned __int128 row() const { return (unsigned __int128)cols * es; }
+    unsigned __int128 end() const { return at() + (rows - 1) * pitch() + row(); }
+};
+
+Rows array(const void* p, int64_t n, int64_t per, size_t es) { return {p, 1, 0, n * per, es}; }
+
+// Whether any element is in both, also where the rows of one lie beside those of the other in a wider matrix.
+// Rows that interleave with a different stride count as overlapping.
+bool overlaps(const Rows& a, const Rows& b) {
+    if (a.p == nullptr || b.p == nullptr || !(a.at() < b.end() && b.at() < a.end())) return false;
+    if (a.rows > 1 && b.rows == 1) return overlaps(b, a);
+    if (b.rows > 1 && (a.rows == 1 || a.stride == b.stride)) {
+        // the place of a's first element behind the start of a row of b (of equal strides, of any row)
+        const unsigned __int128 before = a.at() < b.at() ? b.at() - a.at() : 0, pitch = b.pitch();
+        const unsigned __int128 place = (a.at() + (before + pitch - 1) / pitch * pitch - b.at()) % pitch;
+        // beside that row, and short of the next one; an array behind the last row's columns was apart above
+        if (a.rows > 1) return place < b.row() || place + a.row() > pitch;
+        if (a.at() < b.at()) return true;  // it reaches the first row
+        return place < b.row() || (place + a.row() > pitch && a.at() - place + pitch < b.end());
+    }
+    return true;
+}
+
 bool quantised(int format) { return format == SDM_INT8 || format == SDM_FP8 || format == SDM_INT4; }
 bool float_type(int dtype) { return dtype == SDM_BF16 || dtype == SDM_F32; }
 bool index_type(int dtype) { return dtype == SDM_I32 || dtype == SDM_I64; }
@@ -45,6 +76,11 @@ int quant_rows(uint8_t* codes, float* scales, int64_t n_slots, int hd, int group
     if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(rows, float_size(row_dtype)) ||
         (slots && !aligned(slots, index_size(idx_dtype))))
         return SDM_EALIGN;
+    const Rows r{rows, n_rows, row_stride, hd, float_size(row_dtype)};
+    const Rows c = array(codes, n_slots, sdm_quant_row_bytes(hd, format), 1), sc = array(scales, n_slots, (hd + group - 1) / group, 4);
+    const Rows sl = array(slots, n_rows, 1, index_size(idx_dtype));
+    if (overlaps(c, sc) || overlaps(r, c) || overlaps(r, sc)) return SDM_EOVERLAP;
+    if (write ? overlaps(c, sl) || overlaps(sc, sl) : overlaps(r, sl)) return SDM_EOVERLAP;
     sdm::QuantRowsArgs a{};
     a.codes = codes;
     a.scales = scales;
@@ -152,12 +188,15 @@ int sdm_gather_dw(const void* bank, const float* scales, int64_t n_slots, int hd
     if (!aligned(bank, plain ? float_size(format) : 16) || !aligned(scales, 4) || !aligned(chunk_valid, 4))
         return SDM_EALIGN;
     const size_t bank_bytes = (size_t)n_slots * (plain ? hd * float_size(format) : (size_t)sdm_quant_row_bytes(hd, format));
+    const size_t scale_bytes = plain ? 0 : (size_t)n_slots * ((hd + group - 1) / group) * 4;
     sdm::QGatherArgs a{};
     for (int o = 0; o < n_ops; ++o) {
         if (!idx[o] || !dout[o] || !dw[o]) return SDM_ENULL;
         if (!aligned(idx[o], index_size(idx_dtype)) || !aligned(dw[o], float_size(dw_dtype)) || !aligned(dout[o], 4))
             return SDM_EALIGN;
-        if (overlaps(dw[o], (size_t)tokens * width[o] * float_size(dw_dtype), bank, bank_bytes)) return SDM_EOVERLAP;
+        const size_t dw_bytes = (size_t)tokens * width[o] * float_size(dw_dtype);
+        if (overlaps(dw[o], dw_bytes, bank, bank_bytes) || (!plain && overlaps(dw[o], dw_bytes, scales, scale_bytes)))
+            return SDM_EOVERLAP;
         a.idx[o] = idx[o];
         a.dout[o] = dout[o];
         a.dw[o] = dw[o];
@@ -198,6 +237,16 @@ int sdm_qdecode_seq(void* codes, float* scales, int64_t n_slots, const void* k_i
         !aligned(q_idx, is) || !aligned(k_val, 4) || !aligned(v, 4) || !aligned(beta, 4) || !aligned(g, 4) ||
         !aligned(q_val, 4))
         return SDM_EALIGN;
+    const int64_t tokens = n_streams * T;
+    if (tokens > (int64_t)1 << 40) return SDM_ECOUNT;
+    const Rows c = array(codes, n_slots, sdm_quant_row_bytes(hd, format), 1), sc = array(scales, n_slots, (hd + group - 1) / group, 4);
+    const Rows o = array(out, tokens, hd, float_size(out_dtype));
+    for (const Rows& in : {array(k_idx, tokens, W, is), array(q_idx, tokens, R, is), array(k_val, tokens, W, 4), array(q_val, tokens, R, 4),
+                           array(v, tokens, hd, 4), array(beta, tokens, 1, 4), array(g, tokens, G, 4)}) {
+        // a column of v has been read when its reading is written, so float32 readings may take its place
+        if (overlaps(in, c) || overlaps(in, sc) || (overlaps(in, o) && !(in.p == v && out == v && out_dtype == SDM_F32))) return SDM_EOVERLAP;
+    }
+    if (overlaps(c, sc) || overlaps(o, c) || overlaps(o, sc)) return SDM_EOVERLAP;
     sdm::QDecodeArgs a{};
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = scales;
@@ -261,6 +310,11 @@ int sdm_route(const void* logits, int64_t row_stride, int logit_dtype, const flo
     if (tokens == 0) return SDM_OK;
     if (!w) return SDM_ENULL;
     if (!aligned(w, 4) || !aligned(bias, 4)) return SDM_EALIGN;
+    const Rows oi = array(idx, tokens, k, index_size(idx_dtype)), ow = array(w, tokens, k, 4);
+    for (const Rows& in : {Rows{logits, tokens, row_stride, n, float_size(logit_dtype)}, array(bias, 1, n, 4),
+                           array(base, tokens, 1, index_size(idx_dtype))})
+        if (overlaps(in, oi) || overlaps(in, ow)) return SDM_EOVERLAP;
+    if (overlaps(oi, ow)) return SDM_EOVERLAP;
     sdm::RouteArgs a{};
     a.logits = logits;
     a.row_stride = row_stride;
@@ -290,6 +344,11 @@ int sdm_route_backward_ex(const void* logits, int64_t row_stride, int logit_dtyp
     if (!dw || !dlogits) return SDM_ENULL;
     if (dlogits_stride < n) return SDM_ESTRIDE;
     if (!aligned(w, 4) || !aligned(dw, 4) || !aligned(dlogits, float_size(logit_dtype))) return SDM_EALIGN;
+    const size_t es = float_size(logit_dtype), is = index_size(idx_dtype);
+    const Rows out{dlogits, tokens, dlogits_stride, n, es};
+    for (const Rows& in : {Rows{logits, tokens, row_stride, n, es}, array(idx, tokens, k, is), array(base, tokens, 1, is),
+                           array(w, tokens, k, 4), array(dw, tokens, k, 4)})
+        if (overlaps(in, out)) return SDM_EOVERLAP;
     sdm::RouteArgs a{};
     a.logits = logits;
     a.row_stride = row_stride;

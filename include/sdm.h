@@ -74,7 +74,7 @@ typedef struct CUstream_st* sdm_stream_t;
 #define SDM_ECOUNT (-7)     /* negative count, n_slots < 1 or >= 2^31, or more units than one launch holds */
 #define SDM_ECHUNK (-8)     /* chunk < 1, tokens not a multiple of chunk, or valid outside 0..chunk */
 #define SDM_EALIGN (-9)     /* a pointer is not aligned to its element size */
-#define SDM_EOVERLAP (-10)  /* a gather output or the stash overlaps the bank */
+#define SDM_EOVERLAP (-10)  /* an output overlaps memory that the call reads (a gather's: its bank), or another output */
 #define SDM_ENOPS (-11)     /* gather operand count is not 1 or 2 */
 #define SDM_EPLAN (-12)     /* not an initialised gather or decode plan (wrong tag or record size) */
 #define SDM_EROW (-13)      /* row0 outside 0..row0_max, row0_max + tokens beyond the index rows, or a plan step outside 0..T-1 */
@@ -347,6 +347,10 @@ int sdm_gather_plan_walk(const sdm_gather_plan* plan, const int64_t* row0, const
  * in float32, rounding codes to nearest even. A group whose max|x| is below 2^-100 is stored as
  * zeros with scale 0; one that holds an infinity or NaN gets the scale NaN, so that it reads back
  * as NaN rather than as something plausible.
+ *
+ * In the calls from here on, outputs must not overlap what the call reads, nor one another (SDM_EOVERLAP;
+ * the gathers look at the bank only). Rows by a stride may lie beside others in a wider matrix of that
+ * stride. One output may take its input's place: float32 readings that of v in the decode.
  */
 #define SDM_INT8 2
 #define SDM_FP8 3
