@@ -97,6 +97,8 @@ class RoutedLayerState:
 
     def load_(self, rows: torch.Tensor, seq_len: int) -> "RoutedLayerState":
         """Take the rows [streams * slots, hd] (bfloat16 or float32) as the bank, after ``seq_len`` tokens."""
+        if tuple(rows.shape) != (self.memory.n_slots, self.memory.hd):
+            raise ValueError(f"rows must be [{self.memory.n_slots}, {self.memory.hd}], got {tuple(rows.shape)}")
         quant.quantize_rows(self.memory, rows)
         self._cache_len = int(seq_len)
         return self
