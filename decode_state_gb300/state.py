@@ -132,8 +132,13 @@ class RoutedLayerState:
         self._cache_len += int(k_logits.shape[0])
         return readings
 
+    def _one_reading(self, q_logits: torch.Tensor) -> None:
+        if tuple(q_logits.shape) != (self.streams, self.slots):
+            raise ValueError(f"logits must be [{self.streams}, {self.slots}], got {tuple(q_logits.shape)}")
+
     def read(self, q_logits: torch.Tensor):
         """What logits [S, slots] read, with no write: (readings [S, hd] float32, idx, w)."""
+        self._one_reading(q_logits)
         idx, w = self.choose(q_logits, self.reads)
         out, = quant.gather(self.memory, [(idx, w)])
         return out, idx, w
@@ -142,6 +147,7 @@ class RoutedLayerState:
         """Gradient of the logits of ``read`` from that of its readings (float32 [S, hd]); ``idx`` and ``w`` as
         it returned them. The choice itself has no gradient, as in any top-k router. Where groups or a bias can
         leave too few slots, the weights tell which only filled up; they are computed again when not given."""
+        self._one_reading(q_logits)
         groups = self.router.get("groups", 1)
         if w is None and (self.router.get("bias") is not None or (self.router.get("top_groups") or groups) < groups):
             _, w = self.choose(q_logits, self.reads)

@@ -1,4 +1,4 @@
-"""What the routed decode state refuses: rows that do not fill the bank."""
+"""What the routed decode state refuses: rows that do not fill the bank, logits that are no single reading."""
 
 from __future__ import annotations
 
@@ -22,3 +22,12 @@ def test_load_takes_all_rows(rows):
         s.load_(torch.zeros(rows, 32, device="cuda"), 3)
     assert s.cache_len == 0 and (s.rows() != 0).all()  # the state is as it was
 
+
+def test_read_takes_one_reading():
+    s = _state()
+    q = torch.randn(3, 4, 5, device="cuda")
+    with pytest.raises(ValueError, match="logits must be"):
+        s.read(q)
+    out, idx, w = s.read(q[0])
+    with pytest.raises(ValueError, match="logits must be"):
+        s.read_backward(q, idx, out)
