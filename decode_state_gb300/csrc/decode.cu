@@ -1619,13 +1619,6 @@ int plan_decode(const DecodeArgs& a0, int bank_dtype, int idx_dtype, DecodeLaunc
     return 0;
 }
 
-int decode_status(unsigned int* word, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_decode_status, sizeof(unsigned int));
-    if (e == cudaSuccess && clear) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_decode_status, &zero, sizeof(unsigned int));
-    }
-    return (int)e;
-}
+cudaError_t decode_status(void** word) { return cudaGetSymbolAddress(word, g_decode_status); }
 
 }  // namespace sdm

@@ -418,13 +418,6 @@ int launch_gather(const GatherArgs& a, int bank_dtype, int idx_dtype, int w_dtyp
     return run_gather(L, stream);
 }
 
-int gather_status(unsigned int* word, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_gather_status, sizeof(unsigned int));
-    if (e == cudaSuccess && clear) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_gather_status, &zero, sizeof(unsigned int));
-    }
-    return (int)e;
-}
+cudaError_t gather_status(void** word) { return cudaGetSymbolAddress(word, g_gather_status); }
 
 }  // namespace sdm

@@ -337,13 +337,6 @@ int launch_qdecode(const QDecodeArgs& a0, int format, cudaStream_t stream) {
     return launch_pdl_raw(c.fn, dim3((unsigned)blocks), dim3((unsigned)c.threads), smem, stream, args);
 }
 
-int qdecode_status(unsigned int* word, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_qdecode_status, sizeof(unsigned int));
-    if (e == cudaSuccess && clear) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_qdecode_status, &zero, sizeof(unsigned int));
-    }
-    return (int)e;
-}
+cudaError_t qdecode_status(void** word) { return cudaGetSymbolAddress(word, g_qdecode_status); }
 
 }  // namespace sdm

@@ -357,13 +357,6 @@ int launch_gather_dw(const QGatherArgs& a0, int format, cudaStream_t stream) {
     return run(fn, a, format, true, al, stream);
 }
 
-int qgather_status(unsigned int* word, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_qgather_status, sizeof(unsigned int));
-    if (e == cudaSuccess && clear) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_qgather_status, &zero, sizeof(unsigned int));
-    }
-    return (int)e;
-}
+cudaError_t qgather_status(void** word) { return cudaGetSymbolAddress(word, g_qgather_status); }
 
 }  // namespace sdm

@@ -692,13 +692,6 @@ int launch_gather_ring(const QGatherArgs& a0, int format, bool grad, cudaStream_
     return launch_pdl_raw(k.fn, dim3((unsigned)blocks), dim3(warps * 32), smem, stream, args);
 }
 
-int gather_ring_status(unsigned int* word, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_ring_status, sizeof(unsigned int));
-    if (e == cudaSuccess && clear) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_ring_status, &zero, sizeof(unsigned int));
-    }
-    return (int)e;
-}
+cudaError_t gather_ring_status(void** word) { return cudaGetSymbolAddress(word, g_ring_status); }
 
 }  // namespace sdm

@@ -245,13 +245,6 @@ int launch_quant_rows(const QuantRowsArgs& a0, int format, int row_dtype, bool w
     return launch_pdl_raw(fn, dim3((unsigned)blocks), dim3(kThreads), run ? kRunBytes + 16 : 0, stream, args);
 }
 
-int quant_status(unsigned int* word, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_quant_status, sizeof(unsigned int));
-    if (e == cudaSuccess && clear) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_quant_status, &zero, sizeof(unsigned int));
-    }
-    return (int)e;
-}
+cudaError_t quant_status(void** word) { return cudaGetSymbolAddress(word, g_quant_status); }
 
 }  // namespace sdm

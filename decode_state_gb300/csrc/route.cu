@@ -1233,13 +1233,6 @@ int launch_route_backward(const RouteArgs& a0, cudaStream_t stream) {
     return launch_pdl_raw(team.fn, dim3((unsigned)blocks), dim3(team.threads), 0, stream, args);
 }
 
-int route_status(unsigned int* word, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_route_status, sizeof(unsigned int));
-    if (e == cudaSuccess && clear) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_route_status, &zero, sizeof(unsigned int));
-    }
-    return (int)e;
-}
+cudaError_t route_status(void** word) { return cudaGetSymbolAddress(word, g_route_status); }
 
 }  // namespace sdm

@@ -165,14 +165,14 @@ int launch_qdecode(const QDecodeArgs& a, int format, cudaStream_t stream);
 int launch_route(const RouteArgs& a, cudaStream_t stream);
 int launch_route_backward(const RouteArgs& a, cudaStream_t stream);
 
-// Device status words of the kernel files (OR of SDM_DEV_* bits); read and optionally reset.
-int decode_status(unsigned int* word, bool clear);
-int gather_status(unsigned int* word, bool clear);
-int quant_status(unsigned int* word, bool clear);
-int qgather_status(unsigned int* word, bool clear);
-int gather_ring_status(unsigned int* word, bool clear);
-int qdecode_status(unsigned int* word, bool clear);
-int route_status(unsigned int* word, bool clear);
+// Addresses of the kernel files' status words on the current device (OR of SDM_DEV_* bits).
+cudaError_t decode_status(void** word);
+cudaError_t gather_status(void** word);
+cudaError_t quant_status(void** word);
+cudaError_t qgather_status(void** word);
+cudaError_t gather_ring_status(void** word);
+cudaError_t qdecode_status(void** word);
+cudaError_t route_status(void** word);
 
 // Multiprocessor count of the current device (cached per device).
 int sm_count();
