@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads) qgather_direct(const QGatherArgs a) 
                 slot = entry_slot(a, a.idx[u.op], first + base + lane);
                 w = a.w_bf16 ? to_f32(__ldg(static_cast<const uint16_t*>(a.w[u.op]) + first + base + lane))
                              : __ldg(static_cast<const float*>(a.w[u.op]) + first + base + lane);
+                w = slot >= 0 ? w : 0.0f;  // a skipped entry's may be anything
             }
 #pragma unroll
             for (int s0 = 0; s0 < LR; s0 += BATCH) {
@@ -216,11 +217,12 @@ __global__ void __launch_bounds__(kThreads) gather_dw_direct(const QGatherArgs a
     if (!pad && slices == 1) load_dout<C>(dout, lane % LR * C, hd, a.vec_out, d);
 
     for (int base = u.e0; base < u.e1; base += 32) {
+        int slot = -1;
         float dot[LR];  // row slot rs, step s: entry base + s * SLOTS + rs
 #pragma unroll
         for (int s = 0; s < LR; ++s) dot[s] = 0.0f;
         if (!pad) {
-            const int slot = base + lane < u.e1 ? entry_slot(a, a.idx[u.op], first + base + lane) : -1;
+            if (base + lane < u.e1) slot = entry_slot(a, a.idx[u.op], first + base + lane);
             for (int slice = 0; slice < slices; ++slice) {
                 const int p = slice * LR + lane % LR;
                 if (slices > 1) load_dout<C>(dout, p * C, hd, a.vec_out, d);
@@ -260,8 +262,9 @@ __global__ void __launch_bounds__(kThreads) gather_dw_direct(const QGatherArgs a
                 }
             }
         }
-        const int e = base + lane % LR * SLOTS + rs;
-        if (e < u.e1) store_dw(a, u.op, first + e, dot[0]);
+        const int at = lane % LR * SLOTS + rs, e = base + at;
+        const bool read = __shfl_sync(kAll, slot, at) >= 0;  // a skipped entry's is 0 whatever dout holds
+        if (e < u.e1) store_dw(a, u.op, first + e, read ? dot[0] : 0.0f);
     }
 }
 

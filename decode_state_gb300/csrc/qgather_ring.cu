@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
         if (a.idx64) raw_hi = __ldg(word + 1);
         if (!GRAD) raw_w = a.w_bf16 ? __ldg(static_cast<const uint16_t*>(a.w[at.op]) + i) : __ldg(static_cast<const uint32_t*>(a.w[at.op]) + i);
     };
-    // request the step's rows (one commit for every step, requested or not); gives the lane's weight and,
-    // where a row's slice has one, its scale
+    // request the step's rows (one commit for every step, requested or not); gives the lane's weight (of the
+    // gradient: whether the lane's entry is skipped) and, where a row's slice has one, its scale
     const auto request = [&](S& st, float& weight, float& scale) {
         weight = scale = 0.0f;
         if (at.t >= 0) {
@@ -302,7 +302,10 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
                     slot = (int)x;
                 else
                     atomicOr(&g_ring_status, SDM_DEV_BAD_INDEX);
-                weight = a.w_bf16 ? __uint_as_float(raw_w << 16) : __uint_as_float(raw_w);
+                if (GRAD)
+                    weight = slot < 0 ? 1.0f : 0.0f;
+                else if (slot >= 0)  // a skipped entry's may be anything
+                    weight = a.w_bf16 ? __uint_as_float(raw_w << 16) : __uint_as_float(raw_w);
             }
             const int p = at.slice * LR + lp, g0 = ONE ? 0 : at.slice * LR * C / a.group;
             const unsigned char* bank = static_cast<const unsigned char*>(a.bank) + p * 16;
@@ -616,6 +619,8 @@ __global__ void __launch_bounds__(kRingWarps * 32, 1) gather_ring(const QGatherA
             }
         }
         __syncwarp();  // the stage may be filled again
+        if (GRAD && weights[0] != 0.0f && now.slice + 1 == slices)  // over what is there: 0 whatever dout holds
+            store_dw(a, now.op, (int64_t)now.t * width + now.base + lane, 0.0f);
         head = head == kAhead ? 0 : head + 1;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {

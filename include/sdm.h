@@ -386,7 +386,8 @@ int sdm_dequantize_rows(const void* codes, const float* scales, int64_t n_slots,
  * sdm_qgather - sdm_gather (no stash) over a quantised bank:
  *     out[o][t, :] = sum_n w[o][t, n] * row(idx[o][t, n])
  * with the sum in float32 in an order that depends on the sizes alone. Padding tokens
- * (t % chunk >= valid) read nothing and get zeros. Arguments as sdm_gather and above.
+ * (t % chunk >= valid) read nothing and get zeros. An entry whose index is outside [0, n_slots) is
+ * skipped, whatever its weight, and raises SDM_DEV_BAD_INDEX. Arguments as sdm_gather and above.
  * From 4096 tokens and operands on, the product of a weight with a scale enters in three parts of 11
  * bits, relative to the largest of up to 32 neighbouring entries: it keeps all its bits down to 2^-22 of
  * that, and what lies below 2^-46 of it is lost. (The same holds for dout in sdm_gather_dw, among the
@@ -401,7 +402,7 @@ int sdm_qgather(const void* codes, const float* scales, int64_t n_slots, int hd,
  * sdm_gather_dw - gradient of the weights of sdm_gather or sdm_qgather:
  *     dw[o][t, n] = sum_c dout[o][t, c] * row(idx[o][t, n])[c]
  * summed in float32 and rounded to dw_dtype once. Padding tokens read nothing and get zeros; an
- * entry whose index is outside [0, n_slots) gets zero and raises SDM_DEV_BAD_INDEX.
+ * entry whose index is outside [0, n_slots) gets zero, whatever dout holds, and raises SDM_DEV_BAD_INDEX.
  *
  *   bank       format SDM_BF16 | SDM_F32: the [n_slots, hd] bank (scales and group are ignored);
  *              SDM_INT8 | SDM_FP8 | SDM_INT4: the codes of a quantised bank
