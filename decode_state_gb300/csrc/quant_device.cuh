@@ -240,7 +240,7 @@ __device__ __forceinline__ float group_scale(float top, float* inv) {
     const bool finite = top <= 3.402823466e38f, some = top >= 7.888609052e-31f;  // 2^-100
     *inv = finite && some ? levels_over(F::kLevels, top) : 0.0f;
     // top / L correctly rounded in two operations, since L is known (Brisebarre, Muller: 1 / L as the
-    // sum of two floats; checked for every significand and at the ends of the range of exponents)
+    // sum of two floats; the tests compare every significand, and every exponent, with a division)
     const float scale = fmaf(F::kInvHigh, top, __fmul_rn(F::kInvLow, top));
     return !finite ? __uint_as_float(0x7fc00000u) : some ? scale : 0.0f;
 }

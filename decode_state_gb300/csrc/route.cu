@@ -48,7 +48,7 @@ __device__ __forceinline__ float sigmoid(float x) { return masked(x) ? 0.0f : __
 
 // Scores of N logits: sigmoid() bit by bit (any value for masked ones), but without a branch for each,
 // so that they overlap. A reciprocal of a float in [1, 2^126] is correctly rounded by one Newton step from the
-// hardware's approximation (checked for every significand); the rare others are done again.
+// hardware's approximation (the tests compare ranks with weights over [1, 2]); the rare others are done again.
 template <int N>
 __device__ __forceinline__ void sigmoids(const float* x, float* s) {
     float most = 0.0f;
