@@ -974,10 +974,10 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
             for (int w = 0; w < WARPS; ++w) own += sums[w] * exp_below(largest[w], m);
         }
     };
-    // chosen entry i: its column, its logit and the gradient of its weight. A weight that is 0 whatever the
-    // logits are has no gradient, and its dw, which may be anything, takes no part: kNone for a masked entry
-    // and, with the forward's weights, for one of weight 0; kOutside for an index outside the row.
-    constexpr int kNone = -2, kOutside = -1;
+    // chosen entry i: its column (-1: outside the row), its logit and the gradient of its weight. A weight that
+    // is 0 whatever the logits are has no gradient, and its dw, which may be anything, takes no part: that of a
+    // masked entry, of an index outside the row and, with the forward's weights, of an entry of weight 0. All of
+    // them get a masked logit here.
     const auto chosen = [&](int i, float& x, float& dw) {
         const int64_t e = t * k + i;
         const float given = __ldg(a.dw + e) * a.scale;  // on its way beside the index
@@ -987,7 +987,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
         const bool filled = a.w != nullptr && __ldg(a.w + e) == 0.0f;
         x = in && !filled ? to_f32(__ldg(row + j)) : minus_inf();
         dw = masked(x) ? 0.0f : given;
-        return !in ? kOutside : masked(x) ? kNone : (int)j;
+        return in ? (int)j : -1;
     };
     const auto get = [&](int j, float* x) {  // U logits from j on; masked ones behind the end
         if (U == 2 && words && j + U <= n) {
@@ -1016,7 +1016,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
     float kept_x[KEPT], kept_dw[KEPT];
 #pragma unroll
     for (int q = 0; q < KEPT; ++q) {
-        kept_j[q] = kNone;
+        kept_j[q] = -1;
         kept_x[q] = minus_inf();
         kept_dw[q] = 0.0f;
         if (lane + 32 * q < k && (dense || tid < 32)) kept_j[q] = chosen(lane + 32 * q, kept_x[q], kept_dw[q]);
@@ -1101,16 +1101,19 @@ __global__ void __launch_bounds__(TEAM == 32 ? 128 : TEAM, backward_blocks(TEAM,
             m = warp_max(m);
         }
         all = 0.0f;
-        each_chosen([&](int, float y, float) { all += score_of(y); });
+        each_chosen([&](int, float y, float dw) {
+            const float s = score_of(y);
+            all += s;
+            dot = fmaf(dw, s * 0x1p32f, dot);  // products of tiny scores keep their bits
+        });
         all = warp_sum(all);
-        each_chosen([&](int, float y, float dw) { dot += dw * share_of(score_of(y)); });
-        dot = warp_sum(dot);
+        dot = all > 0.0f ? __fdiv_rn(warp_sum(dot), all * 0x1p32f) : 0.0f;
     }
     sync();
     if (tid >= 32) return;
     each_chosen([&](int j, float y, float dw) {
-        if (j < 0) {  // what is there stays: 0, or in a dense row that of an entry not chosen
-            if (j == kOutside) atomicOr(&g_route_status, SDM_DEV_BAD_INDEX);
+        if (masked(y)) {  // what is there stays: 0, or in a dense row that of an entry not chosen
+            if (j < 0) atomicOr(&g_route_status, SDM_DEV_BAD_INDEX);
             return;
         }
         const float s = score_of(y);
