@@ -22,7 +22,8 @@
 // through L2, where the state of a chunk of tokens stays); a warp spends 1326 instructions on its 16 and 16
 // rows, at 0.55 a cycle and scheduler, 876 of them on the rows written: their 8-bit codes are unpacked for the
 // retrieval, for the scale and for the new codes, since the columns of four rows do not fit the registers.
-// Keeping them two rows at a time spills (4.8 us). So 8-bit rows halve the bytes of a bf16 bank, not its time.
+// Keeping them two rows at a time spills (4.8 us). So 8-bit rows halve the bytes of a bf16 bank, not its time: 1024
+// streams of 16384 rows, from HBM, 64 and 64 a token, 32 tokens take 10.2 us a token (int8) or 9.6 (fp8) and 8.7 on bf16 rows.
 #include <algorithm>
 #include <climits>
 
@@ -300,7 +301,8 @@ Chosen with_items(int entries) {
     return {(const void*)qdecode_kernel<F, LR, NT, RPT, 1>, NT};
 }
 
-// Blocks that fit the GPU at once as two of 256 threads on each of 152 SMs.
+// Blocks that fit the GPU at once as two of 256 threads on each of 152 SMs. A constant, since the threads
+// settle the order of the sums, and results do not depend on the GPU that is there.
 constexpr int64_t kFewBlocks = 304;
 
 // Threads and rows of each. Few blocks get 256 threads, since a token's chain of steps is then all the

@@ -23,7 +23,10 @@ __device__ unsigned int g_qgather_status;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int64_t kRingUnits = 4096;  // units from which on the ring kernel is used
-constexpr int kMaxChunks = 16384;     // chunks whose prefix sums the ring kernel keeps in shared memory
+// Chunks whose prefix sums the ring kernel keeps in shared memory; a call with chunk_valid and more of them
+// stays here, whatever its tokens: 65536 tokens of 64 and 64 fp8 rows (the gradient of 64 int8 rows) take 215 us (138) in
+// 16384 chunks of 4 and 440 (253) in 32768 of 2.
+constexpr int kMaxChunks = 16384;
 constexpr unsigned kAll = 0xffffffffu;
 
 // the slot of entry i, or -1 (flagged) when it lies outside the bank

@@ -41,8 +41,8 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // Warps of a block at most, and the steps whose rows are on their way while one is summed. More of
 // either is slower: the stages take shared memory from L1, whose lines the requests on their way need.
-// Gather / gradient of 65536 tokens, 64 and 64 rows of 128 bytes each: 16 warps 1 ahead 138 / 82 us, 2
-// ahead 173 / 101; 12 warps 1 ahead 146 / 93, 2 ahead 150 / 95; 20 warps 1 ahead 143 / 100.
+// 65536 tokens, half of them padding, a gather of 64 and 64 rows of 128 bytes / the gradient of 64 rows, single calls: 16
+// warps 1 ahead 138 / 82 us, 2 ahead 173 / 101; 12 warps 1 ahead 146 / 93, 2 ahead 150 / 95; 20 warps 1 ahead 143 / 100.
 constexpr int kRingWarps = 16;
 constexpr int kAhead = 1;
 
@@ -663,9 +663,9 @@ Kernel kernel_of(int lr, bool one) {
 
 int launch_gather_ring(const QGatherArgs& a0, int format, bool grad, cudaStream_t stream) {
     QGatherArgs a = a0;
-    // Slices of codes have at most 128 bytes: 65536 tokens with 64 and 64 rows of 256 bytes take 311 us (gradient
-    // 171) in two slices and 392 (227) in one, whose 256 sums fill the registers. bf16 has half the columns in
-    // as many bytes: 107 us in one slice of 256 bytes, 125 in two.
+    // Slices of codes have at most 128 bytes: 65536 tokens, half of them padding, with 64 and 64 rows of 256 bytes take 311
+    // us (the gradient of 64 rows 171) in two slices and 392 (227) in one, whose 256 sums fill the registers. bf16 has
+    // half the columns in as many bytes: the gradient of 64 rows 107 us in one slice of 256 bytes, 125 in two.
     const int lr = row_lanes(a.pieces, format == SDM_F32 ? 32 : format == SDM_BF16 ? 16 : 8);
     a.slices = (a.pieces + lr - 1) / lr;
     const bool one = a.groups <= 1;
@@ -677,8 +677,8 @@ int launch_gather_ring(const QGatherArgs& a0, int format, bool grad, cudaStream_
                           : (format == SDM_INT8  ? kernel_of<Int8, false, 8>(lr, one)
                              : format == SDM_FP8 ? kernel_of<Fp8, false, 8>(lr, one)
                                                  : kernel_of<Int4, false, 8>(lr, one));
-    // a slice starts at a multiple of them, and so does every row; 65536 tokens with 64 and 64 rows of 128 columns
-    // in groups of 32: 191 us (gradient 108) by four, 199 (111) one by one
+    // a slice starts at a multiple of them, and so does every row; the same tokens with 64 and 64 rows of 128 columns
+    // in groups of 32: 191 us (the gradient of 64 rows 108) by four, 199 (111) one by one
     const int slice_groups = std::max(1, lr * (format == SDM_INT4 ? 32 : 16) / a.group);
     a.scale_words = 1;
     for (int words = 2; words <= 4; words *= 2)

@@ -254,8 +254,8 @@ __device__ __forceinline__ float rough_sigmoid(float x) {
 // are too close to call.
 //
 // Bound by instructions and the latencies between them: 65536 rows of 256 by sigmoid, bias and groups, k = 8, take
-// some 1000 instructions for two tokens, 0.6 a cycle and scheduler, at a tenth of the DRAM's rate. So the registers are bounded for
-// 4 to 6 blocks an SM: 52 -> 45 us; 32768 rows of 1000 float32, k = 64, 228 -> 148 (4 blocks; 6: 163).
+// some 1070 instructions for two tokens, 0.74 a cycle and scheduler, at a tenth of the DRAM's rate. So the registers are
+// bounded for 4 to 6 blocks an SM: 45 -> 39 us; 32768 rows of 1000 float32, k = 64, 221 -> 140 (4 blocks; 6: 158).
 template <int LANES, int E, int V, bool SOFTMAX, typename L>
 __global__ void __launch_bounds__(kWarpThreads, E == 32 ? 4 : E == 16 ? 5 : 6) route_warp_kernel(const RouteArgs a) {
     constexpr int TEAMS = kWarpThreads / LANES, Q = V == 0 ? 3 : 2, CANDS = Q * LANES;  // Q: candidates of a lane at most
@@ -566,8 +566,8 @@ __device__ __forceinline__ float block_reduce(float x, bool sum, float* tmp, int
 
 // PLAIN: a softmax without bias and groups, whose ranks are the logits.
 // The steps of a block wait for one another, so blocks are many: the registers are bounded for 12 of 128
-// threads, 5 of 256, or 3 of 512 (16384 rows of 1500, k = 8: 102 us with 4 blocks as the bound, 54 with 12; 2048 of
-// 8000 33 with 3, 26 with 5). What is left is latency and instructions, of the candidates' ranking by counting most.
+// threads, 5 of 256, or 3 of 512 (16384 rows of 1500, k = 8: 78 us with 4 blocks as the bound, 45 with 12; 2048 of
+// 8000 23 with 3, 18 with 5). What is left is latency and instructions, of the candidates' ranking by counting most.
 template <int NT, bool PLAIN, typename L>
 __global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_block_kernel(const RouteArgs a, int staged) {
     constexpr int WARPS = NT / 32;
@@ -922,9 +922,9 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 3 : NT == 256 ? 5 : 12) route_
 
 // Blocks an SM that the registers are bounded for: a token's steps wait for memory and for one another, so
 // tokens have to be many, as long as their rows fit the registers. Softmax without renormalisation, k = 8:
-// 65536 rows of 256 float32 42 us with 12 blocks, 52 with 8, 54 unbounded; 32768 of 500 33, 36, 42; 16384 of 1000 40, 29, 38
-// (it spills with 12); 2048 of 8000 33 with 4 blocks, 45 unbounded; 1024 of 16384 39 with 2, 53 unbounded.
-// Teams of 128 threads for rows up to 6144: 8192 rows of 1500 30 us, on 256 threads 45; 4097 of 4099 34 and 41.
+// 65536 rows of 256 float32 39 us with 12 blocks, 47 with 8, 52 unbounded; 32768 of 500 29, 32, 42; 16384 of 1000 34, 25, 33
+// (it spills with 12); 2048 of 8000 28 with 4 blocks, 32 with 3, 40 unbounded; 1024 of 16384 33 with 2, 48 unbounded.
+// Teams of 128 threads for rows up to 6144: 8192 rows of 1500 26 us, on 256 threads 52; 4097 of 4099 29 and 40.
 constexpr int backward_blocks(int team, int e) {
     return team <= 128 ? (e <= 16 ? 12 : 8) : team == 256 ? (e == 0 ? 6 : 4) : 2;
 }
@@ -1131,7 +1131,7 @@ struct Team {
     int threads, teams;
 };
 
-// Teams with 8 to 32 logits a thread where the row is kept; without a row to keep, of 256 threads.
+// Teams with 8 to 48 logits a thread where the row is kept; without a row to keep, and beyond 1024 entries, of 128 or 256 threads.
 template <typename L>
 Team backward_kernel(int n, bool dense) {
     if (n <= 256) return {(const void*)route_backward_kernel<32, 8, L>, 128, 4};
@@ -1182,9 +1182,9 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     RouteArgs a = a0;
     // The warp kernel, with as few lanes and maxima as leave twice k maxima among the entries whose groups
     // stay: the k-th largest of them is then a close bound. Half a warp and two maxima a lane for 65536 rows
-    // of 256, k = 8, 4 of 8 groups of 32: 46 us, a whole one and one each: 57. Where no such choice is left, and
-    // for more than 32 entries, a bound by halving: 32768 float32 rows of 200, 500, 1000 with k = 64 take 106, 114,
-    // 149 us, the block kernel 189, 151, 174; of 500 with k = 8 the maxima take 37 us, halving 77.
+    // of 256, k = 8, 4 of 8 groups of 32: 39 us, a whole one and one each: 51. Where no such choice is left, and
+    // for more than 32 entries, a bound by halving: 32768 float32 rows of 200, 500, 1000 with k = 64 take 98, 106,
+    // 140 us, the block kernel 180, 139, 162; of 500 with k = 8 the maxima take 28 us, halving 69.
     const bool grouped = a.n_groups > 1 && a.top_groups < a.n_groups;
     const int live = grouped ? a.n / a.n_groups * a.top_groups : a.n;
     if (a.n <= 1024 && a.k <= 64) {
@@ -1210,13 +1210,15 @@ int launch_route(const RouteArgs& a0, cudaStream_t stream) {
     }
     if (a.tokens > INT_MAX) return SDM_ECOUNT;
     // Ranks that are the logits themselves are read again, out of L2, when a row of them is long, since the
-    // shared memory to keep them is room for blocks: 1024 rows of 16384 bf16 logits, k = 64, 30 us and staged 34, 512
-    // of 32768 26 and 36. Sigmoid ranks would be computed again: 68 us and staged 43.
+    // shared memory to keep them is room for blocks: 1024 rows of 16384 bf16 logits, k = 64, 21 us and staged 26, 512
+    // of 32768 19 and 28. Sigmoid ranks would be computed again: 58 us and staged 34.
     const bool plain = a.score == SDM_SOFTMAX && a.bias == nullptr && !grouped;
     int staged = (size_t)a.n * 4 <= kStagedBytes && !(plain && a.n > 8192) ? 1 : 0;
     const size_t smem = staged ? (size_t)(a.n + 4) * 4 : 0;
-    // Threads for 16 to 64 ranks each. 16384 rows of 1500, k = 64: 128 threads 101 us, 256 142, 512 201; 4096 of 4096
-    // 45, 49, 62; 1024 of 16384 30, 31, 32 (by sigmoid 65, 45, 42); 256 of 65536 53, 33, 24.
+    // Threads for 16 to 64 ranks each. 16384 rows of 1500, k = 64: 128 threads 92 us, 256 132, 512 188; 4096 of 4096
+    // 36, 41, 53; 1024 of 16384 29, 23, 23 (by sigmoid 59, 36, 34); 256 of 65536 45, 26, 22. For k up to half the threads: nearer
+    // to them the k-th largest of their maxima is a poor bound, and above them there is none, so that the histograms follow:
+    // 16384 rows of 1500 with k = 128, 129, 256 take 425, 208, 386 us.
     const int threads = a.n > 16384 ? 512 : a.n > 4096 ? 256 : 128;
     const void* fn = a.logit_bf16 ? block_kernel<uint16_t>(threads, plain) : block_kernel<float>(threads, plain);
     // the limit without a request counts the kernel's static arrays (10 KB) too

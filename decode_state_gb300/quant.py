@@ -91,7 +91,12 @@ def gather(bank: QuantBank, ops, *, chunk: int = 1, valid: int | None = None, ch
            stream=None) -> list:
     """Weighted sums of quantised rows (sdm_qgather): for ``ops = [(idx, w), ...]`` (one or two;
     idx and w [tokens, width], w bfloat16 or float32) the list of [tokens, hd] float32 sums.
-    ``chunk``, ``valid`` and ``chunk_valid`` mark padding tokens as in ``sdm.gather``."""
+    ``chunk``, ``valid`` and ``chunk_valid`` mark padding tokens as in ``sdm.gather``; an entry whose
+    index is outside the bank is skipped.
+
+    From 4096 tokens and operands on, a weight times its row's scale keeps all its bits down to 2^-22 of the
+    largest of up to 32 neighbouring entries, and nothing below 2^-46 of it: a small entry beside a large one
+    loses bits that a float32 sum would keep where the large one's code is 0."""
     return binding().gather(bank, ops, chunk, valid, chunk_valid, None, outs, stream, False)
 
 
@@ -100,7 +105,9 @@ def gather_dw(bank, ops, *, chunk: int = 1, valid: int | None = None, chunk_vali
     """Gradient of a gather's weights (sdm_gather_dw): ``bank`` is a QuantBank, or the [n_slots, hd]
     bfloat16 or float32 bank of ``sdm.gather``; ``ops = [(idx, dout), ...]`` with idx [tokens, width]
     and the gradient dout [tokens, hd] (float32) of that operand's output. Returns the list of
-    [tokens, width] gradients in ``dtype`` (bfloat16 or float32)."""
+    [tokens, width] gradients in ``dtype`` (bfloat16 or float32), zero for an index outside the bank. From
+    4096 tokens and operands on, dout enters relative to the largest of its columns as the weights of
+    ``gather`` do (not over a float32 bank)."""
     return binding().gather(bank, ops, chunk, valid, chunk_valid, dtype, dws, stream, True)
 
 

@@ -388,10 +388,12 @@ int sdm_dequantize_rows(const void* codes, const float* scales, int64_t n_slots,
  * with the sum in float32 in an order that depends on the sizes alone. Padding tokens
  * (t % chunk >= valid) read nothing and get zeros. An entry whose index is outside [0, n_slots) is
  * skipped, whatever its weight, and raises SDM_DEV_BAD_INDEX. Arguments as sdm_gather and above.
- * From 4096 tokens and operands on, the product of a weight with a scale enters in three parts of 11
- * bits, relative to the largest of up to 32 neighbouring entries: it keeps all its bits down to 2^-22 of
- * that, and what lies below 2^-46 of it is lost. (The same holds for dout in sdm_gather_dw, among the
- * columns of a row's slice; over a bf16 bank with an infinite row the gradients it enters may be NaN.)
+ * From 4096 tokens and operands on (of a call with chunk_valid: in at most 16384 chunks), the product
+ * of a weight with a scale enters in three parts of 11 bits, relative to the largest of up to 32
+ * neighbouring entries: it keeps all its bits down to 2^-22 of that, and what lies below 2^-46 of it is
+ * lost. (The same holds for dout in sdm_gather_dw, among the columns of a row's slice; over a bf16 bank
+ * with an infinite row the gradients it enters may be NaN.) More chunks, or fewer tokens, are summed in
+ * float32 throughout, by a kernel that is two to three times slower on many tokens.
  */
 int sdm_qgather(const void* codes, const float* scales, int64_t n_slots, int hd, int group, int format, int n_ops,
                 const void* const idx[2], const void* const w[2], float* const out[2], const int width[2],
