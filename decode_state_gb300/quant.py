@@ -65,7 +65,9 @@ class QuantBank:
     def from_rows(cls, rows: torch.Tensor, *, group: int = 128, format: str = "int8", stream=None) -> "QuantBank":
         """The bank [n_slots, hd] (bfloat16 or float32) quantised, e.g. to go on decoding on 8 bits."""
         n, hd = rows.shape
-        given = stream if stream is None or hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, rows.device)
+        given = stream
+        if stream is not None and not hasattr(stream, "cuda_stream"):  # a handle; 1 is the legacy default stream, as 0 is
+            given = torch.cuda.ExternalStream(0 if stream == 1 else stream, rows.device)
         with torch.cuda.stream(given):  # memory that is free for the stream that writes it
             codes = torch.empty((n, row_bytes(hd, format)), dtype=torch.uint8, device=rows.device)
             scales = torch.empty((n, -(-hd // group)), dtype=torch.float32, device=rows.device)

@@ -61,3 +61,15 @@ def test_outputs_are_not_memory_in_use(at, as_handle):
     got = call(side.cuda_stream if as_handle else side)  # its inputs have been complete for long
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
+@pytest.mark.parametrize("at", range(7))
+@pytest.mark.parametrize("handle", (0, 1, 2))
+def test_handles_that_are_names(at, handle):
+    """The default stream's and the thread's own, which are no streams of PyTorch's."""
+    name, call = _calls()[at]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    got = call(handle)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)), name
