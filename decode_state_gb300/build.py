@@ -22,8 +22,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libsdm.so")
 BINDING_PATH = os.path.join(OUT_DIR, "sdm_torch.so")
 BINDING = "torch_binding.cpp"
-SOURCES = ["sdm_abi.cu", "sdm_abi_quant.cu", "decode.cu", "gather.cu", "quant.cu", "qgather.cu", "qgather_ring.cu",
-           "qdecode.cu", "route.cu"]
+SOURCES = ["sdm_abi.cu", "sdm_abi_quant.cu", "sdm_abi_train.cu", "decode.cu", "gather.cu", "quant.cu", "qgather.cu", "qgather_ring.cu",
+           "qdecode.cu", "route.cu", "balance.cu", "lookup.cu", "row_sums.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

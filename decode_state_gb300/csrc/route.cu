@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "quant_device.cuh"
+#include "score_device.cuh"
 #include "sdm_internal.h"
 
 namespace sdm {
@@ -31,19 +32,11 @@ namespace {
 
 __device__ unsigned int g_route_status;
 
-constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kMasked = 1;
 constexpr int kMaxGroups = 256, kMaxK = 256;
 constexpr int kCandidates = 512;
 constexpr size_t kStagedBytes = 192 * 1024;  // ranks a block keeps in shared memory
 
-__device__ __forceinline__ float minus_inf() { return __uint_as_float(0xff800000u); }
-__device__ __forceinline__ bool masked(float x) { return !(x > minus_inf()); }  // NaN too
-
-// exp(x - m) with m the largest of the logits; several +inf are the largest together
-__device__ __forceinline__ float exp_below(float x, float m) {
-    return masked(x) ? 0.0f : x == m ? 1.0f : expf(x - m);
-}
 __device__ __forceinline__ float sigmoid(float x) { return masked(x) ? 0.0f : __frcp_rn(__fadd_rn(1.0f, expf(-x))); }
 
 // Scores of N logits: sigmoid() bit by bit (any value for masked ones), but without a branch for each,
@@ -78,17 +71,6 @@ __device__ __forceinline__ void put_index(const RouteArgs& a, int64_t t, int i, 
         static_cast<int64_t*>(a.idx)[t * a.k + i] = j + (a.base ? __ldg(static_cast<const int64_t*>(a.base) + t) : 0);
     else
         static_cast<int32_t*>(a.idx)[t * a.k + i] = j + (a.base ? __ldg(static_cast<const int32_t*>(a.base) + t) : 0);
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
-    return x;
-}
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, o));
-    return x;
 }
 
 // The two largest values of a set as it grows; empty places hold -inf.

@@ -129,7 +129,7 @@ namespace {
 
 // The kernel files' status words, joined (and reset) by one launch and read by one copy: 7 us for each
 // copy from or to a symbol made 96 us of reading and resetting seven words one by one.
-constexpr int kStatusWords = 7;
+constexpr int kStatusWords = 10;
 struct StatusWords {
     unsigned int* at[kStatusWords];
 };
@@ -551,6 +551,7 @@ const char* sdm_status_string(int status) {
             return "need 1 <= n <= 65536, 1 <= k <= min(n, 256), a known score, 1..256 groups that divide n, "
                    "1 <= top_groups <= n_groups and group_top 1 or 2";
         case SDM_ESTRIDE: return "a row stride is smaller than the row";
+        case SDM_EWORKSPACE: return "the workspace is smaller than the call's _workspace function says";
         default: break;
     }
     if (status > 0) return cudaGetErrorString(static_cast<cudaError_t>(status));
@@ -566,7 +567,8 @@ int sdm_device_status(unsigned int* status, int clear) {
     StatusWords words{};
     int n = 0;
     for (const auto find : {sdm::decode_status, sdm::gather_status, sdm::quant_status, sdm::qgather_status,
-                            sdm::gather_ring_status, sdm::qdecode_status, sdm::route_status}) {
+                            sdm::gather_ring_status, sdm::qdecode_status, sdm::route_status, sdm::balance_status,
+                            sdm::lookup_status, sdm::row_sums_status}) {
         void* word = nullptr;
         if (e == cudaSuccess) e = find(&word);
         words.at[n++] = static_cast<unsigned int*>(word);

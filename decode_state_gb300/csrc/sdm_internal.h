@@ -123,6 +123,74 @@ struct RouteArgs {
     int64_t dlogits_stride;
 };
 
+// The balance loss of a router, with its gradient where dlogits is given.
+struct BalanceArgs {
+    const void* logits;
+    int64_t row_stride;
+    const void* base;
+    const void* idx;
+    const float* w;  // nullptr: every entry counts
+    const int32_t* offsets;  // nullptr: one sequence of all tokens
+    int64_t sequences;
+    float* loss;
+    int32_t* counts;
+    const float* dloss;
+    const void* add;
+    int64_t add_stride;
+    void* dlogits;
+    int64_t dlogits_stride;
+    int64_t tokens;
+    int n, k, score;
+    float scale;
+    int idx64, logit_bf16;
+    void* workspace;
+    int32_t* totals;  // [sequences] in the workspace: entries counted
+    float* parts;     // [teams + sequences] in the workspace: a team's part of a sequence's loss
+    int64_t rows;     // consecutive tokens of a team
+};
+constexpr int kBalanceTeams = 65536;
+
+// Rows of a table by token.
+struct LookupArgs {
+    const void* table;
+    int64_t n_rows;
+    const void* tokens;
+    int64_t n_tokens;
+    int64_t padding;
+    void* out;
+    int hd;
+    float scale;
+    int table_bf16, out_bf16, idx64;
+    uint32_t per_row, magic;  // accesses of a row, and 2^32 over it rounded up
+};
+
+// Sums of weighted rows by slot: the gradient of an embedding table, or of the bank in a gather.
+struct RowSumArgs {
+    int n_ops;
+    const void* idx[2];
+    const void* w[2];  // nullptr: weights of one
+    const void* dout[2];
+    int width[2];
+    int idx64, w_bf16, dout_bf16, out_bf16, accumulate;
+    int64_t tokens;
+    int chunk, valid;
+    const int32_t* chunk_valid;
+    int64_t padding, n_slots;
+    int hd;
+    float scale;
+    void* out;
+    void* workspace;
+    // the entries, sorted by slot (a dropped entry's is n_slots), and the pieces of them that are summed at a time
+    uint32_t entries, split;  // all, and those of the first operand
+    const uint32_t* keys;
+    const uint32_t* ents;
+    uint32_t piece, pieces;
+    float* heads;  // [pieces, hd]: sums of the run that a piece continues
+    float* tails;  // [pieces, hd]: of the run that a piece begins and does not end
+    int slices, slice_cols;
+    int64_t zero_blocks;
+};
+
 // A resolved gather launch: the kernel instance, its geometry and every kernel argument.
 struct GatherLaunch {
     const void* fn;  // kernel (host stub of the template instance); nullptr: nothing to launch
@@ -164,6 +232,11 @@ int row_lanes(int pieces, int most);
 int launch_qdecode(const QDecodeArgs& a, int format, cudaStream_t stream);
 int launch_route(const RouteArgs& a, cudaStream_t stream);
 int launch_route_backward(const RouteArgs& a, cudaStream_t stream);
+int64_t balance_workspace(int64_t sequences);
+int launch_balance(const BalanceArgs& a, cudaStream_t stream);
+int launch_lookup(const LookupArgs& a, cudaStream_t stream);
+int64_t row_sums_workspace(int64_t entries, int64_t n_slots, int hd);
+int launch_row_sums(const RowSumArgs& a, cudaStream_t stream);
 
 // Addresses of the kernel files' status words on the current device (OR of SDM_DEV_* bits).
 cudaError_t decode_status(void** word);
@@ -173,6 +246,9 @@ cudaError_t qgather_status(void** word);
 cudaError_t gather_ring_status(void** word);
 cudaError_t qdecode_status(void** word);
 cudaError_t route_status(void** word);
+cudaError_t balance_status(void** word);
+cudaError_t lookup_status(void** word);
+cudaError_t row_sums_status(void** word);
 
 // Multiprocessor count of the current device (cached per device).
 int sm_count();

@@ -1,4 +1,4 @@
-// Python functions over the C ABI of the quantised banks and the routing, for PyTorch tensors.
+// Python functions over the C ABI of the quantised banks, the routing and their training, for PyTorch tensors.
 //
 // Marshalling only: shapes, types and devices are checked, outputs allocated and pointers passed to
 // the entry points of include/sdm.h, which do the rest. These operators are called once a token, and
@@ -6,6 +6,7 @@
 // read-back of the rows it wrote took 59 us a call through ctypes wrappers, most of it in the checks.
 // Shape errors raise ValueError, types TypeError, and status codes of the library SDMError.
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -15,6 +16,7 @@
 
 #include <climits>
 #include <optional>
+#include <vector>
 
 #include "sdm.h"
 
@@ -127,7 +129,19 @@ struct Launch {
         if (stream == nullptr && PyErr_Occurred()) throw python_error();
         // the handles 1 (the legacy default stream) and 2 (a thread's) are names, not streams of their own
         const cudaStream_t own = stream == reinterpret_cast<sdm_stream_t>(cudaStreamLegacy) ? nullptr : reinterpret_cast<cudaStream_t>(stream);
-        if (own != cudaStreamPerThread) stream_guard.reset_stream(c10::cuda::getStreamFromExternal(own, dev.index()));
+        per_thread = own == cudaStreamPerThread;
+        if (!per_thread) stream_guard.reset_stream(c10::cuda::getStreamFromExternal(own, dev.index()));
+    }
+
+    bool per_thread = false;
+
+    // Memory for the call to work in, given back when the caller lets go of it: free for what the stream does next,
+    // and not before the stream is done with it where it is another one than the memory's.
+    Tensor workspace(int64_t bytes, const at::Device& dev) const {
+        Tensor t = empty({bytes}, at::kByte, dev);
+        if (per_thread && bytes > 0)
+            c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), c10::cuda::getStreamFromExternal(cudaStreamPerThread, dev.index()));
+        return t;
     }
 };
 
@@ -179,16 +193,17 @@ struct Bank {
         scales = static_cast<float*>(s.data_ptr());
     }
 
-    // a plain [n_slots, hd] bank
-    explicit Bank(const Tensor& t) {
-        format = float_code(t.scalar_type(), "bank");
-        TORCH_CHECK_TYPE(t.dim() == 2, "bank must be a QuantBank or a [n_slots, head_dim] bfloat16 or float32 tensor");
+    // a plain [n_slots, hd] bank, or a table of rows
+    explicit Bank(const Tensor& t, const char* name = "bank") {
+        format = float_code(t.scalar_type(), name);
+        TORCH_CHECK_TYPE(t.dim() == 2, name, name[0] == 'b' ? " must be a QuantBank or a [n_slots, head_dim] bfloat16 or float32 tensor"
+                                                            : " must be a [rows, hd] bfloat16 or float32 tensor");
         TORCH_CHECK_VALUE(t.size(1) >= 1 && t.size(1) <= 65536, "head_dim must be in 1..65536, got ", t.size(1));
         n_slots = t.size(0);
         hd = static_cast<int>(t.size(1));
         dev = t.device();
-        need(t, "bank", dev, t.sizes());
-        TORCH_CHECK_VALUE(t.is_cuda(), "bank must be a CUDA tensor, got ", dev);
+        TORCH_CHECK_VALUE(t.is_cuda(), name, " must be a CUDA tensor, got ", dev);
+        need(t, name, dev, t.sizes());
         codes = t.data_ptr();
     }
 };
@@ -492,6 +507,241 @@ PyObject* route_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// balance(logits, idx, score, w or None, base or None, offsets or None, scale, gradient, dloss or None, add or None,
+//         loss or None, counts or None, out or None, stream)
+PyObject* balance(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const Args a{args, n};
+    expect(a, 14, "balance");
+    const Logits x(a.tensor(0, "logits"), "logits");
+    const at::Device dev = x.t.device();
+    const Tensor& idx = a.tensor(1, "idx");
+    const int it = index_code(idx.scalar_type(), "idx");
+    TORCH_CHECK_VALUE(idx.dim() == 2, "idx must be [tokens, k]");
+    const int64_t k = idx.size(1);
+    need(idx, "idx", dev, {x.tokens, k});
+    const float *w = nullptr, *dloss = nullptr;
+    if (!a.none(3)) {
+        need_f32(a.tensor(3, "w"), "w", dev, {x.tokens, k});
+        w = static_cast<const float*>(a.tensor(3, "w").data_ptr());
+    }
+    const void* base = base_of(a, 4, x.tokens, idx.scalar_type(), dev);
+    const int32_t* offsets = nullptr;
+    int64_t sequences = 1;
+    if (!a.none(5)) {
+        const Tensor& o = a.tensor(5, "offsets");
+        TORCH_CHECK_TYPE(o.scalar_type() == at::kInt, "offsets must be int32, got ", o.scalar_type());
+        TORCH_CHECK_VALUE(o.dim() == 1 && o.size(0) >= 1, "offsets must be [sequences + 1], got ", o.sizes());
+        sequences = o.size(0) - 1;
+        need(o, "offsets", dev, {sequences + 1});
+        offsets = static_cast<const int32_t*>(o.data_ptr());
+    }
+    const bool gradient = a.truth(7);
+    TORCH_CHECK_VALUE(gradient || (a.none(8) && a.none(9) && a.none(12)), "dloss, add and out belong to the gradient");
+    if (!a.none(8)) {
+        need_f32(a.tensor(8, "dloss"), "dloss", dev, {sequences});
+        dloss = static_cast<const float*>(a.tensor(8, "dloss").data_ptr());
+    }
+    Launch l(dev, a.a[13]);
+    Tensor made_loss, made_counts, made_out;
+    if (a.none(10)) made_loss = empty({sequences}, at::kFloat, dev);
+    if (a.none(11)) made_counts = empty({sequences, x.t.size(1)}, at::kInt, dev);
+    const Tensor& loss = a.none(10) ? made_loss : a.tensor(10, "loss");
+    const Tensor& counts = a.none(11) ? made_counts : a.tensor(11, "counts");
+    need_f32(loss, "loss", dev, {sequences});
+    TORCH_CHECK_TYPE(counts.scalar_type() == at::kInt, "counts must be int32, got ", counts.scalar_type());
+    need(counts, "counts", dev, {sequences, x.t.size(1)});
+    const auto like_logits = [&](const Logits& g, const char* name) {
+        TORCH_CHECK_TYPE(g.type == x.type && g.t.device() == dev, name, " must have the dtype and the device of the logits");
+        TORCH_CHECK_VALUE(g.t.sizes() == x.t.sizes(), name, " has shape ", g.t.sizes(), ", expected ", x.t.sizes());
+    };
+    const void* add = nullptr;
+    void* dlogits = nullptr;
+    int64_t add_stride = 0, out_stride = 0;
+    if (gradient) {
+        if (!a.none(9)) {
+            const Logits g(a.tensor(9, "add"), "add");
+            like_logits(g, "add");
+            add = g.t.data_ptr();
+            add_stride = g.stride;
+        }
+        if (a.none(12)) made_out = empty(x.t.sizes(), x.t.scalar_type(), dev);
+        const Logits g(a.none(12) ? made_out : a.tensor(12, "out"), "out");
+        like_logits(g, "out");
+        dlogits = g.t.data_ptr();
+        out_stride = g.stride;
+    }
+    int64_t bytes = 0;
+    check("sdm_balance_workspace", sdm_balance_workspace(sequences, &bytes));
+    const Tensor scratch = l.workspace(bytes, dev);
+    check("sdm_balance",
+          sdm_balance(x.t.data_ptr(), x.stride, x.type, base, idx.data_ptr(), w, offsets, sequences, static_cast<float*>(loss.data_ptr()),
+                      static_cast<int32_t*>(counts.data_ptr()), dloss, add, add_stride, dlogits, out_stride, x.tokens, static_cast<int>(x.n),
+                      k > 256 ? 257 : static_cast<int>(k), a.small(2), a.real(6), it, scratch.data_ptr(), bytes, l.stream));
+    PyObject* all = PyTuple_New(gradient ? 3 : 2);
+    if (all == nullptr) throw python_error();
+    PyTuple_SET_ITEM(all, 0, give(a.a[10], made_loss));
+    PyTuple_SET_ITEM(all, 1, give(a.a[11], made_counts));
+    if (gradient) PyTuple_SET_ITEM(all, 2, give(a.a[12], made_out));
+    return all;
+    END_HANDLE_TH_ERRORS
+}
+
+// ---------------------------------------------------------------- rows by token
+
+int64_t padding_of(const Args& a, int i) {
+    if (a.none(i)) return SDM_NO_PADDING;
+    const int64_t p = a.integer(i);
+    TORCH_CHECK_VALUE(p != SDM_NO_PADDING, "no such padding: ", p);
+    return p;
+}
+
+// lookup(table, tokens, scale, padding or None, dtype or None, out or None, stream)
+PyObject* lookup(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const Args a{args, n};
+    expect(a, 7, "lookup");
+    const Tensor &table = a.tensor(0, "table"), &tokens = a.tensor(1, "tokens");
+    const int it = index_code(tokens.scalar_type(), "tokens");
+    const Bank b(table, "table");
+    need(tokens, "tokens", b.dev, tokens.sizes());
+    std::vector<int64_t> shape(tokens.sizes().vec());
+    shape.push_back(b.hd);
+    Launch l(b.dev, a.a[6]);
+    Tensor made;
+    if (a.none(5)) {
+        const auto t = a.none(4) ? table.scalar_type() : a.dtype(4, "dtype");
+        float_code(t, "dtype");
+        made = empty(shape, t, b.dev);
+    }
+    const Tensor& out = a.none(5) ? made : a.tensor(5, "out");
+    const int ot = float_code(out.scalar_type(), "out");
+    need(out, "out", b.dev, shape);
+    check("sdm_lookup", sdm_lookup(b.codes, b.n_slots, b.hd, b.format, tokens.data_ptr(), it, tokens.numel(), padding_of(a, 3), a.real(2),
+                                   out.data_ptr(), ot, l.stream));
+    return give(a.a[5], made);
+    END_HANDLE_TH_ERRORS
+}
+
+// The gradient of rows: made, or given to be written or added to.
+struct RowsOut {
+    Tensor made;
+    const Tensor* t;
+    int type;
+    unsigned flags;
+
+    RowsOut(const Args& a, int dtype, int out, int accumulate, int64_t rows, int64_t hd, const at::Device& dev) {
+        flags = a.truth(accumulate) ? SDM_ACCUMULATE : 0u;
+        TORCH_CHECK_VALUE(!flags || !a.none(out), "there must be an out to add to");
+        TORCH_CHECK_VALUE(rows >= 0, "a negative number of rows");
+        if (a.none(out)) {
+            const auto ty = a.dtype(dtype, "dtype");
+            float_code(ty, "dtype");
+            made = empty({rows, hd}, ty, dev);
+        }
+        t = a.none(out) ? &made : &a.tensor(out, "out");
+        type = float_code(t->scalar_type(), "the gradient");
+        need(*t, "out", dev, {rows, hd});
+    }
+};
+
+// lookup_backward(dout, tokens, rows, scale, padding or None, dtype, out or None, accumulate, stream)
+PyObject* lookup_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const Args a{args, n};
+    expect(a, 9, "lookup_backward");
+    const Tensor &dout = a.tensor(0, "dout"), &tokens = a.tensor(1, "tokens");
+    const at::Device dev = dout.device();
+    const int dt = float_code(dout.scalar_type(), "dout"), it = index_code(tokens.scalar_type(), "tokens");
+    TORCH_CHECK_VALUE(dout.is_cuda(), "dout must be a CUDA tensor, got ", dev);
+    TORCH_CHECK_VALUE(dout.dim() >= 1 && dout.dim() == tokens.dim() + 1, "dout must be [.., hd] for tokens [..], got ", dout.sizes(), " and ",
+                      tokens.sizes());
+    const int64_t hd = dout.size(-1);
+    TORCH_CHECK_VALUE(hd >= 1 && hd <= 65536, "hd must be in 1..65536, got ", hd);
+    need(tokens, "tokens", dev, dout.sizes().slice(0, dout.dim() - 1));
+    need(dout, "dout", dev, dout.sizes());
+    const int64_t count = tokens.numel(), rows = a.integer(2);
+    Launch l(dev, a.a[8]);
+    const RowsOut out(a, 5, 6, 7, rows, hd, dev);
+    int64_t bytes = 0;
+    check("sdm_lookup_backward_workspace", sdm_lookup_backward_workspace(count, rows, static_cast<int>(hd), &bytes));
+    const Tensor scratch = l.workspace(bytes, dev);
+    check("sdm_lookup_backward", sdm_lookup_backward(dout.data_ptr(), dt, tokens.data_ptr(), it, count, padding_of(a, 4), a.real(3),
+                                                     out.t->data_ptr(), rows, static_cast<int>(hd), out.type, out.flags, scratch.data_ptr(),
+                                                     bytes, l.stream));
+    return give(a.a[6], out.made);
+    END_HANDLE_TH_ERRORS
+}
+
+// gather_drows(ops, n_slots, chunk, valid or None, chunk_valid or None, dtype, out or None, accumulate, stream)
+PyObject* gather_drows(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const Args a{args, n};
+    expect(a, 9, "gather_drows");
+    const auto sequence = [](PyObject* o, const char* what) {
+        TORCH_CHECK_TYPE(PyList_Check(o) || PyTuple_Check(o), what, " must be a list or tuple");
+        return o;
+    };
+    PyObject* ops = sequence(a.a[0], "ops");
+    const Py_ssize_t k = PySequence_Fast_GET_SIZE(ops);
+    TORCH_CHECK_VALUE(k == 1 || k == 2, "gather_drows takes one or two operands");
+    const void *idx[2] = {nullptr, nullptr}, *w[2] = {nullptr, nullptr};
+    const float* dout[2] = {nullptr, nullptr};
+    int width[2] = {0, 0}, it = SDM_I32, wt = SDM_F32;
+    int64_t tokens = 0, entries = 0, hd = 0;
+    at::Device dev(at::kCPU);
+    for (Py_ssize_t o = 0; o < k; ++o) {
+        PyObject* three = sequence(PySequence_Fast_GET_ITEM(ops, o), "an operand");
+        TORCH_CHECK_VALUE(PySequence_Fast_GET_SIZE(three) == 3, "an operand is three tensors: idx, w and dout");
+        const Tensor& i = Args::unpack(PySequence_Fast_GET_ITEM(three, 0), "idx");
+        const Tensor& x = Args::unpack(PySequence_Fast_GET_ITEM(three, 1), "w");
+        const Tensor& d = Args::unpack(PySequence_Fast_GET_ITEM(three, 2), "dout");
+        const int t = index_code(i.scalar_type(), "idx"), xt = float_code(x.scalar_type(), "weights");
+        TORCH_CHECK_VALUE(i.dim() == 2 && d.dim() == 2, "idx must be [tokens, width] and dout [tokens, hd]");
+        if (o == 0) {
+            dev = i.device();
+            TORCH_CHECK_VALUE(i.is_cuda(), "idx must be a CUDA tensor, got ", dev);
+            tokens = i.size(0);
+            hd = d.size(1);
+            it = t;
+            wt = xt;
+            TORCH_CHECK_VALUE(hd >= 1 && hd <= 65536, "hd must be in 1..65536, got ", hd);
+        }
+        TORCH_CHECK_TYPE(t == it, "both operands must share the index dtype");
+        TORCH_CHECK_TYPE(xt == wt, "both operands must share the dtype of w");
+        need(i, "idx", dev, {tokens, i.size(1)});
+        need(x, "w", dev, i.sizes());
+        need_f32(d, "dout", dev, {tokens, hd});
+        idx[o] = i.data_ptr();
+        w[o] = x.data_ptr();
+        dout[o] = static_cast<const float*>(d.data_ptr());
+        width[o] = i.size(1) > 256 ? 257 : static_cast<int>(i.size(1));
+        entries += tokens * width[o];
+    }
+    const int chunk = a.small(2);
+    int valid = a.none(3) ? chunk : a.small(3);
+    const int32_t* cv = nullptr;
+    if (!a.none(4)) {
+        const Tensor& c = a.tensor(4, "chunk_valid");
+        TORCH_CHECK_TYPE(c.scalar_type() == at::kInt, "chunk_valid must be int32");
+        TORCH_CHECK_VALUE(chunk >= 1 && tokens % chunk == 0, "tokens must be a multiple of chunk");
+        need(c, "chunk_valid", dev, {tokens / chunk});
+        cv = static_cast<const int32_t*>(c.data_ptr());
+        valid = 0;
+    }
+    const int64_t n_slots = a.integer(1);
+    Launch l(dev, a.a[8]);
+    const RowsOut out(a, 5, 6, 7, n_slots, hd, dev);
+    int64_t bytes = 0;
+    check("sdm_gather_drows_workspace", sdm_gather_drows_workspace(entries, n_slots, static_cast<int>(hd), &bytes));
+    const Tensor scratch = l.workspace(bytes, dev);
+    check("sdm_gather_drows", sdm_gather_drows(static_cast<int>(k), idx, w, dout, width, it, wt, out.t->data_ptr(), n_slots,
+                                               static_cast<int>(hd), out.type, out.flags, tokens, chunk, valid, cv, scratch.data_ptr(), bytes,
+                                               l.stream));
+    return give(a.a[6], out.made);
+    END_HANDLE_TH_ERRORS
+}
+
 // raise_with(f): f(function, status) is called to raise the error of a status code
 PyObject* raise_with(PyObject*, PyObject* f) {
     Py_INCREF(f);
@@ -510,6 +760,10 @@ PyMethodDef methods[] = {{"check_bank", fast(check_bank), METH_FASTCALL, nullptr
                          {"decode", fast(decode), METH_FASTCALL, nullptr},
                          {"route", fast(route), METH_FASTCALL, nullptr},
                          {"route_backward", fast(route_backward), METH_FASTCALL, nullptr},
+                         {"balance", fast(balance), METH_FASTCALL, nullptr},
+                         {"lookup", fast(lookup), METH_FASTCALL, nullptr},
+                         {"lookup_backward", fast(lookup_backward), METH_FASTCALL, nullptr},
+                         {"gather_drows", fast(gather_drows), METH_FASTCALL, nullptr},
                          {"raise_with", raise_with, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

@@ -3,8 +3,8 @@
 A ``QuantBank`` holds a bank's rows as codes of 8 or 4 bits with one float32 scale for every 32, 64
 or 128 columns (layout and rounding: ``include/sdm.h``). ``quantize_rows`` writes rows into its
 slots, ``dequantize_rows`` reads them back, ``gather`` sums rows with weights, ``gather_dw`` is the
-gradient of those weights (also over bfloat16 and float32 banks), and ``decode_step`` /
-``decode_seq`` advance streams on it as ``sdm.decode_step`` / ``sdm.decode_seq`` do on a
+gradient of those weights (also over bfloat16 and float32 banks), ``gather_drows`` that of the rows, and
+``decode_step`` / ``decode_seq`` advance streams on it as ``sdm.decode_step`` / ``sdm.decode_seq`` do on a
 floating-point bank. Everything runs in the CUDA library; the native binding checks arguments and
 passes pointers. Work goes to the current stream of the bank's device unless ``stream`` is given (a
 ``torch.cuda.Stream`` or a handle); outputs are then made in that stream's memory, and whoever uses
@@ -111,6 +111,16 @@ def gather_dw(bank, ops, *, chunk: int = 1, valid: int | None = None, chunk_vali
     4096 tokens and operands on, dout enters relative to the largest of its columns as the weights of
     ``gather`` do (not over a float32 bank)."""
     return binding().gather(bank, ops, chunk, valid, chunk_valid, dtype, dws, stream, True)
+
+
+def gather_drows(ops, n_slots: int, *, chunk: int = 1, valid: int | None = None, chunk_valid=None, dtype=torch.float32, out=None,
+                 accumulate: bool = False, stream=None) -> torch.Tensor:
+    """Gradient of the rows of a gather's bank (sdm_gather_drows), of ``n_slots`` rows of any format: with
+    ``ops = [(idx, w, dout), ...]``, idx and w [tokens, width] as in ``gather`` and the gradient dout [tokens, hd]
+    (float32) of that operand's output, the sums of w * dout by slot, [n_slots, hd] in ``dtype`` (bfloat16 or float32).
+    Entries of weight 0, outside the bank or of padding tokens take no part. ``out`` gives the tensor to write, and with
+    ``accumulate`` the tensor to add to, of which only the slots that were read are touched."""
+    return binding().gather_drows(ops, n_slots, chunk, valid, chunk_valid, dtype, out, accumulate, stream)
 
 
 def decode_step(bank: QuantBank, k_idx, k_val, v, beta, g, q_idx, q_val, out=None, *, out_dtype=torch.bfloat16,

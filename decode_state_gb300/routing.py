@@ -46,3 +46,18 @@ def route_backward(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor, *,
     have no gradient. It is needed wherever ``groups`` or a ``bias`` of -inf may leave fewer than k
     entries; without it every entry with a live logit is taken as chosen."""
     return binding().route_backward(logits, idx, dw, _score(score), renorm, scale, base, w, out, stream)
+
+
+def balance(logits: torch.Tensor, idx: torch.Tensor, *, score: str = "softmax", w=None, base=None, offsets=None, scale: float = 1.0,
+            gradient: bool = False, dloss=None, add=None, loss=None, counts=None, out=None, stream=None):
+    """The balance loss of a router's choices and their counts, and the gradient of its logits in the same pass
+    (sdm_balance). Returns (loss [sequences] float32, counts [sequences, n] int32), with ``gradient`` the logits'
+    gradient [tokens, n] in their dtype too.
+
+    ``logits`` [tokens, n] and ``idx``, ``w``, ``base`` as ``route`` took and returned them; entries of weight 0, which
+    only filled up, are not counted (all are without ``w``). ``offsets`` [sequences + 1] int32 are the first tokens of
+    packed sequences, each with a loss of its own, and the end of the last one (None: one sequence of all tokens); tokens
+    outside them take no part. The loss is ``scale`` for choices spread evenly. ``dloss`` [sequences] float32 is what each
+    loss weighs in the whole (1 when None); ``add`` is added to the gradient, e.g. what ``route_backward`` returned, and
+    ``out`` may be ``add`` itself."""
+    return binding().balance(logits, idx, _score(score), w, base, offsets, scale, gradient, dloss, add, loss, counts, out, stream)

@@ -27,6 +27,8 @@ ENTRY_POINTS = ("sdm_decode_step", "sdm_decode_step_ex", "sdm_decode_seq", "sdm_
                 "sdm_gather_plan_init", "sdm_gather_plan_launch", "sdm_gather_plan_launch_ex", "sdm_gather_plan_walk",
                 "sdm_quant_row_bytes", "sdm_quantize_rows", "sdm_dequantize_rows", "sdm_qgather", "sdm_gather_dw",
                 "sdm_qdecode_step", "sdm_qdecode_seq", "sdm_route", "sdm_route_backward", "sdm_route_backward_ex",
+                "sdm_balance_workspace", "sdm_balance", "sdm_lookup", "sdm_lookup_backward_workspace", "sdm_lookup_backward",
+                "sdm_gather_drows_workspace", "sdm_gather_drows",
                 "sdm_status_string",
                 "sdm_device_status", "sdm_version")
 SDM_INPUTS_READY = 1  # flag of the _ex calls: the inputs predate the kernel launched just before
@@ -107,6 +109,16 @@ def library() -> ctypes.CDLL:
                                                u32, i32, vp]
             lib.sdm_route_backward_ex.argtypes = [vp, i64, i32, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, ctypes.c_float,
                                                   u32, i32, vp]
+            size = ctypes.POINTER(i64)
+            lib.sdm_balance_workspace.argtypes = [i64, size]
+            lib.sdm_balance.argtypes = [vp, i64, i32, vp, vp, vp, vp, i64, vp, vp, vp, vp, i64, vp, i64, i64, i32, i32, i32,
+                                        ctypes.c_float, i32, vp, i64, vp]
+            lib.sdm_lookup.argtypes = [vp, i64, i32, i32, vp, i32, i64, i64, ctypes.c_float, vp, i32, vp]
+            lib.sdm_lookup_backward_workspace.argtypes = [i64, i64, i32, size]
+            lib.sdm_lookup_backward.argtypes = [vp, i32, vp, i32, i64, i64, ctypes.c_float, vp, i64, i32, i32, u32, vp, i64, vp]
+            lib.sdm_gather_drows_workspace.argtypes = [i64, i64, i32, size]
+            lib.sdm_gather_drows.argtypes = [i32, ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(i32),
+                                             i32, i32, vp, i64, i32, i32, u32, i64, i32, i32, vp, vp, i64, vp]
             for name in ENTRY_POINTS[ENTRY_POINTS.index("sdm_quant_row_bytes"):ENTRY_POINTS.index("sdm_status_string")]:
                 getattr(lib, name).restype = i32
             lib.sdm_status_string.argtypes = [i32]

@@ -17,6 +17,9 @@
  *   sdm_quantize_rows  rows into a quantised bank, sdm_dequantize_rows back out of it
  *   sdm_qgather        weighted sums of quantised rows, sdm_gather_dw the weights' gradient
  *   sdm_qdecode_step   write-then-read tokens on a quantised bank (sdm_qdecode_seq: T tokens)
+ *   sdm_balance        a router's balance loss and counts, with the gradient of its logits
+ *   sdm_lookup         scaled rows of a table by token, sdm_lookup_backward the table's gradient
+ *   sdm_gather_drows   the gradient of the bank's rows in a gather
  *
  * Common rules
  *   - Every pointer argument except `stream` (and the host records and arrays named as such) is a
@@ -85,6 +88,7 @@ typedef struct CUstream_st* sdm_stream_t;
 #define SDM_EGROUP (-17)    /* a scale's group is not 32, 64 or 128 columns */
 #define SDM_EROUTE (-18)    /* routing sizes, score kind or groups out of range */
 #define SDM_ESTRIDE (-19)   /* a row stride is smaller than the row */
+#define SDM_EWORKSPACE (-20) /* the workspace is smaller than the call's _workspace function says */
 
 /* bits of the device status word */
 #define SDM_DEV_TIMEOUT 1u   /* reserved: a kernel gave up a bounded wait (no current kernel waits) */
@@ -500,6 +504,95 @@ int sdm_route_backward(const void* logits, int64_t row_stride, int logit_dtype, 
 int sdm_route_backward_ex(const void* logits, int64_t row_stride, int logit_dtype, const void* base, const void* idx,
                           const float* w, const float* dw, void* dlogits, int64_t dlogits_stride, int64_t tokens, int n,
                           int k, int score, float scale, unsigned flags, int idx_dtype, sdm_stream_t stream);
+
+/*
+ * Training: the loss that keeps a router's choices spread over its entries, and the gradients of rows
+ * that are read by index.
+ *
+ * Some of these calls work in memory that the caller lends them: `workspace`, 256-byte aligned device
+ * memory of at least the bytes that the call's _workspace function stores in *bytes (0: none is needed,
+ * and it may be NULL). It holds nothing before the call or after it; calls that may run at the same time
+ * need one each, and so do captured graphs that may be replayed at the same time.
+ *
+ * sdm_balance - for every sequence s of tokens offsets[s] <= t < offsets[s + 1] (all tokens, and one
+ * sequence, when offsets is NULL), with T their number:
+ *     p_tj      = s_tj / sum_i s_ti          the shares of a token's scores (those of sdm_route; masked
+ *                                            entries, and all of a row that is masked throughout, have 0)
+ *     counts[s, j] = how often the sequence's tokens chose entry j
+ *     loss[s]   = scale * n / (T * C) * sum_t sum_j counts[s, j] * p_tj,   C = sum_j counts[s, j]
+ * (0 where T or C is 0): scale where choices or scores are spread evenly, up to scale * n where both are on
+ * one entry. The counts have no gradient. With dlogits, the logits' gradient too:
+ *     dlogits[t, j] = add[t, j] + dloss[s] * scale * n / (T * C) * p_tj * (counts[s, j] - sum_i counts[s, i] * p_ti)
+ * for a softmax, and that second term times 1 - s_tj for a sigmoid. A token outside every sequence takes
+ * no part; its row of dlogits is that of add, or zeros. Masked logits too have a gradient of 0 here.
+ * idx is what sdm_route returned (base added). An entry whose w is 0 is not counted (one that
+ * only filled up); without w every entry is. An index outside the row is not counted and raises
+ * SDM_DEV_BAD_INDEX.
+ *
+ *   offsets    [sequences + 1] int32, not decreasing, within 0..tokens; NULL with sequences 1
+ *   loss       [sequences] float32; counts [sequences, n] int32
+ *   dloss      [sequences] float32, or NULL for ones: the gradient that comes for each loss
+ *   add        tokens rows of logit dtype, or NULL; may be dlogits itself with the same stride
+ *   dlogits    tokens rows of logit dtype, all n columns written; or NULL (then add and dloss are not read)
+ *   tokens and tokens * k below 2^31, sequences below 2^24
+ * Other arguments as sdm_route.
+ */
+int sdm_balance_workspace(int64_t sequences, int64_t* bytes);
+int sdm_balance(const void* logits, int64_t row_stride, int logit_dtype, const void* base, const void* idx, const float* w,
+                const int32_t* offsets, int64_t sequences, float* loss, int32_t* counts, const float* dloss,
+                const void* add, int64_t add_stride, void* dlogits, int64_t dlogits_stride, int64_t tokens, int n, int k,
+                int score, float scale, int idx_dtype, void* workspace, int64_t workspace_bytes, sdm_stream_t stream);
+
+/*
+ * sdm_lookup - scaled rows by token: out[t, :] = scale * table[tokens[t], :], computed in float32 and
+ * rounded to out_dtype once. The token `padding` gives zeros; so does one outside [0, n_rows), which raises
+ * SDM_DEV_BAD_INDEX.
+ *
+ *   table      [n_rows, hd] table_dtype; 1 <= n_rows < 2^31
+ *   tokens     [n_tokens] idx dtype (repeats allowed)
+ *   padding    a token that stands for nothing, inside the table or not; SDM_NO_PADDING: none does
+ *   out        [n_tokens, hd] out_dtype
+ */
+#define SDM_NO_PADDING INT64_MIN
+int sdm_lookup(const void* table, int64_t n_rows, int hd, int table_dtype, const void* tokens, int idx_dtype,
+               int64_t n_tokens, int64_t padding, float scale, void* out, int out_dtype, sdm_stream_t stream);
+
+/*
+ * sdm_lookup_backward - gradient of the table of sdm_lookup:
+ *     grad[r, :] = scale * sum over t with tokens[t] = r of dout[t, :]
+ * summed in float32 in an order that depends on the sizes and the tokens alone, and rounded to grad_dtype
+ * once. Padding tokens and those outside the table (which raise SDM_DEV_BAD_INDEX) take no part; what is
+ * in their dout is not looked at. Rows without tokens become zero; with SDM_ACCUMULATE the sums are added
+ * to what grad holds, and only rows that have tokens are read or written.
+ *
+ *   dout       [n_tokens, hd] dout_dtype; n_tokens below 2^31
+ *   grad       [n_rows, hd] grad_dtype
+ */
+#define SDM_ACCUMULATE 8u
+int sdm_lookup_backward_workspace(int64_t n_tokens, int64_t n_rows, int hd, int64_t* bytes);
+int sdm_lookup_backward(const void* dout, int dout_dtype, const void* tokens, int idx_dtype, int64_t n_tokens,
+                        int64_t padding, float scale, void* grad, int64_t n_rows, int hd, int grad_dtype, unsigned flags,
+                        void* workspace, int64_t workspace_bytes, sdm_stream_t stream);
+
+/*
+ * sdm_gather_drows - gradient of the bank's rows in sdm_gather (or, of the values that its codes stand for,
+ * in sdm_qgather):
+ *     drows[r, :] = sum over operands o, live tokens t and entries n with idx[o][t, n] = r of w[o][t, n] * dout[o][t, :]
+ * summed, rounded and accumulated as in sdm_lookup_backward. Padding tokens (t % chunk >= valid) and entries of
+ * weight 0 take no part, whatever their dout holds; nor do indices outside [0, n_slots), which raise
+ * SDM_DEV_BAD_INDEX.
+ *
+ *   idx[o], w[o]  [tokens, width[o]], w dtype SDM_BF16 | SDM_F32; width[o] 1..256
+ *   dout[o]       [tokens, hd] float32
+ *   drows         [n_slots, hd] drows_dtype
+ *   tokens * (width[0] + width[1]) below 2^31, which is also the `entries` of the workspace
+ * Other arguments as sdm_gather.
+ */
+int sdm_gather_drows_workspace(int64_t entries, int64_t n_slots, int hd, int64_t* bytes);
+int sdm_gather_drows(int n_ops, const void* const idx[2], const void* const w[2], const float* const dout[2],
+                     const int width[2], int idx_dtype, int w_dtype, void* drows, int64_t n_slots, int hd, int drows_dtype,
+                     unsigned flags, int64_t tokens, int chunk, int valid, const int32_t* chunk_valid, void* workspace,
+                     int64_t workspace_bytes, sdm_stream_t stream);
 
 /* A static string naming a return code of the calls above. */
 const char* sdm_status_string(int status);
