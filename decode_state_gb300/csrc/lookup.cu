@@ -2,9 +2,8 @@
 //
 // Math (include/sdm.h): out[t] = round(scale * row(token[t])), zeros for a padding token.
 //
-// Design. A copy, bound by memory: a thread moves kUnits accesses of 16 bytes of the table, whose tokens and then
-// rows it loads together before it stores any. Consecutive threads take consecutive accesses of a row and then the
-// next row's, so that rows of any length leave no thread without work.
+// Design. A copy, bound by memory: a team of lanes moves 16 bytes of the table each, of ROWS rows at once, whose tokens
+// and then rows are loaded together before any is stored. Rows longer than 256 such accesses are shared by blocks.
 #include <algorithm>
 #include <climits>
 
@@ -17,7 +16,7 @@ namespace {
 
 __device__ unsigned int g_lookup_status;
 
-constexpr int kThreads = 256, kUnits = 4;
+constexpr int kThreads = 256;
 
 // V elements of type T moved together.
 template <typename T, int V>
@@ -25,55 +24,50 @@ struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
     T v[V];
 };
 
-template <typename T, typename O, int V>
+template <typename T, typename O, int V, int ROWS>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t from = (int64_t)blockIdx.x * (kThreads * kUnits);
-    const int64_t t0 = from / a.per_row;  // the block's first token, and the access of its row
-    const uint32_t first = (uint32_t)(from - t0 * a.per_row);
-    Pack<T, V> x[kUnits];
-    int64_t to[kUnits];
-    int64_t slot[kUnits];
+    const int lanes = 1 << a.lane_bits, teams = kThreads >> a.lane_bits, lane = threadIdx.x & (lanes - 1);
+    const int64_t group = blockIdx.x / a.column_blocks;
+    const int col = ((int)(blockIdx.x - group * a.column_blocks) * lanes + lane) * V;
+    const int64_t first = group * (teams * ROWS) + (threadIdx.x >> a.lane_bits);
+    if (col >= a.hd) return;
+    int64_t slot[ROWS];
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        const uint32_t at = first + threadIdx.x + u * kThreads;
-        const uint32_t row = a.magic ? __umulhi(at, a.magic) : at / a.per_row;
-        const int64_t t = t0 + row;
-        to[u] = t < a.n_tokens ? t * a.hd + (int64_t)(at - row * a.per_row) * V : -1;
-        slot[u] = -1;
-        if (to[u] >= 0) {
-            slot[u] = a.idx64 ? __ldg(static_cast<const int64_t*>(a.tokens) + t) : __ldg(static_cast<const int32_t*>(a.tokens) + t);
-            if (slot[u] == a.padding) {
-                slot[u] = -1;
-            } else if (slot[u] < 0 || slot[u] >= a.n_rows) {
-                slot[u] = -1;
-                atomicOr(&g_lookup_status, SDM_DEV_BAD_INDEX);
-            }
-            if (slot[u] >= 0) slot[u] = slot[u] * a.hd + (int64_t)(at - row * a.per_row) * V;
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t t = first + r * teams;
+        slot[r] = a.padding;
+        if (t < a.n_tokens) slot[r] = a.idx64 ? __ldg(static_cast<const int64_t*>(a.tokens) + t) : __ldg(static_cast<const int32_t*>(a.tokens) + t);
+    }
+    Pack<T, V> x[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const bool in = slot[r] >= 0 && slot[r] < a.n_rows;
+        if (!in && slot[r] != a.padding) atomicOr(&g_lookup_status, SDM_DEV_BAD_INDEX);
+        if (!in || slot[r] == a.padding) {
+            slot[r] = -1;
+#pragma unroll
+            for (int c = 0; c < V; ++c) x[r].v[c] = T(0);
+        } else {
+            x[r] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(a.table) + slot[r] * a.hd + col);
         }
     }
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        if (slot[u] >= 0)
-            x[u] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(a.table) + slot[u]);
-        else
-#pragma unroll
-            for (int c = 0; c < V; ++c) x[u].v[c] = T(0);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        if (to[u] < 0) continue;
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t t = first + r * teams;
+        if (t >= a.n_tokens) break;
         Pack<O, V> y;
 #pragma unroll
-        for (int c = 0; c < V; ++c) y.v[c] = from_f32<O>(slot[u] >= 0 ? to_f32(x[u].v[c]) * a.scale : 0.0f);
-        *reinterpret_cast<Pack<O, V>*>(static_cast<O*>(a.out) + to[u]) = y;
+        for (int c = 0; c < V; ++c) y.v[c] = slot[r] < 0 ? O(0) : from_f32<O>(to_f32(x[r].v[c]) * a.scale);
+        *reinterpret_cast<Pack<O, V>*>(static_cast<O*>(a.out) + t * a.hd + col) = y;
     }
 }
 
 template <typename T, typename O>
-const void* kernel(bool vec) {
-    return vec ? (const void*)lookup_kernel<T, O, 16 / sizeof(T)> : (const void*)lookup_kernel<T, O, 1>;
+const void* kernel(bool vec, bool many) {
+    constexpr int V = 16 / sizeof(T);
+    return vec ? (many ? (const void*)lookup_kernel<T, O, V, 4> : (const void*)lookup_kernel<T, O, V, 1>) : (const void*)lookup_kernel<T, O, 1, 4>;
 }
 
 }  // namespace
@@ -83,13 +77,23 @@ int launch_lookup(const LookupArgs& a0, cudaStream_t stream) {
     const int v = a.table_bf16 ? 8 : 4;
     const bool vec = a.hd % v == 0 && reinterpret_cast<uintptr_t>(a.table) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(a.out) % std::min(16, v * (a.out_bf16 ? 2 : 4)) == 0;
-    a.per_row = vec ? a.hd / v : a.hd;
-    // x * magic >> 32 is x / per_row for x < 2^32 / per_row, and x < per_row + 1024 here
-    a.magic = a.per_row > 1 && a.per_row <= 32768 ? (uint32_t)(((uint64_t)1 << 32) / a.per_row + 1) : 0;
-    const int64_t units = a.n_tokens * a.per_row, blocks = (units + kThreads * kUnits - 1) / (kThreads * kUnits);
+    const int accesses = vec ? a.hd / v : a.hd;
+    // of 8 to 256 lanes, the most that leave the fewest without work in a row's last access
+    a.lane_bits = 3;
+    for (int bits = 4, least = (accesses + 7) / 8 * 8; bits <= 8; ++bits) {
+        const int taken = (accesses + (1 << bits) - 1 >> bits) << bits;
+        if (taken <= least) {
+            least = taken;
+            a.lane_bits = bits;
+        }
+    }
+    a.column_blocks = (accesses + (1 << a.lane_bits) - 1) >> a.lane_bits;
+    const int teams = kThreads >> a.lane_bits;
+    const bool many = !vec || a.n_tokens * a.column_blocks >= (int64_t)8 * 4 * teams * sm_count();
+    const int64_t blocks = (a.n_tokens + teams * (many ? 4 : 1) - 1) / (teams * (many ? 4 : 1)) * a.column_blocks;
     if (blocks > INT_MAX) return SDM_ECOUNT;
-    const void* fn = a.table_bf16 ? (a.out_bf16 ? kernel<uint16_t, uint16_t>(vec) : kernel<uint16_t, float>(vec))
-                                  : (a.out_bf16 ? kernel<float, uint16_t>(vec) : kernel<float, float>(vec));
+    const void* fn = a.table_bf16 ? (a.out_bf16 ? kernel<uint16_t, uint16_t>(vec, many) : kernel<uint16_t, float>(vec, many))
+                                  : (a.out_bf16 ? kernel<float, uint16_t>(vec, many) : kernel<float, float>(vec, many));
     void* args[] = {&a};
     return launch_pdl_raw(fn, dim3((unsigned)blocks), dim3(kThreads), 0, stream, args);
 }

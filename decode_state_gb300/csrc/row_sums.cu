@@ -24,7 +24,6 @@ __device__ unsigned int g_row_sums_status;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr uint32_t kDirect = 512;    // entries that one launch sums
 constexpr uint32_t kRanked = 8192;   // entries ranked by counting
-constexpr int kItems = 16, kTile = kThreads * kItems;
 constexpr int kMostBits = 11;
 constexpr int kZeroRows = 256;       // rows that a block sets to zero, at most
 
@@ -171,18 +170,40 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
 // ---------------------------------------------------------------- the sort
 
 // Places by counting. A block takes 32 entries, a warp four of them, and compares with all.
-__global__ void __launch_bounds__(kThreads) rank_kernel(const RowSumArgs a, uint32_t* keys_out, uint32_t* ents_out) {
+__global__ void __launch_bounds__(kThreads) rank_kernel(const RowSumArgs a, uint2* sorted) {
     extern __shared__ uint32_t all[];
+    __shared__ int alive[kWarps];
     grid_dependency_wait();
     grid_launch_dependents();
     const int n = (int)a.entries, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int e = threadIdx.x; e < n; e += kThreads) all[e] = key_of(a, e);
+    int live = 0;
+    for (int e0 = threadIdx.x; e0 < n; e0 += 8 * kThreads) {
+        uint32_t key[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) key[i] = e0 + i * kThreads < n ? key_of(a, e0 + i * kThreads) : (uint32_t)a.n_slots;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (e0 + i * kThreads < n) all[e0 + i * kThreads] = key[i];
+            live += key[i] < a.n_slots;
+        }
+    }
+    if (blockIdx.x == 0) {
+        live = __reduce_add_sync(kAll, live);
+        if (lane == 0) alive[warp] = live;
+    }
     __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        live = 0;
+        for (int w = 0; w < kWarps; ++w) live += alive[w];
+        a.counters[0] = live;
+        a.counters[1] = 0;
+    }
     const int e0 = blockIdx.x * 32 + warp * 4;
     uint32_t key[4];
     int before[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int q = 0; q < 4; ++q) key[q] = e0 + q < n ? all[e0 + q] : 0u;
+#pragma unroll 4
     for (int i = lane; i < n; i += 32) {
         const uint32_t k = all[i];
 #pragma unroll
@@ -191,109 +212,49 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const RowSumArgs a, uint
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         before[q] = __reduce_add_sync(kAll, before[q]);
-        if (lane == q && e0 + q < n) {
-            keys_out[before[q]] = key[q];
-            ents_out[before[q]] = e0 + q;
-        }
+        if (lane == q && e0 + q < n && key[q] < a.n_slots) sorted[before[q]] = make_uint2(key[q], e0 + q);
     }
 }
 
-// The counts of a tile's digits, counts[digit * tiles + tile]. FIRST: the keys are made here and kept.
-template <bool FIRST>
-__global__ void __launch_bounds__(kThreads) digit_count_kernel(const RowSumArgs a, uint32_t* keys, uint32_t* counts, int shift, int bits) {
+// The digits of a pass.
+struct Digit {
+    int shift, bits;
+    __device__ __forceinline__ uint32_t of(uint32_t key) const { return key >> shift & ((1u << bits) - 1); }
+};
+
+// The counts of a tile's digits, counts[tile][digit]. FIRST: the keys are made here and kept, and entries
+// that take no part are not counted; later passes have the others only.
+template <bool FIRST, int ITEMS>
+__global__ void __launch_bounds__(kThreads) digit_count_kernel(const RowSumArgs a, uint32_t* keys, const uint2* in, uint32_t* counts, Digit digit) {
     __shared__ uint32_t bins[1 << kMostBits];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int all = 1 << bits;
+    const uint32_t entries = FIRST ? a.entries : a.counters[0], from = blockIdx.x * (uint32_t)(kThreads * ITEMS);
+    if (FIRST && blockIdx.x == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
+    const int all = 1 << digit.bits;
     for (int b = threadIdx.x; b < all; b += kThreads) bins[b] = 0;
     __syncthreads();
-    const uint32_t from = blockIdx.x * (uint32_t)kTile;
-#pragma unroll 4
-    for (int i = 0; i < kItems; ++i) {
+    uint32_t key[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
         const uint32_t e = from + i * kThreads + threadIdx.x;
-        if (e < a.entries) {
-            const uint32_t key = FIRST ? key_of(a, e) : keys[e];
-            if (FIRST) keys[e] = key;
-            atomicAdd(&bins[key >> shift & (all - 1)], 1u);
-        }
+        key[i] = (uint32_t)a.n_slots;
+        if (e < entries) key[i] = FIRST ? key_of(a, e) : in[e].x;
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const uint32_t e = from + i * kThreads + threadIdx.x;
+        if (FIRST && e < entries) keys[e] = key[i];
+        if (key[i] < a.n_slots) atomicAdd(&bins[digit.of(key[i])], 1u);
     }
     __syncthreads();
-    for (int b = threadIdx.x; b < all; b += kThreads) counts[(int64_t)b * gridDim.x + blockIdx.x] = bins[b];
+    for (int b = threadIdx.x; b < all; b += kThreads) counts[((int64_t)blockIdx.x << digit.bits) + b] = bins[b];
 }
 
-// Each digit's counts become their running sums over the tiles, and their total.
-__global__ void __launch_bounds__(kThreads) digit_scan_kernel(uint32_t* counts, uint32_t* totals, int tiles) {
-    __shared__ uint32_t sums[kWarps];
-    grid_dependency_wait();
-    grid_launch_dependents();
-    uint32_t* row = counts + (int64_t)blockIdx.x * tiles;
+// The sum of `own` over the block's threads before this one, and over all of them.
+__device__ __forceinline__ uint32_t sum_before(uint32_t own, uint32_t* sums, uint32_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t carry = 0;
-    for (int base = 0; base < tiles; base += kThreads) {
-        const int i = base + threadIdx.x;
-        const uint32_t own = i < tiles ? row[i] : 0u;
-        uint32_t sum = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(kAll, sum, o);
-            if (lane >= o) sum += y;
-        }
-        if (lane == 31) sums[warp] = sum;
-        __syncthreads();
-        uint32_t before = carry;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += sums[w];
-            carry += sums[w];
-        }
-        if (i < tiles) row[i] = before + sum - own;
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) totals[blockIdx.x] = carry;
-}
-
-// A tile's keys go to their places: behind all smaller digits, behind the same digit of earlier tiles, in order.
-__global__ void __launch_bounds__(kThreads) digit_place_kernel(uint32_t entries, const uint32_t* keys_in, const uint32_t* ents_in,
-                                                               uint32_t* keys_out, uint32_t* ents_out, const uint32_t* counts,
-                                                               const uint32_t* totals, int shift, int bits) {
-    __shared__ uint16_t own[kWarps][1 << kMostBits];
-    __shared__ uint32_t start[1 << kMostBits];
-    __shared__ uint32_t sums[kWarps];
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int all = 1 << bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int b = lane; b < all; b += 32) own[warp][b] = 0;
-    __syncwarp();
-    // a warp's keys are consecutive, 32 at a time
-    const uint32_t from = blockIdx.x * (uint32_t)kTile + warp * (32 * kItems);
-    uint32_t key[kItems];
-    uint16_t rank[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const uint32_t e = from + i * 32 + lane;
-        key[i] = e < entries ? keys_in[e] : 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const bool on = from + i * 32 + lane < entries;
-        const uint32_t d = key[i] >> shift & (all - 1);
-        unsigned same = __ballot_sync(kAll, on);  // lanes with the same digit
-        for (int b = 0; b < bits; ++b) {
-            const bool set = d >> b & 1;
-            const unsigned with = __ballot_sync(kAll, set);
-            same &= set ? with : ~with;
-        }
-        const uint32_t before = own[warp][d];
-        __syncwarp();
-        if (on && lane == 31 - __clz(same)) own[warp][d] = (uint16_t)(before + __popc(same));
-        __syncwarp();
-        rank[i] = (uint16_t)(before + __popc(same & ((1u << lane) - 1)));
-    }
-    __syncthreads();
-    // where each digit starts: running sums of the totals, eight consecutive digits a thread at most
-    const int per = (all + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
-    uint32_t mine = 0;
-    for (int b = b0; b < b0 + per && b < all; ++b) mine += __ldg(totals + b);
-    uint32_t sum = mine;
+    uint32_t sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(kAll, sum, o);
@@ -301,43 +262,200 @@ __global__ void __launch_bounds__(kThreads) digit_place_kernel(uint32_t entries,
     }
     if (lane == 31) sums[warp] = sum;
     __syncthreads();
-    uint32_t before = sum - mine;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-    for (int b = b0; b < b0 + per && b < all; ++b) {
-        start[b] = before + __ldg(counts + (int64_t)b * gridDim.x + blockIdx.x);
-        before += __ldg(totals + b);
-        uint32_t run = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            const uint32_t c = own[w][b];
-            own[w][b] = (uint16_t)run;
-            run += c;
+    uint32_t before = 0, every = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sums[w];
+        every += sums[w];
+    }
+    *total = every;
+    return before + sum - own;
+}
+
+// Each digit's counts become their running sums over the tiles, and their total. A block takes 32 digits, a lane
+// each; its warps share out the tiles.
+constexpr int kScanWarps = 32;
+__global__ void __launch_bounds__(32 * kScanWarps) digit_scan_kernel(uint32_t* counts, uint32_t* totals, int tiles, int bits) {
+    __shared__ uint32_t sums[kScanWarps][32];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = (tiles + kScanWarps - 1) / kScanWarps;
+    const int digit = blockIdx.x * 32 + lane, first = warp * share, last = min(first + share, tiles);
+    if (blockIdx.x * 32 >= 1u << bits) return;
+    const bool on = digit < 1 << bits;
+    uint32_t* column = counts + (on ? digit : 0);
+    uint32_t sum = 0;
+#pragma unroll 16
+    for (int t = first; t < last; ++t) sum += column[(int64_t)t << bits];
+    sums[warp][lane] = sum;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kScanWarps; ++w) {
+        if (w < warp) before += sums[w][lane];
+        all += sums[w][lane];
+    }
+    if (!on) return;
+    if (warp == 0) totals[digit] = all;
+    for (int t0 = first; t0 < last; t0 += 16) {
+        uint32_t own[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) own[i] = t0 + i < last ? column[(int64_t)(t0 + i) << bits] : 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (t0 + i < last) column[(int64_t)(t0 + i) << bits] = before;
+            before += own[i];
+        }
+    }
+}
+
+// A tile's entries go to their places: behind all smaller digits, behind the same digit of earlier tiles, in order. They
+// are put in order in shared memory first, so that what goes to one place is written side by side. SCANNED: counts are
+// running sums over the tiles, totals their ends; else a block adds up the counts of the few tiles itself.
+template <bool FIRST, bool SCANNED, int ITEMS>
+__global__ void __launch_bounds__(kThreads) digit_place_kernel(const RowSumArgs a, const uint32_t* keys, const uint2* in, uint2* out,
+                                                               const uint32_t* counts, const uint32_t* totals, Digit digit) {
+    constexpr int TILE = kThreads * ITEMS;
+    // a warp's counts of each digit; then the tile's entries
+    __shared__ union {
+        uint16_t own[kWarps][1 << kMostBits];
+        uint2 staged[TILE];
+    } m;
+    __shared__ uint32_t shift_of[1 << kMostBits];  // from an entry's place in the tile to its place in the output
+    __shared__ uint32_t sums[kWarps];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int all = 1 << digit.bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t entries = FIRST ? a.entries : a.counters[0], tile = blockIdx.x, tiles = gridDim.x;
+    if (tile * (uint32_t)TILE >= entries && !(FIRST && tile == 0)) return;
+    for (int b = lane * 2; b < all; b += 64) *reinterpret_cast<uint32_t*>(&m.own[warp][b]) = 0;
+    __syncwarp();
+    // a warp's entries are consecutive, 32 at a time
+    const uint32_t from = tile * (uint32_t)TILE + warp * (32 * ITEMS);
+    uint32_t key[ITEMS], ent[ITEMS];
+    uint16_t rank[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const uint32_t e = from + i * 32 + lane;
+        key[i] = (uint32_t)a.n_slots;
+        ent[i] = e;
+        if (e < entries) {
+            if constexpr (FIRST) {
+                key[i] = keys[e];
+            } else {
+                const uint2 pair = in[e];
+                key[i] = pair.x;
+                ent[i] = pair.y;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const bool on = key[i] < a.n_slots;
+        const uint32_t d = digit.of(key[i]);
+        unsigned same = __ballot_sync(kAll, on);  // lanes with the same digit
+        for (int b = 0; b < digit.bits; ++b) {
+            const bool set = d >> b & 1;
+            const unsigned with = __ballot_sync(kAll, set);
+            same &= set ? with : ~with;
+        }
+        const uint32_t before = m.own[warp][d];
+        __syncwarp();
+        if (on && lane == 31 - __clz(same)) m.own[warp][d] = (uint16_t)(before + __popc(same));
+        __syncwarp();
+        rank[i] = (uint16_t)(before + __popc(same & ((1u << lane) - 1)));
+    }
+    __syncthreads();
+    // Where each digit starts, among all entries and in the tile: running sums over the digits, up to eight consecutive
+    // ones a thread.
+    constexpr int PER = (1 << kMostBits) / kThreads;
+    const int per = (all + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
+    uint32_t total[PER], earlier[PER], of_all = 0, of_tile = 0, unused;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        total[i] = earlier[i] = 0;
+        const int b = b0 + i;
+        if (i < per && b < all) {
+            if constexpr (SCANNED) {
+                total[i] = __ldg(totals + b);
+                earlier[i] = __ldg(counts + ((int64_t)tile << digit.bits) + b);
+            } else {
+#pragma unroll 8
+                for (uint32_t t = 0; t < tiles; ++t) {
+                    const uint32_t c = __ldg(counts + ((int64_t)t << digit.bits) + b);
+                    total[i] += c;
+                    if (t < tile) earlier[i] += c;
+                }
+            }
+            of_all += total[i];
+            uint32_t run = 0;
+            for (int w = 0; w < kWarps; ++w) run += m.own[w][b];
+            of_tile += run;
+        }
+    }
+    uint32_t start = sum_before(of_all, sums, &unused), live;
+    if (FIRST && tile == 0 && threadIdx.x == 0) a.counters[0] = unused;
+    __syncthreads();
+    uint32_t local = sum_before(of_tile, sums, &live);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int b = b0 + i;
+        if (i < per && b < all) {
+            shift_of[b] = start + earlier[i] - local;
+            start += total[i];
+            for (int w = 0; w < kWarps; ++w) {
+                const uint32_t c = m.own[w][b];
+                m.own[w][b] = (uint16_t)local;
+                local += c;
+            }
         }
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const uint32_t e = from + i * 32 + lane;
-        if (e < entries) {
-            const uint32_t d = key[i] >> shift & (all - 1), to = start[d] + own[warp][d] + rank[i];
-            keys_out[to] = key[i];
-            ents_out[to] = ents_in != nullptr ? ents_in[e] : e;
-        }
+    for (int i = 0; i < ITEMS; ++i)
+        if (key[i] < a.n_slots) rank[i] += m.own[warp][digit.of(key[i])];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+        if (key[i] < a.n_slots) m.staged[rank[i]] = make_uint2(key[i], ent[i]);
+    __syncthreads();
+#pragma unroll 4
+    for (uint32_t p = threadIdx.x; p < live; p += kThreads) {
+        const uint2 pair = m.staged[p];
+        out[p + shift_of[digit.of(pair.x)]] = pair;
     }
 }
 
 // ---------------------------------------------------------------- the sums
 
-// The first place whose key is not below `key`, in keys[lo, hi).
-__device__ __forceinline__ uint32_t lower_bound(const uint32_t* keys, uint32_t lo, uint32_t hi, uint32_t key) {
+// The first place whose key is not below `key`, in sorted[lo, hi).
+__device__ __forceinline__ uint32_t lower_bound(const uint2* sorted, uint32_t lo, uint32_t hi, uint32_t key) {
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo) / 2;
-        if (__ldg(keys + mid) < key)
+        if (__ldg(&sorted[mid].x) < key)
             lo = mid + 1;
         else
             hi = mid;
     }
     return lo;
 }
+
+// The same by a warp, 32 places at a time.
+__device__ __forceinline__ uint32_t warp_lower_bound(const uint2* sorted, uint32_t n, uint32_t key) {
+    const int lane = threadIdx.x & 31;
+    uint32_t lo = 0, len = n;  // the answer is in [lo, lo + len]
+    while (len > 0) {
+        const uint32_t step = (len + 31) / 32, at = min((uint32_t)lane * step + step, len) - 1;  // the last of each of 32 shares
+        const bool below = __ldg(&sorted[lo + at].x) < key;
+        const int shares = __popc(__ballot_sync(kAll, below));
+        const uint32_t skip = min(shares * step, len);
+        lo += skip;
+        len = shares == 32 ? 0 : min(step, len - skip) - 1;  // the last of the share is not below
+    }
+    return lo;
+}
+
+constexpr uint32_t kShort = 32;  // entries of a run beyond the end of a piece that its warp sums as well
 
 template <typename D, typename O, int V>
 __global__ void __launch_bounds__(kThreads) sums_kernel(const RowSumArgs a, int zero_span) {
@@ -346,41 +464,69 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const RowSumArgs a, int 
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
+    const uint32_t entries = a.counters[0];
     if ((int64_t)blockIdx.x < a.zero_blocks) {
         const int64_t first = (int64_t)blockIdx.x * zero_span;
-        const int count = (int)min((int64_t)zero_span, a.n_slots - first);
-        if (threadIdx.x < 2) range[threadIdx.x] = lower_bound(a.keys, 0, a.entries, (uint32_t)(first + threadIdx.x * count));
+        const int count = (int)min((int64_t)zero_span, a.n_slots - first), warp = threadIdx.x >> 5;
+        if (warp < 2) range[warp] = warp_lower_bound(a.sorted, entries, (uint32_t)(first + warp * count));
+        for (int r = threadIdx.x; r < count; r += kThreads) touched[r] = 0;
         __syncthreads();
-        for (int r = threadIdx.x; r < count; r += kThreads) {
-            const uint32_t at = lower_bound(a.keys, range[0], range[1], (uint32_t)(first + r));
-            touched[r] = at < range[1] && __ldg(a.keys + at) == (uint32_t)(first + r);
+        const uint32_t lo = range[0], hi = range[1];
+        if (hi - lo <= 8 * kThreads) {
+            for (uint32_t i = lo + threadIdx.x; i < hi; i += kThreads) touched[__ldg(&a.sorted[i].x) - first] = 1;
+        } else {  // long runs: a search for each row
+            for (int r = threadIdx.x; r < count; r += kThreads) {
+                const uint32_t at = lower_bound(a.sorted, lo, hi, (uint32_t)(first + r));
+                touched[r] = at < hi && __ldg(&a.sorted[at].x) == (uint32_t)(first + r);
+            }
         }
         __syncthreads();
         zero_rows<O, V>(a, first, count, touched);
         return;
     }
     const int64_t unit = ((int64_t)blockIdx.x - a.zero_blocks) * kWarps + (threadIdx.x >> 5);
-    const uint32_t piece = (uint32_t)(unit / a.slices);
-    if (piece >= a.pieces) return;
-    const uint32_t from = piece * a.piece, to = min(from + a.piece, a.entries);
-    const int in_slice = lane * V, col = (int)(unit % a.slices) * a.slice_cols + in_slice;
+    const int64_t piece = unit / a.slices;
+    uint32_t from = (uint32_t)min(piece * a.piece, (int64_t)entries), to = (uint32_t)min((piece + 1) * a.piece, (int64_t)entries);
+    if (from >= to) return;
+    const int slice = (int)(unit % a.slices), in_slice = lane * V, col = slice * a.slice_cols + in_slice;
     const bool on = in_slice < a.slice_cols && col < a.hd;
-    uint32_t current = __ldg(a.keys + from);
-    if (current >= a.n_slots) return;
-    bool continues = from > 0 && __ldg(a.keys + from - 1) == current;
-    const uint32_t next = to < a.entries ? __ldg(a.keys + to) : 0xffffffffu;
+    // A run that began before this piece is summed by the warp before, if few of its entries are left here; else
+    // its part here goes to `heads`, to be joined.
+    bool continues = false;
+    if (from > 0) {
+        const uint32_t before = __ldg(&a.sorted[from - 1].x);
+        const bool same = from + lane < entries && __ldg(&a.sorted[from + lane].x) == before;
+        const unsigned rest = __ballot_sync(kAll, same);
+        if (rest == kAll)
+            continues = true;
+        else
+            from += __popc(rest);
+    }
+    bool goes_on = false;
+    if (to < entries) {
+        const uint32_t last = __ldg(&a.sorted[to - 1].x);
+        const bool same = to + lane < entries && __ldg(&a.sorted[to + lane].x) == last;
+        const unsigned rest = __ballot_sync(kAll, same);
+        if (rest == kAll)
+            goes_on = true;
+        else if (from < to)  // not all of the piece was the end of another's run
+            to += __popc(rest);
+    }
+    if (from >= to) return;
+    uint32_t current = __ldg(&a.sorted[from].x);
     float sum[V];
 #pragma unroll
     for (int c = 0; c < V; ++c) sum[c] = 0.0f;
     const auto flush = [&](bool ends) {
-        if (on) {
-            if (continues || !ends) {
-                float* part = (continues ? a.heads : a.tails) + (int64_t)piece * a.hd + col;
+        if (continues || !ends) {
+            if (on) {
+                float* part = (continues ? a.heads : a.tails) + piece * a.hd + col;
 #pragma unroll
                 for (int c = 0; c < V; ++c) part[c] = sum[c];
-            } else {
-                put_row<O, V>(a, current, col, sum);
             }
+            if (!continues && slice == 0 && lane == 0) a.list[atomicAdd(a.counters + 1, 1u)] = (uint32_t)piece;
+        } else if (on) {
+            put_row<O, V>(a, current, col, sum);
         }
         continues = false;
 #pragma unroll
@@ -388,18 +534,18 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const RowSumArgs a, int 
     };
     constexpr int U = 8;
     for (uint32_t base = from; base < to; base += 32) {
-        uint32_t key = 0xffffffffu;
+        uint32_t key = 0;
         float w = 0.0f;
         const D* row = nullptr;
         if (base + lane < to) {
-            key = __ldg(a.keys + base + lane);
-            if (key < a.n_slots) {
-                const Place p = place_of(a, __ldg(a.ents + base + lane));
-                w = weight_of(a, p.op, p.at);
-                row = static_cast<const D*>(p.op ? a.dout[1] : a.dout[0]) + (int64_t)p.token * a.hd;
-            }
+            const uint2 pair = __ldg(a.sorted + base + lane);
+            key = pair.x;
+            const Place p = place_of(a, pair.y);
+            w = weight_of(a, p.op, p.at);
+            row = static_cast<const D*>(p.op ? a.dout[1] : a.dout[0]) + (int64_t)p.token * a.hd;
         }
-        for (int j0 = 0; j0 < 32 && base + j0 < to; j0 += U) {  // U divides a piece: only the last one ends within
+        const int left = (int)min(to - base, 32u);
+        for (int j0 = 0; j0 < left; j0 += U) {
             Pack<D, V> x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -410,69 +556,64 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const RowSumArgs a, int 
             for (int u = 0; u < U; ++u) {
                 const uint32_t k = __shfl_sync(kAll, key, j0 + u);
                 const float f = __shfl_sync(kAll, w, j0 + u);
-                if (k != current) {
-                    if (current < a.n_slots) flush(true);
-                    current = k;
-                }
-                if (k < a.n_slots) {
+                if (j0 + u < left) {
+                    if (k != current) {
+                        flush(true);
+                        current = k;
+                    }
 #pragma unroll
                     for (int c = 0; c < V; ++c) sum[c] = fmaf(f, to_f32(x[u].v[c]), sum[c]);
                 }
             }
-            if (current >= a.n_slots) return;  // nothing but dropped entries, or the end of the last piece
         }
     }
-    flush(next != current);
+    flush(!goes_on);
 }
 
-// The runs that cross the ends of pieces: the sum in the piece where a run begins, then those that continue it. A
-// block for each piece and slice; its warps share out the pieces of a long run.
+// The listed runs, which go on far beyond the piece they begin in: the sum in that piece, then those in the pieces that
+// continue it. A block for each run and slice; its warps share out the pieces of a long run.
 template <typename O, int V>
 __global__ void __launch_bounds__(kThreads) join_kernel(const RowSumArgs a) {
     __shared__ float parts[kWarps][32 * V];
     grid_dependency_wait();
     grid_launch_dependents();
-    const uint32_t piece = blockIdx.x / a.slices, from = piece * a.piece, to = from + a.piece;
-    if (to >= a.entries) return;
-    const uint32_t key = __ldg(a.keys + to - 1);
-    if (key >= a.n_slots || __ldg(a.keys + to) != key) return;
-    if (from > 0 && __ldg(a.keys + from - 1) == key) return;  // it began earlier
-    // the pieces that begin with this slot: piece + 1 .. piece + more
-    uint32_t lo = piece + 1, hi = a.pieces;
-    while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (__ldg(a.keys + (int64_t)mid * a.piece) <= key)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    const uint32_t more = lo - piece - 1, share = (more + kWarps - 1) / kWarps;
+    const uint32_t entries = a.counters[0];
+    const int64_t units = (int64_t)a.counters[1] * a.slices;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int in_slice = lane * V, col = (int)(blockIdx.x % a.slices) * a.slice_cols + in_slice;
-    const bool on = in_slice < a.slice_cols && col < a.hd;
-    float sum[V];
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int64_t piece = a.list[unit / a.slices];
+        const uint32_t key = __ldg(&a.sorted[(piece + 1) * a.piece].x);
+        // the pieces that begin with this slot and go on with it for more than kShort entries
+        const uint32_t end = lower_bound(a.sorted, (uint32_t)((piece + 1) * a.piece), entries, key + 1);
+        const int64_t more = ((int64_t)end - kShort) / a.piece - piece, share = (more + kWarps - 1) / kWarps;
+        const int in_slice = lane * V, col = (int)(unit % a.slices) * a.slice_cols + in_slice;
+        const bool on = in_slice < a.slice_cols && col < a.hd;
+        float sum[V];
 #pragma unroll
-    for (int c = 0; c < V; ++c) sum[c] = 0.0f;
-    if (on) {
-        const uint32_t last = min((uint32_t)(warp + 1) * share, more);
+        for (int c = 0; c < V; ++c) sum[c] = 0.0f;
+        if (on) {
+            const int64_t last = min((warp + 1) * share, more);
 #pragma unroll 8
-        for (uint32_t q = warp * share; q < last; ++q) {
-            const float* part = a.heads + (int64_t)(piece + 1 + q) * a.hd + col;
+            for (int64_t q = warp * share; q < last; ++q) {
+                const float* part = a.heads + (piece + 1 + q) * a.hd + col;
 #pragma unroll
-            for (int c = 0; c < V; ++c) sum[c] += part[c];
+                for (int c = 0; c < V; ++c) sum[c] += part[c];
+            }
+#pragma unroll
+            for (int c = 0; c < V; ++c) parts[warp][in_slice + c] = sum[c];
         }
+        __syncthreads();
+        if (warp == 0 && on) {
+            const float* tail = a.tails + piece * a.hd + col;
 #pragma unroll
-        for (int c = 0; c < V; ++c) parts[warp][in_slice + c] = sum[c];
+            for (int c = 0; c < V; ++c) {
+                sum[c] = tail[c];
+                for (int w = 0; w < kWarps; ++w) sum[c] += parts[w][in_slice + c];
+            }
+            put_row<O, V>(a, key, col, sum);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    if (warp != 0 || !on) return;
-    const float* tail = a.tails + (int64_t)piece * a.hd + col;
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
-        sum[c] = tail[c];
-        for (int w = 0; w < kWarps; ++w) sum[c] += parts[w][in_slice + c];
-    }
-    put_row<O, V>(a, key, col, sum);
 }
 
 struct Kernels {
@@ -497,15 +638,83 @@ uint32_t piece_of(int64_t entries, int hd) {
 }
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
+// The passes of the sort over slots below n_slots. Tiles of 1024 entries, of which few entries make more blocks, else
+// of 4096, whose digits come in longer runs; up to 32 tiles are added up by each block that needs their sums.
+struct Radix {
+    int passes, bits, items;
+    int64_t tiles;
+    bool scanned;
+};
+Radix radix_of(int64_t entries, int64_t n_slots) {
+    int significant = 1;
+    while ((n_slots - 1) >> significant != 0) ++significant;
+    Radix r{};
+    r.passes = (significant + kMostBits - 1) / kMostBits;
+    r.bits = (significant + r.passes - 1) / r.passes;
+    r.items = entries <= 131072 ? 4 : 16;
+    r.tiles = (entries + kThreads * r.items - 1) / (kThreads * r.items);
+    r.scanned = r.tiles > 32;
+    return r;
+}
+
+// Where everything lies in the workspace, in words.
+struct Layout {
+    int64_t counters, pairs, keys, counts, totals, heads, tails, list, words;
+};
+Layout layout_of(int64_t entries, int64_t n_slots, int hd) {
+    const Radix radix = radix_of(entries, n_slots);
+    const bool sorted = entries > kRanked;
+    const int64_t e = round_up(entries, 64), piece = piece_of(entries, hd), pieces = (entries + piece - 1) / piece;
+    Layout l{};
+    l.pairs = l.counters + 64;
+    l.keys = l.pairs + (sorted ? 4 : 2) * e;
+    l.counts = l.keys + (sorted ? e : 0);
+    l.totals = l.counts + (sorted ? round_up((int64_t)radix.tiles << radix.bits, 64) : 0);
+    l.heads = l.totals + (sorted ? 1 << kMostBits : 0);
+    l.tails = l.heads + round_up(pieces * hd, 64);
+    l.list = l.tails + round_up(pieces * hd, 64);
+    l.words = l.list + round_up(pieces, 64);
+    return l;
+}
+
+template <bool FIRST, bool SCANNED>
+const void* place_kernel(int items) {
+    return items == 4 ? (const void*)digit_place_kernel<FIRST, SCANNED, 4> : (const void*)digit_place_kernel<FIRST, SCANNED, 16>;
+}
+
+// Sorts the entries; `sorted` becomes where they are.
+int launch_sort(const RowSumArgs& a, const Layout& l, uint32_t* words, const uint2** sorted, cudaStream_t stream) {
+    Radix r = radix_of(a.entries, a.n_slots);
+    uint32_t *keys = words + l.keys, *counts = words + l.counts, *totals = words + l.totals;
+    uint2* pairs[2] = {reinterpret_cast<uint2*>(words + l.pairs), reinterpret_cast<uint2*>(words + l.pairs) + round_up(a.entries, 64)};
+    RowSumArgs args = a;
+    for (int p = 0; p < r.passes; ++p) {
+        Digit digit{p * r.bits, r.bits};
+        uint2 *in = pairs[~p & 1], *out = pairs[p & 1];
+        void* count_args[] = {&args, &keys, &in, &counts, &digit};
+        const void* count = p == 0 ? (r.items == 4 ? (const void*)digit_count_kernel<true, 4> : (const void*)digit_count_kernel<true, 16>)
+                                   : (r.items == 4 ? (const void*)digit_count_kernel<false, 4> : (const void*)digit_count_kernel<false, 16>);
+        int rc = launch_pdl_raw(count, dim3(r.tiles), dim3(kThreads), 0, stream, count_args);
+        if (rc == 0 && r.scanned) {
+            int tiles = (int)r.tiles;
+            void* scan_args[] = {&counts, &totals, &tiles, &r.bits};
+            rc = launch_pdl_raw((const void*)digit_scan_kernel, dim3(((1u << r.bits) + 31) / 32), dim3(32 * kScanWarps), 0, stream, scan_args);
+        }
+        if (rc != 0) return rc;
+        void* place_args[] = {&args, &keys, &in, &out, &counts, &totals, &digit};
+        const void* place = p == 0 ? (r.scanned ? place_kernel<true, true>(r.items) : place_kernel<true, false>(r.items))
+                                   : (r.scanned ? place_kernel<false, true>(r.items) : place_kernel<false, false>(r.items));
+        rc = launch_pdl_raw(place, dim3(r.tiles), dim3(kThreads), 0, stream, place_args);
+        if (rc != 0) return rc;
+        *sorted = out;
+    }
+    return 0;
+}
+
 }  // namespace
 
 int64_t row_sums_workspace(int64_t entries, int64_t n_slots, int hd) {
-    (void)n_slots;
-    if (entries <= kDirect) return 0;
-    const int64_t e = round_up(entries, 64), tiles = (entries + kTile - 1) / kTile, piece = piece_of(entries, hd);
-    const int64_t pieces = (entries + piece - 1) / piece;
-    const int64_t sort = entries <= kRanked ? 2 * e : 4 * e + round_up((tiles + 1) << kMostBits, 64);
-    return 4 * (sort + 2 * round_up(pieces * hd, 64));
+    return entries <= kDirect ? 0 : 4 * layout_of(entries, n_slots, hd).words;
 }
 
 int launch_row_sums(const RowSumArgs& a0, cudaStream_t stream) {
@@ -528,61 +737,36 @@ int launch_row_sums(const RowSumArgs& a0, cudaStream_t stream) {
     // rows that a block sets to zero: 128 KB of them
     int zero_span = (int)std::clamp<int64_t>((int64_t)128 * 1024 / ((int64_t)a.hd * (a.out_bf16 ? 2 : 4)), 8, kZeroRows);
     a.zero_blocks = a.accumulate ? 0 : (a.n_slots + zero_span - 1) / zero_span;
-    int rc;
     if (a.entries <= kDirect) {
         const int64_t blocks = a.zero_blocks + ((int64_t)a.entries * a.slices + kWarps - 1) / kWarps;
         if (blocks == 0) return 0;
         void* args[] = {&a, &zero_span};
         return launch_pdl_raw(fn.direct, dim3((unsigned)blocks), dim3(kThreads), 0, stream, args);
     }
-    const int64_t e = round_up(a.entries, 64);
+    const Layout l = layout_of(a.entries, a.n_slots, a.hd);
     uint32_t* words = static_cast<uint32_t*>(a.workspace);
-    if (a.entries <= kRanked) {
-        uint32_t *keys = words, *ents = words + e;
-        void* args[] = {&a, &keys, &ents};
-        rc = launch_pdl_raw((const void*)rank_kernel, dim3((a.entries + 31) / 32), dim3(kThreads), a.entries * 4, stream, args);
-        if (rc != 0) return rc;
-        a.keys = keys;
-        a.ents = ents;
-        words += 2 * e;
-    } else {
-        int tiles = (int)((a.entries + (int64_t)kTile - 1) / kTile);
-        uint32_t *keys[2] = {words, words + e}, *ents[2] = {words + 2 * e, words + 3 * e};
-        uint32_t *totals = words + 4 * e, *counts = totals + (1 << kMostBits);
-        int significant = 1;
-        while ((a.n_slots >> significant) != 0) ++significant;  // n_slots itself is a key
-        const int passes = (significant + kMostBits - 1) / kMostBits;
-        int bits = (significant + passes - 1) / passes;
-        for (int p = 0; p < passes; ++p) {
-            int shift = p * bits;
-            uint32_t *in = keys[p & 1], *out = keys[~p & 1], *ents_in = p ? ents[p & 1] : nullptr, *ents_out = ents[~p & 1];
-            void* count_args[] = {&a, &in, &counts, &shift, &bits};
-            rc = launch_pdl_raw(p ? (const void*)digit_count_kernel<false> : (const void*)digit_count_kernel<true>, dim3(tiles),
-                                dim3(kThreads), 0, stream, count_args);
-            if (rc != 0) return rc;
-            void* scan_args[] = {&counts, &totals, &tiles};
-            rc = launch_pdl_raw((const void*)digit_scan_kernel, dim3(1u << bits), dim3(kThreads), 0, stream, scan_args);
-            if (rc != 0) return rc;
-            uint32_t entries = a.entries;
-            void* place_args[] = {&entries, &in, &ents_in, &out, &ents_out, &counts, &totals, &shift, &bits};
-            rc = launch_pdl_raw((const void*)digit_place_kernel, dim3(tiles), dim3(kThreads), 0, stream, place_args);
-            if (rc != 0) return rc;
-        }
-        a.keys = keys[passes & 1];
-        a.ents = ents[passes & 1];
-        words += 4 * e + round_up((int64_t)(tiles + 1) << kMostBits, 64);
-    }
+    a.counters = words + l.counters;
+    a.heads = reinterpret_cast<float*>(words + l.heads);
+    a.tails = reinterpret_cast<float*>(words + l.tails);
+    a.list = words + l.list;
     a.piece = piece_of(a.entries, a.hd);
-    a.pieces = (a.entries + a.piece - 1) / a.piece;
-    a.heads = reinterpret_cast<float*>(words);
-    a.tails = a.heads + round_up((int64_t)a.pieces * a.hd, 64);
-    const int64_t blocks = a.zero_blocks + ((int64_t)a.pieces * a.slices + kWarps - 1) / kWarps;
-    if (blocks > INT_MAX || (int64_t)a.pieces * a.slices > INT_MAX) return SDM_ECOUNT;
+    const int64_t pieces = ((int64_t)a.entries + a.piece - 1) / a.piece, blocks = a.zero_blocks + (pieces * a.slices + kWarps - 1) / kWarps;
+    if (blocks > INT_MAX) return SDM_ECOUNT;
+    int rc;
+    if (a.entries <= kRanked) {
+        uint2* sorted = reinterpret_cast<uint2*>(words + l.pairs);
+        void* args[] = {&a, &sorted};
+        rc = launch_pdl_raw((const void*)rank_kernel, dim3((a.entries + 31) / 32), dim3(kThreads), a.entries * 4, stream, args);
+        a.sorted = sorted;
+    } else {
+        rc = launch_sort(a, l, words, &a.sorted, stream);
+    }
+    if (rc != 0) return rc;
     void* args[] = {&a, &zero_span};
     rc = launch_pdl_raw(fn.sums, dim3((unsigned)blocks), dim3(kThreads), 0, stream, args);
     if (rc != 0) return rc;
-    void* join_args[] = {&a};
-    return launch_pdl_raw(fn.join, dim3(a.pieces * (uint32_t)a.slices), dim3(kThreads), 0, stream, join_args);
+    const int64_t joins = std::min<int64_t>(pieces * a.slices, 2 * sm_count());
+    return launch_pdl_raw(fn.join, dim3((unsigned)joins), dim3(kThreads), 0, stream, args);
 }
 
 cudaError_t row_sums_status(void** word) { return cudaGetSymbolAddress(word, g_row_sums_status); }

@@ -161,7 +161,7 @@ struct LookupArgs {
     int hd;
     float scale;
     int table_bf16, out_bf16, idx64;
-    uint32_t per_row, magic;  // accesses of a row, and 2^32 over it rounded up
+    int lane_bits, column_blocks;  // lanes that move a row, or a block's columns of it; blocks that share a row
 };
 
 // Sums of weighted rows by slot: the gradient of an embedding table, or of the bank in a gather.
@@ -180,13 +180,14 @@ struct RowSumArgs {
     float scale;
     void* out;
     void* workspace;
-    // the entries, sorted by slot (a dropped entry's is n_slots), and the pieces of them that are summed at a time
     uint32_t entries, split;  // all, and those of the first operand
-    const uint32_t* keys;
-    const uint32_t* ents;
-    uint32_t piece, pieces;
-    float* heads;  // [pieces, hd]: sums of the run that a piece continues
-    float* tails;  // [pieces, hd]: of the run that a piece begins and does not end
+    // in the workspace
+    uint32_t* counters;   // entries that take part; runs to join
+    const uint2* sorted;  // (slot, entry) of those that take part
+    uint32_t piece;       // sorted entries that a warp sums
+    float* heads;         // [pieces, hd]: sums of the run that a piece continues
+    float* tails;         // [pieces, hd]: of the run that a piece begins and others continue
+    uint32_t* list;       // the pieces with such a tail
     int slices, slice_cols;
     int64_t zero_blocks;
 };
