@@ -128,18 +128,18 @@ __device__ __forceinline__ float exp_score(float x) {
     return y;
 }
 
-// A token's row for a team of TEAM threads (lanes of a warp, or a block), E logits a thread from one read to the
-// gradient's write (E 0: rows too long for that are read again). VEC: 16 bytes an access, for rows that start on
-// 16-byte boundaries; else 4. An access holds V consecutive entries, thread tid has those from (i * TEAM + tid) * V on.
+// A token's row for a team of TEAM threads (lanes of a warp, or a block). VEC: 16 bytes an access, for rows that start
+// on 16-byte boundaries; else 4. An access holds V consecutive entries, thread tid has those from (i * TEAM + tid) * V on.
+// Lanes of a warp keep the row in registers, E logits each, a block in shared memory (each thread what is its own).
 template <int TEAM, int E, bool VEC, typename L>
 struct Row {
-    static constexpr int V = (VEC ? 16 : 4) / sizeof(L), W = V * sizeof(L) / 4, LANES = TEAM <= 32 ? TEAM : 32, WARPS = TEAM <= 32 ? 1 : TEAM / 32;
-    static constexpr int R = E > 0 ? E : V, RAW = R / V * W;
+    static constexpr int V = (VEC ? 16 : 4) / sizeof(L), W = V * sizeof(L) / 4, WARPS = TEAM <= 32 ? 1 : TEAM / 32;
+    static constexpr int RAW = E / V * W;  // words of a lane's share
 
     int n, tid;
-    bool softmax, words;  // words: 4-byte accesses of two bf16 are aligned
+    bool words;  // 4-byte accesses of two bf16 are aligned
 
-    __device__ __forceinline__ Row(const BalanceArgs& a, int tid_) : n(a.n), tid(tid_), softmax(a.score == SDM_SOFTMAX) {
+    __device__ __forceinline__ Row(const BalanceArgs& a, int tid_) : n(a.n), tid(tid_) {
         words = VEC || V == 1 ||
                 ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits) | reinterpret_cast<uintptr_t>(a.add)) % 4 == 0 &&
                  ((a.row_stride | (a.dlogits ? a.dlogits_stride : 0) | (a.add ? a.add_stride : 0)) * sizeof(L)) % 4 == 0);
@@ -200,161 +200,39 @@ struct Row {
                 if (j + c < n) row[j + c] = from_f32<L>(d[c]);
         }
     }
-    // all of a thread's share of a row (none of it where the team has no row)
-    __device__ __forceinline__ void get_all(const L* row, bool on, uint32_t* w, uint32_t fill) const {
-#pragma unroll
-        for (int i = 0; i < R / V; ++i) get(row, on ? column(i) : n, w + i * W, fill);
-    }
 
-    // the largest m of the team, the sums z and d of what is relative to each thread's own m
-    __device__ __forceinline__ void join(bool soft, float& m, float& z, float& d, float (*joint)[WARPS]) const {
-        if (TEAM < 32 ? __any_sync(kAll, soft) : soft) {
-            const float mine = m;
-            m = warp_max<LANES>(m);
-            const float scale = soft ? exp_below(mine, m) : 1.0f;
-            z *= scale;
-            d *= scale;
-        }
-        z = warp_sum<LANES>(z);
-        d = warp_sum<LANES>(d);
-        if constexpr (TEAM > 32) {
-            if ((tid & 31) == 0) {
-                joint[0][tid >> 5] = m;
-                joint[1][tid >> 5] = z;
-                joint[2][tid >> 5] = d;
-            }
-            __syncthreads();
-            const int lane = tid & 31, w = lane % WARPS;  // every warp for itself
-            const float theirs = joint[0][w];
-            m = warp_max<WARPS>(theirs);
-            const float scale = lane >= WARPS ? 0.0f : soft ? exp_below(theirs, m) : 1.0f;
-            z = warp_sum(joint[1][w] * scale);
-            d = warp_sum(joint[2][w] * scale);
+    // Of V logits: their scores, those of a softmax relative to m, added to z and, times their counts, to d; `kept` is what
+    // the gradient takes of each: the score, times what a sigmoid leaves to one.
+    static __device__ __forceinline__ void soft_scores(const float* y, float m, const float* c, float* kept, float& z, float& d) {
+        const bool plain = fabsf(m) <= 3.402823466e38f;  // neither +inf nor masked throughout
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            kept[v] = plain ? exp_score<L>(fmaxf(y[v], minus_inf()) - m) : exp_below(y[v], m);  // NaN is masked
+            z += kept[v];
+            d = fmaf(kept[v], c[v], d);
         }
     }
-
-    // What the row adds to its sequence's loss, and its gradient where GRAD. `raw` holds the row (E 0: nothing); counts(i, j, c)
-    // gives the counts less their mean of the V entries of access i, which start with entry j; `joint` is
-    // shared memory that the team is done with.
-    template <bool GRAD, typename C>
-    __device__ __forceinline__ float pass(const L* row, uint32_t* raw, bool on, const C& counts, float unit, float g, L* out, const L* add,
-                                          float (*joint)[WARPS]) const {
-        uint32_t adds[RAW];
-        constexpr bool EARLY = GRAD && E > 0 && TEAM <= 32 && RAW <= 8;  // what is added is on its way meanwhile
-        if (EARLY && add != nullptr) get_all(add, on, adds, 0u);
-        // Sigmoid scores so small that their sum loses bits are shares of exp(x) instead, as for a softmax.
-        bool soft = softmax;
-        float x[GRAD && E > 0 ? R : 1];  // scores; s (1 - s) of a sigmoid
-        float m, mine, z, d;
-        for (;;) {
-            m = minus_inf();
-            z = d = 0.0f;
-            // f(access, first column, its V logits)
-            const auto each = [&](const auto& f) {
-                if constexpr (E > 0) {
+    static __device__ __forceinline__ void sigmoid_scores(const float* y, const float* c, float* kept, float& z, float& d) {
 #pragma unroll
-                    for (int i = 0; i < R / V; ++i) {
-                        float y[V];
-                        unpack(raw + i * W, y);
-                        f(i, column(i), y);
-                    }
-                } else {
-#pragma unroll 4
-                    for (int i = 0; column(i) < n; ++i) {
-                        uint32_t w[W];
-                        float y[V];
-                        get(row, column(i), w, kNone);
-                        unpack(w, y);
-                        f(i, column(i), y);
-                    }
-                }
-            };
-            if (soft)
-                each([&](int, int, const float* y) {
-#pragma unroll
-                    for (int c = 0; c < V; ++c) m = fmaxf(m, y[c]);  // NaN is left out
-                });
-            const bool plain = fabsf(m) <= 3.402823466e38f;  // neither +inf nor masked throughout
-            const float below = plain ? m : 0.0f;
-            each([&](int i, int j, const float* y) {
-                float c[V];
-                counts(i, j, c);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float logit = fmaxf(y[v], minus_inf());  // NaN is masked
-                    float s, kept;
-                    if (soft) {
-                        s = kept = plain ? exp_score<L>(logit - below) : exp_below(logit, m);
-                    } else {  // t = 0 and s = 0 where masked
-                        const float t = exp_score<L>(-fabsf(logit));
-                        float r;
-                        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
-                        const float tr = t * r;
-                        s = logit < 0.0f ? tr : r;
-                        kept = tr * r;
-                    }
-                    if constexpr (GRAD && E > 0) x[i * V + v] = kept;
-                    z += s;
-                    d = fmaf(s, c[v], d);
-                }
-            });
-            mine = m;
-            join(soft, m, z, d, joint);
-            const bool low = on && !soft && z < 0x1p-100f;
-            if (!(TEAM <= 32 ? __any_sync(kAll, low) : low)) break;
-            if constexpr (TEAM > 32) __syncthreads();  // joint is written again
-            soft |= low;
+        for (int v = 0; v < V; ++v) {
+            const float logit = fmaxf(y[v], minus_inf()), t = exp_score<L>(-fabsf(logit));  // t = 0 and s = 0 where masked
+            float r;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));  // 1 ulp
+            const float tr = t * r, s = logit < 0.0f ? tr : r;
+            kept[v] = tr * r;
+            z += s;
+            d = fmaf(s, c[v], d);
         }
-        const float mean = z > 0.0f ? __fdiv_rn(d, z) : 0.0f;
-        if constexpr (GRAD) {
-            if (on) {
-                const float gz = z > 0.0f ? __fdiv_rn(g, z) * (soft ? exp_below(mine, m) : 1.0f) : 0.0f, gm = -gz * mean;
-                const auto write = [&](int i, int j, const float* kept) {
-                    float c[V], y[V];
-                    counts(i, j, c);
-                    if (add != nullptr) {
-                        if constexpr (EARLY) {
-                            unpack(adds + i * W, y);
-                        } else {
-                            uint32_t w[W];
-                            get(add, j, w, 0u);
-                            unpack(w, y);
-                        }
-                    } else {
+    }
+    // The gradient of V logits, from what was kept of them.
+    static __device__ __forceinline__ void gradient(float* kept, const float* c, float gz, float gm, const float* add) {
 #pragma unroll
-                        for (int v = 0; v < V; ++v) y[v] = 0.0f;
-                    }
-#pragma unroll
-                    for (int v = 0; v < V; ++v) y[v] = fmaf(kept[v], fmaf(gz, c[v], gm), y[v]);
-                    put(out, j, y);
-                };
-                if constexpr (E > 0) {
-#pragma unroll
-                    for (int i = 0; i < R / V; ++i) write(i, column(i), x + i * V);
-                } else {
-                    for (int i = 0; column(i) < n; ++i) {
-                        uint32_t w[W];
-                        float y[V];
-                        get(row, column(i), w, kNone);
-                        unpack(w, y);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            const float logit = fmaxf(y[v], minus_inf());
-                            if (soft) {
-                                y[v] = exp_below(logit, mine);
-                            } else {
-                                const float t = exp_score<L>(-fabsf(logit)), r = __frcp_rn(1.0f + t);
-                                y[v] = t * r * r;
-                            }
-                        }
-                        write(i, column(i), y);
-                    }
-                }
-            }
-        }
-        return z > 0.0f ? fmaf(unit, mean, 1.0f) : 0.0f;
+        for (int v = 0; v < V; ++v) kept[v] = fmaf(kept[v], fmaf(gz, c[v], gm), add[v]);
     }
 };
+
+// Sums of sigmoid scores below this lose bits; the row's shares are then those of exp(x), as for a softmax.
+constexpr float kLowScores = 0x1p-60f;
 
 // A sequence's factors: the mean of its counts, its inverse, and what its gradient is multiplied by.
 struct Factors {
@@ -389,75 +267,278 @@ __device__ __forceinline__ void centred(const int32_t* counts, int n, bool whole
     }
 }
 
-// Blocks an SM that the registers are bounded for.
-constexpr int rows_blocks(int team, int e) { return team <= 128 ? (team <= 32 && e >= 32 ? 6 : 8) : team == 256 ? 4 : 2; }
+// What the tokens of a team's run share: the sequence that they are in, and the sum of their parts of its loss.
+struct Run {
+    Sequence q{-1, 0, 0};
+    Factors f{0.0f, 0.0f, 0.0f};
+    float sum = 0.0f;
 
-// A team takes a run of consecutive tokens; rows of the next token are on their way while a warp works on one.
+    // Token t is next; true where another sequence begins.
+    __device__ __forceinline__ bool next(const BalanceArgs& a, int64_t t, int64_t team, bool writes) {
+        if (t >= q.begin && t < q.end) return false;
+        done(a, team, writes);
+        sum = 0.0f;
+        q = sequence_of(a.offsets, a.sequences, a.tokens, t);
+        f = q.s >= 0 ? factors_of(a, q.s, q.end - q.begin, __ldg(a.totals + q.s)) : Factors{0.0f, 0.0f, 0.0f};
+        return true;
+    }
+    __device__ __forceinline__ void done(const BalanceArgs& a, int64_t team, bool writes) const {
+        if (q.s >= 0 && writes) a.parts[team + q.s] = sum;
+    }
+};
+
+// Rows of up to 512 entries: TEAM lanes a row, E logits each. The next token's row is on its way while a warp
+// works on one, and the counts of the sequence stay in registers.
 template <int TEAM, int E, bool VEC, bool GRAD, typename L>
-__global__ void __launch_bounds__(TEAM <= 32 ? 128 : TEAM, rows_blocks(TEAM, E)) balance_rows_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(128, E <= 8 ? (sizeof(L) == 2 && VEC ? 8 : 6) : 5) balance_lanes_kernel(const BalanceArgs a) {
     using R = Row<TEAM, E, VEC, L>;
-    constexpr int NT = TEAM <= 32 ? 128 : TEAM, TEAMS = NT / TEAM, V = R::V;
-    constexpr bool KEPT = TEAM <= 32 && E <= 16;          // the sequence's counts stay in registers
-    constexpr bool AHEAD = TEAM <= 32 && R::RAW <= 8;     // the next row is loaded early
-    __shared__ float joint[2][3][R::WARPS];
+    constexpr int TEAMS = 128 / TEAM, V = R::V, ACCESSES = E / V;
+    constexpr bool AHEAD = R::RAW <= 8;
     grid_dependency_wait();
     grid_launch_dependents();
     const R r(a, threadIdx.x % TEAM);
     const int64_t team = (int64_t)blockIdx.x * TEAMS + threadIdx.x / TEAM, first = team * a.rows;
-    const bool whole = reinterpret_cast<uintptr_t>(a.counts) % 16 == 0 && a.n % 4 == 0;
-    Sequence q{-1, 0, 0};
-    Factors f{0.0f, 0.0f, 0.0f};
-    float sum = 0.0f;
-    float kept[KEPT ? R::R : 1];
+    const bool whole = reinterpret_cast<uintptr_t>(a.counts) % 16 == 0 && a.n % 4 == 0, softmax = a.score == SDM_SOFTMAX;
+    Run run;
+    float counts[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) counts[e] = 0.0f;
     uint32_t raw[R::RAW], next[AHEAD ? R::RAW : 1];
-    const auto row_of = [&](int64_t t) { return static_cast<const L*>(a.logits) + (t < a.tokens ? t : 0) * a.row_stride; };
-    if constexpr (AHEAD) r.get_all(row_of(first), first < a.tokens, next, R::kNone);
-    for (int64_t i = 0; i < a.rows; ++i) {
+    const auto get_all = [&](const L* row, bool on, uint32_t* w, uint32_t fill) {
+#pragma unroll
+        for (int i = 0; i < ACCESSES; ++i) r.get(row, on ? r.column(i) : r.n, w + i * R::W, fill);
+    };
+    const L* row = static_cast<const L*>(a.logits) + (first < a.tokens ? first : 0) * a.row_stride;
+    if constexpr (AHEAD) get_all(row, first < a.tokens, next, R::kNone);
+    const int count = (int)min(a.rows, max(a.tokens - first, (int64_t)0)), steps = __reduce_max_sync(kAll, count);
+    for (int i = 0; i < steps; ++i) {  // lanes of a warp that hold several teams stay together
         const int64_t t = first + i;
-        const bool on = t < a.tokens;
-        if (TEAM >= 32 && !on) break;  // lanes of a warp that hold several teams stay together
+        const bool on = i < count;
         if constexpr (AHEAD) {
 #pragma unroll
             for (int w = 0; w < R::RAW; ++w) raw[w] = next[w];
-            r.get_all(row_of(t + 1), i + 1 < a.rows && t + 1 < a.tokens, next, R::kNone);
-        } else if constexpr (E > 0) {
-            r.get_all(row_of(t), on, raw, R::kNone);
+            get_all(row + a.row_stride, i + 1 < count, next, R::kNone);
+        } else {
+            get_all(row, on, raw, R::kNone);
         }
-        if (on && (t < q.begin || t >= q.end)) {
-            if (q.s >= 0 && r.tid == 0) a.parts[team + q.s] = sum;
-            sum = 0.0f;
-            q = sequence_of(a.offsets, a.sequences, a.tokens, t);
-            f = q.s >= 0 ? factors_of(a, q.s, q.end - q.begin, __ldg(a.totals + q.s)) : Factors{0.0f, 0.0f, 0.0f};
-            if constexpr (KEPT) {
+        uint32_t adds[GRAD ? R::RAW : 1];
+        if (GRAD && a.add != nullptr) get_all(static_cast<const L*>(a.add) + (on ? t : 0) * a.add_stride, on, adds, 0u);
+        if (on && run.next(a, t, team, r.tid == 0)) {
 #pragma unroll
-                for (int e = 0; e < R::R; e += V) {
-                    if (q.s >= 0) {
-                        centred<V>(a.counts + q.s * a.n, a.n, whole, f.centre, r.column(e / V), kept + e);
-                    } else {
+            for (int e = 0; e < E; e += V) {
+                if (run.q.s >= 0) {
+                    centred<V>(a.counts + run.q.s * a.n, a.n, whole, run.f.centre, r.column(e / V), counts + e);
+                } else {
 #pragma unroll
-                        for (int c = 0; c < V; ++c) kept[e + c] = 0.0f;
-                    }
+                    for (int v = 0; v < V; ++v) counts[e + v] = 0.0f;
                 }
             }
         }
         __syncwarp();
-        const int32_t* from = q.s >= 0 ? a.counts + q.s * a.n : nullptr;
-        const auto counts = [&](int access, int j, float* c) {
-            if constexpr (KEPT) {
+        float kept[E], m = 0.0f, z = 0.0f, d = 0.0f;
+        // the shares of exp(x), in all lanes of the warp; `mine`: in this team's
+        const auto soft = [&](bool mine) {
+            float top = minus_inf(), zs = 0.0f, ds = 0.0f, y[E], e[E];
 #pragma unroll
-                for (int v = 0; v < V; ++v) c[v] = kept[access * V + v];
-            } else if (from != nullptr) {
-                centred<V>(from, a.n, whole, f.centre, j, c);
+            for (int i2 = 0; i2 < ACCESSES; ++i2) R::unpack(raw + i2 * R::W, y + i2 * V);
+#pragma unroll
+            for (int i2 = 0; i2 < E; ++i2) top = fmaxf(top, y[i2]);  // NaN is left out
+            top = warp_max<TEAM>(top);
+#pragma unroll
+            for (int i2 = 0; i2 < E; i2 += V) R::soft_scores(y + i2, top, counts + i2, e + i2, zs, ds);
+            zs = warp_sum<TEAM>(zs);
+            ds = warp_sum<TEAM>(ds);
+            if (mine) {
+                m = top, z = zs, d = ds;
+#pragma unroll
+                for (int i2 = 0; i2 < E; ++i2) kept[i2] = e[i2];
+            }
+        };
+        if (softmax) {
+            soft(true);
+        } else {
+#pragma unroll
+            for (int i2 = 0; i2 < ACCESSES; ++i2) {
+                float y[V];
+                R::unpack(raw + i2 * R::W, y);
+                R::sigmoid_scores(y, counts + i2 * V, kept + i2 * V, z, d);
+            }
+            z = warp_sum<TEAM>(z);
+            d = warp_sum<TEAM>(d);
+            const bool low = on && z < kLowScores;
+            if (__any_sync(kAll, low)) soft(low);
+        }
+        const float inverse = z > 0.0f ? __frcp_rn(z) : 0.0f, mean = d * inverse;
+        if (z > 0.0f) run.sum += fmaf(run.f.unit, mean, 1.0f);
+        if (GRAD && on) {
+            L* out = static_cast<L*>(a.dlogits) + t * a.dlogits_stride;
+            const float gz = run.f.g * inverse, gm = -gz * mean;
+#pragma unroll
+            for (int i2 = 0; i2 < ACCESSES; ++i2) {
+                float add[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) add[v] = 0.0f;
+                if (a.add != nullptr) R::unpack(adds + i2 * R::W, add);
+                R::gradient(kept + i2 * V, counts + i2 * V, gz, gm, add);
+                r.put(out, r.column(i2), kept + i2 * V);
+            }
+        }
+        row += a.row_stride;
+    }
+    run.done(a, team, r.tid == 0);
+}
+
+// Longer rows: a block a row. What the gradient takes of each logit waits in shared memory (STAGED) between the
+// sums and the gradient; rows too long for that are read again.
+template <int TEAM, bool VEC, bool GRAD, bool STAGED, typename L>
+__global__ void __launch_bounds__(TEAM, 1024 / TEAM) balance_block_kernel(const BalanceArgs a) {
+    using R = Row<TEAM, 0, VEC, L>;
+    constexpr int V = R::V, U = 4;  // accesses on their way together
+    extern __shared__ float4 stage4[];
+    __shared__ float joints[2][3][R::WARPS];
+    int half = 0;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    float* stage = reinterpret_cast<float*>(stage4);
+    const R r(a, threadIdx.x);
+    const int64_t first = blockIdx.x * a.rows, last = min(first + a.rows, a.tokens);
+    const bool whole = reinterpret_cast<uintptr_t>(a.counts) % 16 == 0 && a.n % 4 == 0, softmax = a.score == SDM_SOFTMAX;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Run run;
+    for (int64_t t = first; t < last; ++t) {
+        run.next(a, t, blockIdx.x, threadIdx.x == 0);
+        const L* row = static_cast<const L*>(a.logits) + t * a.row_stride;
+        const int32_t* from = run.q.s >= 0 ? a.counts + run.q.s * a.n : nullptr;
+        const auto counts = [&](int j, float* c) {
+            if (from != nullptr) {
+                centred<V>(from, a.n, whole, run.f.centre, j, c);
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) c[v] = 0.0f;
             }
         };
-        L* out = GRAD ? static_cast<L*>(a.dlogits) + t * a.dlogits_stride : nullptr;
-        const L* add = GRAD && a.add != nullptr ? static_cast<const L*>(a.add) + t * a.add_stride : nullptr;
-        sum += r.template pass<GRAD>(row_of(t), raw, on, counts, f.unit, f.g, out, add, joint[t & 1]);
+        // f(access, first column, V logits) over this thread's share
+        const auto each = [&](const auto& f) {
+            for (int i0 = 0; r.column(i0) < r.n; i0 += U) {
+                uint32_t w[U][R::W];
+#pragma unroll
+                for (int u = 0; u < U; ++u) r.get(row, r.column(i0 + u), w[u], R::kNone);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float y[V];
+                    R::unpack(w[u], y);
+                    if (r.column(i0 + u) < r.n) f(i0 + u, r.column(i0 + u), y);
+                }
+            }
+        };
+        // a thread's V values of an access
+        const auto put_stage = [&](int i, const float* x) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) stage[(i * V + v) * TEAM + threadIdx.x] = x[v];
+        };
+        const auto get_stage = [&](int i, float* x) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[v] = stage[(i * V + v) * TEAM + threadIdx.x];
+        };
+        float m = minus_inf(), mine = 0.0f, z = 0.0f, d = 0.0f;
+        bool soft = softmax;
+        for (;;) {
+            if (soft) {
+                each([&](int i, int, const float* y) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) m = fmaxf(m, y[v]);  // NaN is left out
+                    if (STAGED) put_stage(i, y);
+                });
+                mine = m;
+                const auto add_up = [&](int i, int j, const float* y) {
+                    float c[V], kept[V];
+                    counts(j, c);
+                    R::soft_scores(y, mine, c, kept, z, d);
+                    if (STAGED && GRAD) put_stage(i, kept);
+                };
+                if constexpr (STAGED) {
+#pragma unroll 4
+                    for (int i = 0; r.column(i) < r.n; ++i) {
+                        float y[V];
+                        get_stage(i, y);
+                        add_up(i, r.column(i), y);
+                    }
+                } else {
+                    each(add_up);
+                }
+                m = warp_max(m);
+                const float scale = exp_below(mine, m);
+                z *= scale;
+                d *= scale;
+            } else {
+                each([&](int i, int j, const float* y) {
+                    float c[V], kept[V];
+                    counts(j, c);
+                    R::sigmoid_scores(y, c, kept, z, d);
+                    if (STAGED && GRAD) put_stage(i, kept);
+                });
+            }
+            z = warp_sum(z);
+            d = warp_sum(d);
+            float(*joint)[R::WARPS] = joints[half ^= 1];  // the other half may still be read
+            if (lane == 0) {
+                joint[0][warp] = m;
+                joint[1][warp] = z;
+                joint[2][warp] = d;
+            }
+            __syncthreads();
+            const int w = lane % R::WARPS;  // every warp for itself
+            const float theirs = joint[0][w];
+            m = warp_max<R::WARPS>(theirs);
+            const float scale = lane >= R::WARPS ? 0.0f : soft ? exp_below(theirs, m) : 1.0f;
+            z = warp_sum(joint[1][w] * scale);
+            d = warp_sum(joint[2][w] * scale);
+            if (soft || z >= kLowScores) break;
+            soft = true;
+            m = minus_inf();
+            z = d = 0.0f;
+        }
+        const float inverse = z > 0.0f ? __frcp_rn(z) : 0.0f, mean = d * inverse;
+        if (z > 0.0f) run.sum += fmaf(run.f.unit, mean, 1.0f);
+        if constexpr (GRAD) {
+            L* out = static_cast<L*>(a.dlogits) + t * a.dlogits_stride;
+            const L* add = a.add != nullptr ? static_cast<const L*>(a.add) + t * a.add_stride : nullptr;
+            const float gz = run.f.g * inverse * (soft ? exp_below(mine, m) : 1.0f), gm = -gz * mean;
+            const auto write = [&](int j, float* kept) {
+                float c[V], adds[V];
+                counts(j, c);
+#pragma unroll
+                for (int v = 0; v < V; ++v) adds[v] = 0.0f;
+                if (add != nullptr) {
+                    uint32_t w[R::W];
+                    r.get(add, j, w, 0u);
+                    R::unpack(w, adds);
+                }
+                R::gradient(kept, c, gz, gm, adds);
+                r.put(out, j, kept);
+            };
+            if constexpr (STAGED) {
+#pragma unroll 4
+                for (int i = 0; r.column(i) < r.n; ++i) {
+                    float kept[V];
+                    get_stage(i, kept);
+                    write(r.column(i), kept);
+                }
+            } else {
+                each([&](int, int j, const float* y) {
+                    float none[V], kept[V], unused = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) none[v] = 0.0f;
+                    if (soft)
+                        R::soft_scores(y, mine, none, kept, unused, unused);
+                    else
+                        R::sigmoid_scores(y, none, kept, unused, unused);
+                    write(j, kept);
+                });
+            }
+        }
     }
-    if (q.s >= 0 && r.tid == 0) a.parts[team + q.s] = sum;
+    run.done(a, blockIdx.x, threadIdx.x == 0);
 }
 
 // A sequence's loss out of its parts: those of the teams that met it lie side by side.
@@ -489,29 +570,32 @@ __global__ void __launch_bounds__(kCountThreads) balance_loss_kernel(const Balan
 struct Team {
     const void* fn;
     int threads, teams;
+    size_t smem;
 };
 
-// Without the gradient a row need not stay in registers, and a block reads it at the pace of memory. Teams as in
-// the routing's gradient.
+// Eight logits a lane up to 256 entries, in fewer lanes for shorter rows; then blocks of 128 to 512 threads, which
+// stage rows of up to 48 K entries.
+constexpr int kStaged = 48 * 1024;
+template <int TEAM, bool VEC, bool GRAD, typename L>
+Team block_team(int n) {
+    constexpr int V = (VEC ? 16 : 4) / sizeof(L);
+    const size_t smem = (size_t)(n + TEAM * V - 1) / (TEAM * V) * (TEAM * V) * sizeof(float);
+    if (n <= kStaged) return {(const void*)balance_block_kernel<TEAM, VEC, GRAD, true, L>, TEAM, 1, smem};
+    return {(const void*)balance_block_kernel<TEAM, VEC, GRAD, false, L>, TEAM, 1, 0};
+}
 template <bool VEC, bool GRAD, typename L>
-Team rows_kernel(int n) {
-    if (n <= 32) return {(const void*)balance_rows_kernel<4, 8, VEC, GRAD, L>, 128, 32};
-    if (n <= 64) return {(const void*)balance_rows_kernel<8, 8, VEC, GRAD, L>, 128, 16};
-    if (n <= 128) return {(const void*)balance_rows_kernel<16, 8, VEC, GRAD, L>, 128, 8};
-    if (n <= 256) return {(const void*)balance_rows_kernel<32, 8, VEC, GRAD, L>, 128, 4};
-    if (n <= 512) return {(const void*)balance_rows_kernel<32, 16, VEC, GRAD, L>, 128, 4};
-    if (n <= 1024) return {(const void*)balance_rows_kernel<32, 32, VEC, GRAD, L>, 128, 4};
-    if (n <= 2048) return {(const void*)balance_rows_kernel<128, 16, VEC, GRAD, L>, 128, 1};
-    if (n <= 4096) return {(const void*)balance_rows_kernel<128, 32, VEC, GRAD, L>, 128, 1};
-    if (n <= 6144) return {(const void*)balance_rows_kernel<128, 48, VEC, GRAD, L>, 128, 1};
-    if (n <= 8192) return {(const void*)balance_rows_kernel<256, 32, VEC, GRAD, L>, 256, 1};
-    if (n <= 16384) return {(const void*)balance_rows_kernel<512, 32, VEC, GRAD, L>, 512, 1};
-    return {(const void*)balance_rows_kernel<512, 0, VEC, GRAD, L>, 512, 1};
+Team rows_team(int n) {
+    if (n <= 32) return {(const void*)balance_lanes_kernel<4, 8, VEC, GRAD, L>, 128, 32, 0};
+    if (n <= 64) return {(const void*)balance_lanes_kernel<8, 8, VEC, GRAD, L>, 128, 16, 0};
+    if (n <= 128) return {(const void*)balance_lanes_kernel<16, 8, VEC, GRAD, L>, 128, 8, 0};
+    if (n <= 256) return {(const void*)balance_lanes_kernel<32, 8, VEC, GRAD, L>, 128, 4, 0};
+    if (n <= 512) return {(const void*)balance_lanes_kernel<32, 16, VEC, GRAD, L>, 128, 4, 0};
+    if (n <= 6144) return block_team<128, VEC, GRAD, L>(n);
+    return n <= 12288 ? block_team<256, VEC, GRAD, L>(n) : block_team<512, VEC, GRAD, L>(n);
 }
 template <typename L>
-Team rows_kernel(int n, bool vec, bool grad) {
-    return vec ? (grad ? rows_kernel<true, true, L>(n) : rows_kernel<true, false, L>(n))
-               : (grad ? rows_kernel<false, true, L>(n) : rows_kernel<false, false, L>(n));
+Team rows_team(int n, bool vec, bool grad) {
+    return vec ? (grad ? rows_team<true, true, L>(n) : rows_team<true, false, L>(n)) : (grad ? rows_team<false, true, L>(n) : rows_team<false, false, L>(n));
 }
 
 }  // namespace
@@ -527,7 +611,7 @@ int launch_balance(const BalanceArgs& a0, cudaStream_t stream) {
         return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * es % 16 == 0);
     };
     const bool vec = whole(a.logits, a.row_stride) && whole(a.dlogits, a.dlogits_stride) && whole(a.add, a.add_stride), grad = a.dlogits != nullptr;
-    const Team team = a.logit_bf16 ? rows_kernel<uint16_t>(a.n, vec, grad) : rows_kernel<float>(a.n, vec, grad);
+    const Team team = a.logit_bf16 ? rows_team<uint16_t>(a.n, vec, grad) : rows_team<float>(a.n, vec, grad);
     const int64_t sms = sm_count();
     if (a.sequences > 0) {
         const int64_t zeros = std::min<int64_t>((a.sequences * a.n + 4 * kCountThreads - 1) / (4 * kCountThreads), 8 * sms);
@@ -549,11 +633,13 @@ int launch_balance(const BalanceArgs& a0, cudaStream_t stream) {
     a.rows = 1;
     if (a.tokens > 0) {
         // runs that fill the GPU once
-        const int64_t most = std::min<int64_t>(kBalanceTeams, sms * std::max(1, blocks_per_sm(team.fn, team.threads, 0)) * team.teams);
+        int rc = allow_smem(team.fn, team.smem);
+        if (rc != 0) return rc;
+        const int64_t most = std::min<int64_t>(kBalanceTeams, sms * std::max(1, blocks_per_sm(team.fn, team.threads, team.smem)) * team.teams);
         a.rows = (a.tokens + most - 1) / most;
         const int64_t teams = (a.tokens + a.rows - 1) / a.rows;
         void* args[] = {&a};
-        const int rc = launch_pdl_raw(team.fn, dim3((unsigned)((teams + team.teams - 1) / team.teams)), dim3(team.threads), 0, stream, args);
+        rc = launch_pdl_raw(team.fn, dim3((unsigned)((teams + team.teams - 1) / team.teams)), dim3(team.threads), team.smem, stream, args);
         if (rc != 0) return rc;
     }
     if (a.sequences == 0) return 0;

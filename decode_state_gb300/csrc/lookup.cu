@@ -41,26 +41,39 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
         if (t < a.n_tokens) slot[r] = a.idx64 ? __ldg(static_cast<const int64_t*>(a.tokens) + t) : __ldg(static_cast<const int32_t*>(a.tokens) + t);
     }
     Pack<T, V> x[ROWS];
+    float scale[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        const bool in = slot[r] >= 0 && slot[r] < a.n_rows;
-        if (!in && slot[r] != a.padding) atomicOr(&g_lookup_status, SDM_DEV_BAD_INDEX);
-        if (!in || slot[r] == a.padding) {
-            slot[r] = -1;
+        const bool in = slot[r] >= 0 && slot[r] < a.n_rows, none = slot[r] == a.padding;
+        if (!in && !none) atomicOr(&g_lookup_status, SDM_DEV_BAD_INDEX);
+        scale[r] = a.scale;
+        if (in && !none) {
+            x[r] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(a.table) + slot[r] * a.hd + col);
+        } else {
+            scale[r] = 0.0f;
 #pragma unroll
             for (int c = 0; c < V; ++c) x[r].v[c] = T(0);
-        } else {
-            x[r] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(a.table) + slot[r] * a.hd + col);
         }
     }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const int64_t t = first + r * teams;
         if (t >= a.n_tokens) break;
-        Pack<O, V> y;
+        O* to = static_cast<O*>(a.out) + t * a.hd + col;
+        if constexpr (sizeof(O) == 2 && V > 1) {
+            uint32_t y[V / 2];
 #pragma unroll
-        for (int c = 0; c < V; ++c) y.v[c] = slot[r] < 0 ? O(0) : from_f32<O>(to_f32(x[r].v[c]) * a.scale);
-        *reinterpret_cast<Pack<O, V>*>(static_cast<O*>(a.out) + t * a.hd + col) = y;
+            for (int c = 0; c < V / 2; ++c) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(to_f32(x[r].v[2 * c]) * scale[r], to_f32(x[r].v[2 * c + 1]) * scale[r]);
+                y[c] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<Pack<uint32_t, V / 2>*>(to) = *reinterpret_cast<const Pack<uint32_t, V / 2>*>(y);
+        } else {
+            Pack<O, V> y;
+#pragma unroll
+            for (int c = 0; c < V; ++c) y.v[c] = from_f32<O>(to_f32(x[r].v[c]) * scale[r]);
+            *reinterpret_cast<Pack<O, V>*>(to) = y;
+        }
     }
 }
 

@@ -7,7 +7,7 @@
 // each warp and column slice, however unevenly the slots share them: a run of equal slots that crosses the ends of
 // pieces leaves one float32 sum for each of them, which a last launch adds up in order.
 //   up to 512 entries    one launch: the warp of a slot's first entry finds the others by scanning all of them
-//   up to 8192           ranks by counting: an entry's place is the number of entries that come before it
+//   up to 2048           ranks by counting: an entry's place is the number of entries that come before it
 //   more                 a stable radix sort with digits of at most 11 bits: counts, their running sums, places
 // Rows without entries are set to zero by blocks of the same launch as the sums, which search the sorted slots.
 #include <algorithm>
@@ -23,9 +23,12 @@ __device__ unsigned int g_row_sums_status;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr uint32_t kDirect = 512;    // entries that one launch sums
-constexpr uint32_t kRanked = 8192;   // entries ranked by counting
+constexpr uint32_t kRanked = 2048;   // entries ranked by counting
 constexpr int kMostBits = 11;
 constexpr int kZeroRows = 256;       // rows that a block sets to zero, at most
+
+// x / d for x < 2^31 as a product (Granlund and Montgomery): m = ceil(2^(31 + l) / d), l = ceil(log2 d).
+__device__ __forceinline__ uint32_t divided(uint32_t x, const Divisor& d) { return d.m == 0 ? x : __umulhi(x, d.m) >> d.shift; }
 
 struct Place {
     int op;
@@ -34,7 +37,7 @@ struct Place {
 __device__ __forceinline__ Place place_of(const RowSumArgs& a, uint32_t e) {
     const int op = e >= a.split;
     const uint32_t at = op ? e - a.split : e;
-    return {op, at / (uint32_t)(op ? a.width[1] : a.width[0]), at};
+    return {op, divided(at, op ? a.by_width[1] : a.by_width[0]), at};
 }
 __device__ __forceinline__ float weight_of(const RowSumArgs& a, int op, uint32_t at) {
     const void* w = op ? a.w[1] : a.w[0];
@@ -45,9 +48,11 @@ __device__ __forceinline__ float weight_of(const RowSumArgs& a, int op, uint32_t
 // The slot of entry e, or n_slots where it takes no part: padding, a weight of zero, an index outside the bank (flagged).
 __device__ __forceinline__ uint32_t key_of(const RowSumArgs& a, uint32_t e) {
     const Place p = place_of(a, e);
-    const int chunk = a.chunk;
-    const int valid = a.chunk_valid != nullptr ? __ldg(a.chunk_valid + p.token / chunk) : a.valid;
-    if ((int)(p.token % chunk) >= valid) return (uint32_t)a.n_slots;
+    if (a.chunk_valid != nullptr || a.valid < a.chunk) {
+        const uint32_t chunk = divided(p.token, a.by_chunk);
+        const int valid = a.chunk_valid != nullptr ? __ldg(a.chunk_valid + chunk) : a.valid;
+        if ((int)(p.token - chunk * a.chunk) >= valid) return (uint32_t)a.n_slots;
+    }
     const void* idx = p.op ? a.idx[1] : a.idx[0];
     const int64_t j = a.idx64 ? __ldg(static_cast<const int64_t*>(idx) + p.at) : __ldg(static_cast<const int32_t*>(idx) + p.at);
     if (j == a.padding) return (uint32_t)a.n_slots;
@@ -86,9 +91,27 @@ __device__ __forceinline__ void put_row(const RowSumArgs& a, int64_t row, int co
     *to = y;
 }
 
-// Rows [first, first + count) of the output whose flag is not set become zero, by a block.
+// Rows [first, first + count) of the output whose flag is not set become zero, by a block: copies of `zeros` in shared
+// memory where rows are whole 16-byte pieces, which cost a thread one instruction a row, else stores.
+constexpr int kZeroBytes = 4096;
 template <typename O, int V>
-__device__ __forceinline__ void zero_rows(const RowSumArgs& a, int64_t first, int count, const uint8_t* touched) {
+__device__ __forceinline__ void zero_rows(const RowSumArgs& a, int64_t first, int count, const uint8_t* touched, uint4* zeros) {
+    const int64_t bytes = (int64_t)a.hd * sizeof(O);
+    if ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)bytes) % 16 == 0) {
+        for (int i = threadIdx.x; i < kZeroBytes / 16; i += kThreads) zeros[i] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_shared();
+        __syncthreads();
+        char* rows = static_cast<char*>(a.out) + first * bytes;
+        const int parts = (int)((bytes + kZeroBytes - 1) / kZeroBytes);
+        for (int u = threadIdx.x; u < count * parts; u += kThreads) {
+            const int r = u / parts;
+            const int64_t at = (int64_t)(u - r * parts) * kZeroBytes;
+            if (!touched[r]) bulk_s2g(rows + r * bytes + at, zeros, (uint32_t)min((int64_t)kZeroBytes, bytes - at));
+        }
+        bulk_commit();
+        bulk_wait_read_all();  // the block's shared memory is given back with its end
+        return;
+    }
     Pack<O, V> none;
 #pragma unroll
     for (int c = 0; c < V; ++c) none.v[c] = O(0);
@@ -99,6 +122,13 @@ __device__ __forceinline__ void zero_rows(const RowSumArgs& a, int64_t first, in
     }
 }
 
+// Which of the launch's blocks sets rows to zero, the `zero_blocks` of them spread evenly among the others: its number, or
+// -1 less that of another.
+__device__ __forceinline__ int64_t zero_block(const RowSumArgs& a) {
+    const uint64_t b = blockIdx.x, z = (uint64_t)a.zero_blocks, before = b * z / gridDim.x;
+    return (b + 1) * z / gridDim.x > before ? (int64_t)before : -1 - (int64_t)(b - before);
+}
+
 // ---------------------------------------------------------------- few entries
 
 template <typename D, typename O, int V>
@@ -106,23 +136,26 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
     __shared__ uint32_t keys[kDirect];
     __shared__ uint16_t list[kWarps][kDirect];
     __shared__ uint8_t touched[kZeroRows];
+    __shared__ uint4 zeros[kZeroBytes / 16];
     grid_dependency_wait();
     grid_launch_dependents();
     const int n = (int)a.entries, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t zero = zero_block(a);
+#pragma unroll 2
     for (int e = threadIdx.x; e < n; e += kThreads) keys[e] = key_of(a, e);
-    if ((int64_t)blockIdx.x < a.zero_blocks) {
-        const int64_t first = (int64_t)blockIdx.x * zero_span;
+    if (zero >= 0) {
+        const int64_t first = zero * zero_span;
         const int count = (int)min((int64_t)zero_span, a.n_slots - first);
         for (int r = threadIdx.x; r < count; r += kThreads) touched[r] = 0;
         __syncthreads();
         for (int e = threadIdx.x; e < n; e += kThreads)
             if (keys[e] >= first && keys[e] < first + count) touched[keys[e] - first] = 1;
         __syncthreads();
-        zero_rows<O, V>(a, first, count, touched);
+        zero_rows<O, V>(a, first, count, touched, zeros);
         return;
     }
     __syncthreads();
-    const int64_t unit = ((int64_t)blockIdx.x - a.zero_blocks) * kWarps + warp;
+    const int64_t unit = (-1 - zero) * kWarps + warp;
     const int e = (int)(unit / a.slices);
     if (e >= n) return;
     const uint32_t key = keys[e];
@@ -460,13 +493,15 @@ constexpr uint32_t kShort = 32;  // entries of a run beyond the end of a piece t
 template <typename D, typename O, int V>
 __global__ void __launch_bounds__(kThreads) sums_kernel(const RowSumArgs a, int zero_span) {
     __shared__ uint8_t touched[kZeroRows];
+    __shared__ uint4 zeros[kZeroBytes / 16];
     __shared__ uint32_t range[2];
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     const uint32_t entries = a.counters[0];
-    if ((int64_t)blockIdx.x < a.zero_blocks) {
-        const int64_t first = (int64_t)blockIdx.x * zero_span;
+    const int64_t zero = zero_block(a);
+    if (zero >= 0) {
+        const int64_t first = zero * zero_span;
         const int count = (int)min((int64_t)zero_span, a.n_slots - first), warp = threadIdx.x >> 5;
         if (warp < 2) range[warp] = warp_lower_bound(a.sorted, entries, (uint32_t)(first + warp * count));
         for (int r = threadIdx.x; r < count; r += kThreads) touched[r] = 0;
@@ -481,10 +516,10 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const RowSumArgs a, int 
             }
         }
         __syncthreads();
-        zero_rows<O, V>(a, first, count, touched);
+        zero_rows<O, V>(a, first, count, touched, zeros);
         return;
     }
-    const int64_t unit = ((int64_t)blockIdx.x - a.zero_blocks) * kWarps + (threadIdx.x >> 5);
+    const int64_t unit = (-1 - zero) * kWarps + (threadIdx.x >> 5);
     const int64_t piece = unit / a.slices;
     uint32_t from = (uint32_t)min(piece * a.piece, (int64_t)entries), to = (uint32_t)min((piece + 1) * a.piece, (int64_t)entries);
     if (from >= to) return;
@@ -520,9 +555,10 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const RowSumArgs a, int 
     const auto flush = [&](bool ends) {
         if (continues || !ends) {
             if (on) {
-                float* part = (continues ? a.heads : a.tails) + piece * a.hd + col;
+                Pack<float, V> part;
 #pragma unroll
-                for (int c = 0; c < V; ++c) part[c] = sum[c];
+                for (int c = 0; c < V; ++c) part.v[c] = sum[c];
+                *reinterpret_cast<Pack<float, V>*>((continues ? a.heads : a.tails) + piece * a.hd + col) = part;
             }
             if (!continues && slice == 0 && lane == 0) a.list[atomicAdd(a.counters + 1, 1u)] = (uint32_t)piece;
         } else if (on) {
@@ -584,7 +620,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const RowSumArgs a) {
         const int64_t piece = a.list[unit / a.slices];
         const uint32_t key = __ldg(&a.sorted[(piece + 1) * a.piece].x);
         // the pieces that begin with this slot and go on with it for more than kShort entries
-        const uint32_t end = lower_bound(a.sorted, (uint32_t)((piece + 1) * a.piece), entries, key + 1);
+        const uint32_t from = (uint32_t)((piece + 1) * a.piece), end = from + warp_lower_bound(a.sorted + from, entries - from, key + 1);
         const int64_t more = ((int64_t)end - kShort) / a.piece - piece, share = (more + kWarps - 1) / kWarps;
         const int in_slice = lane * V, col = (int)(unit % a.slices) * a.slice_cols + in_slice;
         const bool on = in_slice < a.slice_cols && col < a.hd;
@@ -595,19 +631,19 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const RowSumArgs a) {
             const int64_t last = min((warp + 1) * share, more);
 #pragma unroll 8
             for (int64_t q = warp * share; q < last; ++q) {
-                const float* part = a.heads + (piece + 1 + q) * a.hd + col;
+                const Pack<float, V> part = load_pack<float, V>(a.heads + (piece + 1 + q) * a.hd + col);
 #pragma unroll
-                for (int c = 0; c < V; ++c) sum[c] += part[c];
+                for (int c = 0; c < V; ++c) sum[c] += part.v[c];
             }
 #pragma unroll
             for (int c = 0; c < V; ++c) parts[warp][in_slice + c] = sum[c];
         }
         __syncthreads();
         if (warp == 0 && on) {
-            const float* tail = a.tails + piece * a.hd + col;
+            const Pack<float, V> tail = load_pack<float, V>(a.tails + piece * a.hd + col);
 #pragma unroll
             for (int c = 0; c < V; ++c) {
-                sum[c] = tail[c];
+                sum[c] = tail.v[c];
                 for (int w = 0; w < kWarps; ++w) sum[c] += parts[w][in_slice + c];
             }
             put_row<O, V>(a, key, col, sum);
@@ -637,6 +673,13 @@ uint32_t piece_of(int64_t entries, int hd) {
     return piece;
 }
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+Divisor divisor(int d) {
+    int l = 0;
+    while (((int64_t)1 << l) < d) ++l;
+    if (l == 0) return {0u, 0};
+    return {(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), l - 1};
+}
 
 // The passes of the sort over slots below n_slots. Tiles of 1024 entries, of which few entries make more blocks, else
 // of 4096, whose digits come in longer runs; up to 32 tiles are added up by each block that needs their sums.
@@ -719,6 +762,8 @@ int64_t row_sums_workspace(int64_t entries, int64_t n_slots, int hd) {
 
 int launch_row_sums(const RowSumArgs& a0, cudaStream_t stream) {
     RowSumArgs a = a0;
+    for (int o = 0; o < 2; ++o) a.by_width[o] = divisor(a.width[o]);
+    a.by_chunk = divisor(a.chunk);
     const auto whole = [&](int v) {  // accesses of v columns are aligned everywhere
         if (a.hd % v != 0) return false;
         const uintptr_t in = std::min(16, v * (a.dout_bf16 ? 2 : 4)), out = std::min(16, v * (a.out_bf16 ? 2 : 4));

@@ -164,6 +164,12 @@ struct LookupArgs {
     int lane_bits, column_blocks;  // lanes that move a row, or a block's columns of it; blocks that share a row
 };
 
+// Division of numbers below 2^31 (m 0: by one).
+struct Divisor {
+    uint32_t m;
+    int shift;
+};
+
 // Sums of weighted rows by slot: the gradient of an embedding table, or of the bank in a gather.
 struct RowSumArgs {
     int n_ops;
@@ -181,6 +187,7 @@ struct RowSumArgs {
     void* out;
     void* workspace;
     uint32_t entries, split;  // all, and those of the first operand
+    Divisor by_width[2], by_chunk;
     // in the workspace
     uint32_t* counters;   // entries that take part; runs to join
     const uint2* sorted;  // (slot, entry) of those that take part
