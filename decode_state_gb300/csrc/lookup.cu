@@ -6,6 +6,7 @@
 // and then rows are loaded together before any is stored. Rows longer than 256 such accesses are shared by blocks.
 #include <algorithm>
 #include <climits>
+#include <cstring>
 
 #include "sdm.h"
 #include "sdm_device.cuh"
@@ -41,39 +42,44 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
         if (t < a.n_tokens) slot[r] = a.idx64 ? __ldg(static_cast<const int64_t*>(a.tokens) + t) : __ldg(static_cast<const int32_t*>(a.tokens) + t);
     }
     Pack<T, V> x[ROWS];
-    float scale[ROWS];
+    bool outside = false;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const bool in = slot[r] >= 0 && slot[r] < a.n_rows, none = slot[r] == a.padding;
-        if (!in && !none) atomicOr(&g_lookup_status, SDM_DEV_BAD_INDEX);
-        scale[r] = a.scale;
-        if (in && !none) {
-            x[r] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(a.table) + slot[r] * a.hd + col);
-        } else {
-            scale[r] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < V; ++c) x[r].v[c] = T(0);
-        }
+        outside |= !in && !none;
+        if (!in || none) slot[r] = -1;
+        if (slot[r] >= 0) x[r] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(a.table) + slot[r] * a.hd + col);
     }
+    if (outside) atomicOr(&g_lookup_status, SDM_DEV_BAD_INDEX);
+    O* to = static_cast<O*>(a.out) + first * a.hd + col;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        const int64_t t = first + r * teams;
-        if (t >= a.n_tokens) break;
-        O* to = static_cast<O*>(a.out) + t * a.hd + col;
-        if constexpr (sizeof(O) == 2 && V > 1) {
-            uint32_t y[V / 2];
+        if (first + r * teams >= a.n_tokens) break;
+        Pack<O, V> y;
+        if (slot[r] < 0) {
+#pragma unroll
+            for (int c = 0; c < V; ++c) y.v[c] = O(0);
+        } else if constexpr (sizeof(T) == 2 && V > 1) {
+            uint32_t w[V / 2];
+            memcpy(w, &x[r], sizeof(w));
 #pragma unroll
             for (int c = 0; c < V / 2; ++c) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(to_f32(x[r].v[2 * c]) * scale[r], to_f32(x[r].v[2 * c + 1]) * scale[r]);
-                y[c] = *reinterpret_cast<const uint32_t*>(&b);
+                const float low = __uint_as_float(w[c] << 16) * a.scale, high = __uint_as_float(w[c] & 0xffff0000u) * a.scale;
+                if constexpr (sizeof(O) == 2) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(low, high);
+                    memcpy(&w[c], &b, 4);
+                } else {
+                    y.v[2 * c] = low;
+                    y.v[2 * c + 1] = high;
+                }
             }
-            *reinterpret_cast<Pack<uint32_t, V / 2>*>(to) = *reinterpret_cast<const Pack<uint32_t, V / 2>*>(y);
+            if constexpr (sizeof(O) == 2) memcpy(&y, w, sizeof(w));
         } else {
-            Pack<O, V> y;
 #pragma unroll
-            for (int c = 0; c < V; ++c) y.v[c] = from_f32<O>(to_f32(x[r].v[c]) * scale[r]);
-            *reinterpret_cast<Pack<O, V>*>(to) = y;
+            for (int c = 0; c < V; ++c) y.v[c] = from_f32<O>(to_f32(x[r].v[c]) * a.scale);
         }
+        *reinterpret_cast<Pack<O, V>*>(to) = y;
+        to += (int64_t)teams * a.hd;
     }
 }
 

@@ -45,22 +45,40 @@ __device__ __forceinline__ float weight_of(const RowSumArgs& a, int op, uint32_t
     return a.w_bf16 ? to_f32(__ldg(static_cast<const uint16_t*>(w) + at)) : __ldg(static_cast<const float*>(w) + at);
 }
 
-// The slot of entry e, or n_slots where it takes no part: padding, a weight of zero, an index outside the bank (flagged).
-__device__ __forceinline__ uint32_t key_of(const RowSumArgs& a, uint32_t e) {
-    const Place p = place_of(a, e);
-    if (a.chunk_valid != nullptr || a.valid < a.chunk) {
-        const uint32_t chunk = divided(p.token, a.by_chunk);
-        const int valid = a.chunk_valid != nullptr ? __ldg(a.chunk_valid + chunk) : a.valid;
-        if ((int)(p.token - chunk * a.chunk) >= valid) return (uint32_t)a.n_slots;
+// The slots of entries e, e + step, ..., or n_slots where one takes no part: padding, a weight of zero, an index
+// outside the bank (flagged), nothing behind the last. The loads of all are on their way together.
+template <int N>
+__device__ __forceinline__ void keys_of(const RowSumArgs& a, uint32_t e, uint32_t step, uint32_t* key) {
+    int64_t j[N];
+    float w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t at = e + i * step;
+        j[i] = a.padding;
+        w[i] = 0.0f;
+        if (at < a.entries) {
+            const Place p = place_of(a, at);
+            bool live = true;
+            if (a.chunk_valid != nullptr || a.valid < a.chunk) {
+                const uint32_t chunk = divided(p.token, a.by_chunk);
+                const int valid = a.chunk_valid != nullptr ? __ldg(a.chunk_valid + chunk) : a.valid;
+                live = (int)(p.token - chunk * a.chunk) < valid;
+            }
+            if (live) {
+                const void* idx = p.op ? a.idx[1] : a.idx[0];
+                j[i] = a.idx64 ? __ldg(static_cast<const int64_t*>(idx) + p.at) : __ldg(static_cast<const int32_t*>(idx) + p.at);
+                w[i] = weight_of(a, p.op, p.at);
+            }
+        }
     }
-    const void* idx = p.op ? a.idx[1] : a.idx[0];
-    const int64_t j = a.idx64 ? __ldg(static_cast<const int64_t*>(idx) + p.at) : __ldg(static_cast<const int32_t*>(idx) + p.at);
-    if (j == a.padding) return (uint32_t)a.n_slots;
-    if (j < 0 || j >= a.n_slots) {
-        atomicOr(&g_row_sums_status, SDM_DEV_BAD_INDEX);
-        return (uint32_t)a.n_slots;
+    bool outside = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool in = j[i] >= 0 && j[i] < a.n_slots, none = j[i] == a.padding;
+        outside |= !in && !none;
+        key[i] = in && !none && w[i] != 0.0f ? (uint32_t)j[i] : (uint32_t)a.n_slots;
     }
-    return weight_of(a, p.op, p.at) == 0.0f ? (uint32_t)a.n_slots : (uint32_t)j;
+    if (outside) atomicOr(&g_row_sums_status, SDM_DEV_BAD_INDEX);
 }
 
 // ---------------------------------------------------------------- columns
@@ -141,8 +159,9 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
     grid_launch_dependents();
     const int n = (int)a.entries, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t zero = zero_block(a);
-#pragma unroll 2
-    for (int e = threadIdx.x; e < n; e += kThreads) keys[e] = key_of(a, e);
+    uint32_t own[kDirect / kThreads];
+    keys_of<kDirect / kThreads>(a, threadIdx.x, kThreads, own);
+    for (int i = 0; i < kDirect / kThreads; ++i) keys[i * kThreads + threadIdx.x] = own[i];
     if (zero >= 0) {
         const int64_t first = zero * zero_span;
         const int count = (int)min((int64_t)zero_span, a.n_slots - first);
@@ -212,8 +231,7 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const RowSumArgs a, uint
     int live = 0;
     for (int e0 = threadIdx.x; e0 < n; e0 += 8 * kThreads) {
         uint32_t key[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) key[i] = e0 + i * kThreads < n ? key_of(a, e0 + i * kThreads) : (uint32_t)a.n_slots;
+        keys_of<8>(a, e0, kThreads, key);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (e0 + i * kThreads < n) all[e0 + i * kThreads] = key[i];
@@ -267,18 +285,25 @@ __global__ void __launch_bounds__(kThreads) digit_count_kernel(const RowSumArgs 
     const int all = 1 << digit.bits;
     for (int b = threadIdx.x; b < all; b += kThreads) bins[b] = 0;
     __syncthreads();
-    uint32_t key[ITEMS];
+    constexpr int BATCH = ITEMS < 8 ? ITEMS : 8;
+    for (int i0 = 0; i0 < ITEMS; i0 += BATCH) {
+        const uint32_t first = from + i0 * kThreads + threadIdx.x;
+        uint32_t key[BATCH];
+        if constexpr (FIRST) {
+            keys_of<BATCH>(a, first, kThreads, key);
+        } else {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const uint32_t e = from + i * kThreads + threadIdx.x;
-        key[i] = (uint32_t)a.n_slots;
-        if (e < entries) key[i] = FIRST ? key_of(a, e) : in[e].x;
-    }
+            for (int i = 0; i < BATCH; ++i) {
+                const uint32_t e = first + i * kThreads;
+                key[i] = e < entries ? in[e].x : (uint32_t)a.n_slots;
+            }
+        }
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const uint32_t e = from + i * kThreads + threadIdx.x;
-        if (FIRST && e < entries) keys[e] = key[i];
-        if (key[i] < a.n_slots) atomicAdd(&bins[digit.of(key[i])], 1u);
+        for (int i = 0; i < BATCH; ++i) {
+            const uint32_t e = first + i * kThreads;
+            if (FIRST && e < entries) keys[e] = key[i];
+            if (key[i] < a.n_slots) atomicAdd(&bins[digit.of(key[i])], 1u);
+        }
     }
     __syncthreads();
     for (int b = threadIdx.x; b < all; b += kThreads) counts[((int64_t)blockIdx.x << digit.bits) + b] = bins[b];
@@ -346,7 +371,7 @@ __global__ void __launch_bounds__(32 * kScanWarps) digit_scan_kernel(uint32_t* c
 // are put in order in shared memory first, so that what goes to one place is written side by side. SCANNED: counts are
 // running sums over the tiles, totals their ends; else a block adds up the counts of the few tiles itself.
 template <bool FIRST, bool SCANNED, int ITEMS>
-__global__ void __launch_bounds__(kThreads) digit_place_kernel(const RowSumArgs a, const uint32_t* keys, const uint2* in, uint2* out,
+__global__ void __launch_bounds__(kThreads, 3) digit_place_kernel(const RowSumArgs a, const uint32_t* keys, const uint2* in, uint2* out,
                                                                const uint32_t* counts, const uint32_t* totals, Digit digit) {
     constexpr int TILE = kThreads * ITEMS;
     // a warp's counts of each digit; then the tile's entries
@@ -386,12 +411,7 @@ __global__ void __launch_bounds__(kThreads) digit_place_kernel(const RowSumArgs 
     for (int i = 0; i < ITEMS; ++i) {
         const bool on = key[i] < a.n_slots;
         const uint32_t d = digit.of(key[i]);
-        unsigned same = __ballot_sync(kAll, on);  // lanes with the same digit
-        for (int b = 0; b < digit.bits; ++b) {
-            const bool set = d >> b & 1;
-            const unsigned with = __ballot_sync(kAll, set);
-            same &= set ? with : ~with;
-        }
+        const unsigned same = __match_any_sync(kAll, on ? d : 0xffffffffu);  // lanes with the same digit
         const uint32_t before = m.own[warp][d];
         __syncwarp();
         if (on && lane == 31 - __clz(same)) m.own[warp][d] = (uint16_t)(before + __popc(same));
@@ -491,7 +511,7 @@ __device__ __forceinline__ uint32_t warp_lower_bound(const uint2* sorted, uint32
 constexpr uint32_t kShort = 32;  // entries of a run beyond the end of a piece that its warp sums as well
 
 template <typename D, typename O, int V>
-__global__ void __launch_bounds__(kThreads) sums_kernel(const RowSumArgs a, int zero_span) {
+__global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : 3) sums_kernel(const RowSumArgs a, int zero_span) {
     __shared__ uint8_t touched[kZeroRows];
     __shared__ uint4 zeros[kZeroBytes / 16];
     __shared__ uint32_t range[2];
@@ -568,38 +588,42 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const RowSumArgs a, int 
 #pragma unroll
         for (int c = 0; c < V; ++c) sum[c] = 0.0f;
     };
-    constexpr int U = 8;
+    const D* dout0 = static_cast<const D*>(a.dout[0]) + col;
+    const D* dout1 = static_cast<const D*>(a.dout[a.n_ops - 1]) + col;
     for (uint32_t base = from; base < to; base += 32) {
-        uint32_t key = 0;
+        // a lane's entry: its slot, weight and row of dout, in the second operand below zero
+        uint32_t key = current;
         float w = 0.0f;
-        const D* row = nullptr;
-        if (base + lane < to) {
+        int row = 0;
+        const int left = (int)min(to - base, 32u);
+        if (lane < left) {
             const uint2 pair = __ldg(a.sorted + base + lane);
             key = pair.x;
             const Place p = place_of(a, pair.y);
             w = weight_of(a, p.op, p.at);
-            row = static_cast<const D*>(p.op ? a.dout[1] : a.dout[0]) + (int64_t)p.token * a.hd;
+            row = p.op ? ~(int)p.token : (int)p.token;
         }
-        const int left = (int)min(to - base, 32u);
+        uint32_t before = __shfl_up_sync(kAll, key, 1);
+        if (lane == 0) before = current;
+        const unsigned begins = __ballot_sync(kAll, lane < left && key != before);  // entries that begin another run
+        constexpr int U = 8;
         for (int j0 = 0; j0 < left; j0 += U) {
             Pack<D, V> x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const D* r = reinterpret_cast<const D*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(row), j0 + u));
-                if (r != nullptr && on) x[u] = load_pack<D, V>(r + col);
+                const int r = __shfl_sync(kAll, row, j0 + u);
+                if (on) x[u] = load_pack<D, V>(r < 0 ? dout1 + (int64_t)~r * a.hd : dout0 + (int64_t)r * a.hd);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const uint32_t k = __shfl_sync(kAll, key, j0 + u);
-                const float f = __shfl_sync(kAll, w, j0 + u);
-                if (j0 + u < left) {
-                    if (k != current) {
-                        flush(true);
-                        current = k;
-                    }
-#pragma unroll
-                    for (int c = 0; c < V; ++c) sum[c] = fmaf(f, to_f32(x[u].v[c]), sum[c]);
+                if (j0 + u >= left) break;
+                if (begins >> (j0 + u) & 1) {
+                    flush(true);
+                    current = __shfl_sync(kAll, key, j0 + u);
                 }
+                const float f = __shfl_sync(kAll, w, j0 + u);
+#pragma unroll
+                for (int c = 0; c < V; ++c) sum[c] = fmaf(f, to_f32(x[u].v[c]), sum[c]);
             }
         }
     }
