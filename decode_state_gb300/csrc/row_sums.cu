@@ -95,8 +95,8 @@ __device__ __forceinline__ Pack<D, V> load_pack(const D* p) {
 }
 
 template <typename O, int V>
-__device__ __forceinline__ void put_row(const RowSumArgs& a, int64_t row, int col, const float* sum) {
-    Pack<O, V>* to = reinterpret_cast<Pack<O, V>*>(static_cast<O*>(a.out) + row * a.hd + col);
+__device__ __forceinline__ void put_row(const RowSumArgs& a, uint32_t row, int col, const float* sum) {
+    Pack<O, V>* to = reinterpret_cast<Pack<O, V>*>(static_cast<O*>(a.out) + (uint64_t)row * (uint32_t)a.hd + col);
     Pack<O, V> y;
     if (a.accumulate) {
         y = *to;
@@ -390,33 +390,31 @@ __global__ void __launch_bounds__(kThreads, 3) digit_place_kernel(const RowSumAr
     __syncwarp();
     // a warp's entries are consecutive, 32 at a time
     const uint32_t from = tile * (uint32_t)TILE + warp * (32 * ITEMS);
-    uint32_t key[ITEMS], ent[ITEMS];
-    uint16_t rank[ITEMS];
+    uint32_t key[ITEMS], rank[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         const uint32_t e = from + i * 32 + lane;
         key[i] = (uint32_t)a.n_slots;
-        ent[i] = e;
-        if (e < entries) {
-            if constexpr (FIRST) {
-                key[i] = keys[e];
-            } else {
-                const uint2 pair = in[e];
-                key[i] = pair.x;
-                ent[i] = pair.y;
-            }
+        if (e < entries) key[i] = FIRST ? keys[e] : in[e].x;
+    }
+    // lanes with the same digit, bit by bit (a match over all bits at once took half as long again)
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) rank[i] = __ballot_sync(kAll, key[i] < a.n_slots);
+    for (int b = digit.shift; b < digit.shift + digit.bits; ++b) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const uint32_t bit = key[i] >> b & 1;
+            rank[i] &= ~(__ballot_sync(kAll, bit) ^ (0u - bit));
         }
     }
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        const bool on = key[i] < a.n_slots;
-        const uint32_t d = digit.of(key[i]);
-        const unsigned same = __match_any_sync(kAll, on ? d : 0xffffffffu);  // lanes with the same digit
-        const uint32_t before = m.own[warp][d];
+        const unsigned same = rank[i];
+        const uint32_t d = digit.of(key[i]), before = m.own[warp][d];
         __syncwarp();
-        if (on && lane == 31 - __clz(same)) m.own[warp][d] = (uint16_t)(before + __popc(same));
+        if (key[i] < a.n_slots && lane == 31 - __clz(same)) m.own[warp][d] = (uint16_t)(before + __popc(same));
         __syncwarp();
-        rank[i] = (uint16_t)(before + __popc(same & ((1u << lane) - 1)));
+        rank[i] = before + __popc(same & ((1u << lane) - 1));
     }
     __syncthreads();
     // Where each digit starts, among all entries and in the tile: running sums over the digits, up to eight consecutive
@@ -469,8 +467,10 @@ __global__ void __launch_bounds__(kThreads, 3) digit_place_kernel(const RowSumAr
         if (key[i] < a.n_slots) rank[i] += m.own[warp][digit.of(key[i])];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-        if (key[i] < a.n_slots) m.staged[rank[i]] = make_uint2(key[i], ent[i]);
+    for (int i = 0; i < ITEMS; ++i) {
+        const uint32_t e = from + i * 32 + lane;
+        if (key[i] < a.n_slots) m.staged[rank[i]] = make_uint2(key[i], FIRST ? e : in[e].y);
+    }
     __syncthreads();
 #pragma unroll 4
     for (uint32_t p = threadIdx.x; p < live; p += kThreads) {
@@ -508,12 +508,23 @@ __device__ __forceinline__ uint32_t warp_lower_bound(const uint2* sorted, uint32
     return lo;
 }
 
+// A sorted entry as its warp sums it.
+template <typename D>
+struct alignas(16) Entry {
+    const D* row;
+    float w;
+    uint32_t key;
+};
+
 constexpr uint32_t kShort = 32;  // entries of a run beyond the end of a piece that its warp sums as well
 
 template <typename D, typename O, int V>
 __global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : 3) sums_kernel(const RowSumArgs a, int zero_span) {
+    __shared__ union {
+        uint4 zeros[kZeroBytes / 16];
+        Entry<D> batch[kWarps][32];
+    } m;
     __shared__ uint8_t touched[kZeroRows];
-    __shared__ uint4 zeros[kZeroBytes / 16];
     __shared__ uint32_t range[2];
     grid_dependency_wait();
     grid_launch_dependents();
@@ -536,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : 3) sums_kernel(const Ro
             }
         }
         __syncthreads();
-        zero_rows<O, V>(a, first, count, touched, zeros);
+        zero_rows<O, V>(a, first, count, touched, m.zeros);
         return;
     }
     const int64_t unit = (-1 - zero) * kWarps + (threadIdx.x >> 5);
@@ -588,44 +599,47 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : 3) sums_kernel(const Ro
 #pragma unroll
         for (int c = 0; c < V; ++c) sum[c] = 0.0f;
     };
-    const D* dout0 = static_cast<const D*>(a.dout[0]) + col;
-    const D* dout1 = static_cast<const D*>(a.dout[a.n_ops - 1]) + col;
+    Entry<D>* mine = m.batch[threadIdx.x >> 5];
+    const auto fetch = [&](uint32_t at) -> Entry<D> {
+        if (at + lane >= to) return {nullptr, 0.0f, 0u};
+        const uint2 pair = __ldg(a.sorted + at + lane);
+        const Place p = place_of(a, pair.y);
+        return {static_cast<const D*>(p.op ? a.dout[1] : a.dout[0]) + (uint64_t)p.token * (uint32_t)a.hd, weight_of(a, p.op, p.at), pair.x};
+    };
+    Entry<D> next = fetch(from);  // 32 entries ahead
     for (uint32_t base = from; base < to; base += 32) {
-        // a lane's entry: its slot, weight and row of dout, in the second operand below zero
-        uint32_t key = current;
-        float w = 0.0f;
-        int row = 0;
+        // these 32 entries go through shared memory, where each of them is one load for the whole warp
         const int left = (int)min(to - base, 32u);
-        if (lane < left) {
-            const uint2 pair = __ldg(a.sorted + base + lane);
-            key = pair.x;
-            const Place p = place_of(a, pair.y);
-            w = weight_of(a, p.op, p.at);
-            row = p.op ? ~(int)p.token : (int)p.token;
-        }
+        const uint32_t key = next.key;
+        mine[lane] = next;
+        next = fetch(base + 32);
         uint32_t before = __shfl_up_sync(kAll, key, 1);
         if (lane == 0) before = current;
+        __syncwarp();
         const unsigned begins = __ballot_sync(kAll, lane < left && key != before);  // entries that begin another run
         constexpr int U = 8;
         for (int j0 = 0; j0 < left; j0 += U) {
+            const int count = left - j0;
             Pack<D, V> x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int r = __shfl_sync(kAll, row, j0 + u);
-                if (on) x[u] = load_pack<D, V>(r < 0 ? dout1 + (int64_t)~r * a.hd : dout0 + (int64_t)r * a.hd);
+                if (u < count && on) x[u] = load_pack<D, V>(mine[j0 + u].row + col);
             }
+            const unsigned first = begins >> j0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (j0 + u >= left) break;
-                if (begins >> (j0 + u) & 1) {
-                    flush(true);
-                    current = __shfl_sync(kAll, key, j0 + u);
-                }
-                const float f = __shfl_sync(kAll, w, j0 + u);
+                if (u < count) {
+                    if (first >> u & 1) {
+                        flush(true);
+                        current = mine[j0 + u].key;
+                    }
+                    const float w = mine[j0 + u].w;
 #pragma unroll
-                for (int c = 0; c < V; ++c) sum[c] = fmaf(f, to_f32(x[u].v[c]), sum[c]);
+                    for (int c = 0; c < V; ++c) sum[c] = fmaf(w, to_f32(x[u].v[c]), sum[c]);
+                }
             }
         }
+        __syncwarp();
     }
     flush(!goes_on);
 }
@@ -689,11 +703,11 @@ Kernels kernels(int v) {
 }
 
 // Entries of a piece: as many as leave 8192 pieces and slices of 256 columns, so that all warps have work, from 16,
-// below which the sums at the ends are most of the work, to 256.
+// below which the sums at the ends are most of the work, to 128.
 uint32_t piece_of(int64_t entries, int hd) {
     const int64_t want = (entries * ((hd + 255) / 256) + 8191) / 8192;
     uint32_t piece = 16;
-    while (piece < want && piece < 256) piece *= 2;
+    while (piece < want && piece < 128) piece *= 2;
     return piece;
 }
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
