@@ -26,89 +26,128 @@ constexpr int kCountBins = 4096;  // entries of a row that a block counts in sha
 // The sequence of token t: its number (-1: none) and the tokens around t that share it (offsets out of order give
 // some such range, empty perhaps).
 struct Sequence {
-    int64_t s;
-    int64_t begin, end;
+    int s, begin, end;
 };
-__device__ __forceinline__ Sequence sequence_of(const int32_t* offsets, int64_t sequences, int64_t tokens, int64_t t) {
-    if (offsets == nullptr) return {0, 0, tokens};
-    int64_t lo = 0, hi = sequences + 1;  // the first offset beyond t
+__device__ __forceinline__ Sequence sequence_at(const BalanceArgs& a, int beyond) {  // `beyond`: the first offset beyond the token
+    const int begin = beyond > 0 ? __ldg(a.offsets + beyond - 1) : 0, end = beyond <= a.sequences ? __ldg(a.offsets + beyond) : a.tokens;
+    return {beyond > 0 && beyond <= a.sequences ? beyond - 1 : -1, begin, min(end, a.tokens)};
+}
+__device__ __forceinline__ Sequence sequence_of(const BalanceArgs& a, int t) {
+    if (a.offsets == nullptr) return {0, 0, a.tokens};
+    int lo = 0, hi = a.sequences + 1;
     while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (__ldg(offsets + mid) > t)
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.offsets + mid) > t)
             hi = mid;
         else
             lo = mid + 1;
     }
-    const int64_t begin = lo > 0 ? __ldg(offsets + lo - 1) : 0, end = lo <= sequences ? __ldg(offsets + lo) : tokens;
-    return {lo > 0 && lo <= sequences ? lo - 1 : -1, begin, end < tokens ? end : tokens};
+    return sequence_at(a, lo);
+}
+// The same by a whole warp, 32 offsets at a time.
+__device__ __forceinline__ Sequence warp_sequence_of(const BalanceArgs& a, int t) {
+    if (a.offsets == nullptr) return {0, 0, a.tokens};
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = a.sequences + 1;  // the answer is in [lo, lo + len]
+    while (len > 0) {
+        const int step = (len + 31) / 32, at = min((lane + 1) * step, len) - 1;  // the last of each of 32 shares
+        const int shares = __popc(__ballot_sync(kAll, __ldg(a.offsets + lo + at) <= t));
+        const int skip = min(shares * step, len);
+        lo += skip;
+        len = shares == 32 ? 0 : min(step, len - skip) - 1;  // the last of the share is beyond t
+    }
+    return sequence_at(a, lo);
 }
 
 __global__ void __launch_bounds__(kCountThreads) balance_zero_kernel(const BalanceArgs a) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t all = a.sequences * a.n, step = (int64_t)gridDim.x * kCountThreads;
+    const int64_t all = (int64_t)a.sequences * a.n, step = (int64_t)gridDim.x * kCountThreads;
     for (int64_t i = (int64_t)blockIdx.x * kCountThreads + threadIdx.x; i < all; i += step) a.counts[i] = 0;
     for (int64_t i = (int64_t)blockIdx.x * kCountThreads + threadIdx.x; i < a.sequences; i += step) a.totals[i] = 0;
 }
 
-// The column of entry e of token t, or -1: an entry of weight 0, or an index outside the row (flagged).
-__device__ __forceinline__ int counted_column(const BalanceArgs& a, int64_t e, int64_t t) {
-    int64_t j = a.idx64 ? __ldg(static_cast<const int64_t*>(a.idx) + e) : __ldg(static_cast<const int32_t*>(a.idx) + e);
-    if (a.base != nullptr) j -= a.idx64 ? __ldg(static_cast<const int64_t*>(a.base) + t) : __ldg(static_cast<const int32_t*>(a.base) + t);
-    if (j < 0 || j >= a.n) {
-        atomicOr(&g_balance_status, SDM_DEV_BAD_INDEX);
-        return -1;
+// The columns of N entries e, e + step, ... below `end`, or -1: of weight 0, or an index outside the row (flagged). Their
+// loads are on their way together.
+template <int N>
+__device__ __forceinline__ void counted_columns(const BalanceArgs& a, uint32_t e, uint32_t step, uint32_t end, int* column) {
+    int64_t j[N];
+    float w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t at = e + i * step;
+        j[i] = -1;
+        w[i] = 1.0f;
+        if (at < end) {
+            j[i] = a.idx64 ? __ldg(static_cast<const int64_t*>(a.idx) + at) : __ldg(static_cast<const int32_t*>(a.idx) + at);
+            if (a.w != nullptr) w[i] = __ldg(a.w + at);
+            if (a.base != nullptr) {
+                const uint32_t t = at / (uint32_t)a.k;
+                j[i] -= a.idx64 ? __ldg(static_cast<const int64_t*>(a.base) + t) : __ldg(static_cast<const int32_t*>(a.base) + t);
+            }
+        }
     }
-    return a.w != nullptr && __ldg(a.w + e) == 0.0f ? -1 : (int)j;
+    bool outside = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool in = j[i] >= 0 && j[i] < a.n;
+        outside |= !in && e + i * step < end;
+        column[i] = in && w[i] != 0.0f ? (int)j[i] : -1;
+    }
+    if (outside) atomicOr(&g_balance_status, SDM_DEV_BAD_INDEX);
 }
 
 // Each block counts the entries of a run of tokens. LOCAL: in shared memory, one sequence of the run after the
 // other, so that few entries of a short row do not queue up at the same words of L2.
 template <bool LOCAL>
-__global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const BalanceArgs a, int64_t run) {
+__global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const BalanceArgs a, int run) {
     __shared__ int bins[LOCAL ? kCountBins : 1];
     __shared__ int all;
+    constexpr int N = 4;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t first = blockIdx.x * run, last = first + run < a.tokens ? first + run : a.tokens;
-    const int tid = threadIdx.x;
+    const int first = blockIdx.x * run, last = min(first + run, a.tokens), tid = threadIdx.x;
     if constexpr (LOCAL) {
-        for (int64_t t = first; t < last;) {
-            const Sequence q = sequence_of(a.offsets, a.sequences, a.tokens, t);
-            const int64_t end = q.end < t + 1 ? t + 1 : q.end < last ? q.end : last;
+        for (int t = first; t < last;) {
+            const Sequence q = warp_sequence_of(a, t);
+            const int end = max(t + 1, min(q.end, last));
             if (q.s >= 0) {
                 for (int j = tid; j < a.n; j += kCountThreads) bins[j] = 0;
                 if (tid == 0) all = 0;
                 __syncthreads();
                 int mine = 0;
-                for (int64_t e = t * a.k + tid; e < end * a.k; e += kCountThreads) {
-                    const int j = counted_column(a, e, a.base != nullptr ? (int64_t)((uint32_t)e / (uint32_t)a.k) : 0);
-                    if (j >= 0) {
-                        atomicAdd(&bins[j], 1);
-                        ++mine;
+                const uint32_t until = (uint32_t)end * a.k;
+                for (uint32_t e = (uint32_t)t * a.k + tid; e < until; e += N * kCountThreads) {
+                    int column[N];
+                    counted_columns<N>(a, e, kCountThreads, until, column);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        if (column[i] >= 0) {
+                            atomicAdd(&bins[column[i]], 1);
+                            ++mine;
+                        }
                     }
                 }
                 mine = __reduce_add_sync(kAll, mine);
                 if ((tid & 31) == 0 && mine) atomicAdd(&all, mine);
                 __syncthreads();
                 for (int j = tid; j < a.n; j += kCountThreads)
-                    if (bins[j]) atomicAdd(a.counts + q.s * a.n + j, bins[j]);
+                    if (bins[j]) atomicAdd(a.counts + (int64_t)q.s * a.n + j, bins[j]);
                 if (tid == 0 && all) atomicAdd(a.totals + q.s, all);
                 __syncthreads();
             }
             t = end;
         }
     } else {
-        const int64_t from = first * a.k, to = last * a.k;
-        for (int64_t e0 = from; e0 < to; e0 += kCountThreads) {  // whole warps stay together
-            const int64_t e = e0 + tid;
-            int64_t s = -1;
+        const uint32_t from = (uint32_t)first * a.k, to = (uint32_t)last * a.k;
+        for (uint32_t e0 = from; e0 < to; e0 += kCountThreads) {  // whole warps stay together
+            const uint32_t e = e0 + tid;
+            int s = -1, column = -1;
             if (e < to) {
-                const int64_t t = (uint32_t)e / (uint32_t)a.k;
-                s = sequence_of(a.offsets, a.sequences, a.tokens, t).s;
-                const int j = s >= 0 ? counted_column(a, e, t) : -1;
-                if (j >= 0)
-                    atomicAdd(a.counts + s * a.n + j, 1);
+                s = sequence_of(a, (int)(e / (uint32_t)a.k)).s;
+                if (s >= 0) counted_columns<1>(a, e, 0, to, &column);
+                if (column >= 0)
+                    atomicAdd(a.counts + (int64_t)s * a.n + column, 1);
                 else
                     s = -1;
             }
@@ -231,6 +270,13 @@ struct Row {
     }
 };
 
+// 1 / z of a sum of scores, which is at least 2^-60 or 0 (1 ulp).
+__device__ __forceinline__ float inverse_of(float z) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(z));
+    return z > 0.0f ? r : 0.0f;
+}
+
 // Sums of sigmoid scores below this lose bits; the row's shares are then those of exp(x), as for a softmax.
 constexpr float kLowScores = 0x1p-60f;
 
@@ -238,7 +284,7 @@ constexpr float kLowScores = 0x1p-60f;
 struct Factors {
     float centre, unit, g;
 };
-__device__ __forceinline__ Factors factors_of(const BalanceArgs& a, int64_t s, int64_t length, int total) {
+__device__ __forceinline__ Factors factors_of(const BalanceArgs& a, int s, int length, int total) {
     Factors f{0.0f, 0.0f, 0.0f};
     if (total > 0 && length > 0) {
         const double per = (double)a.n / total;
@@ -274,30 +320,32 @@ struct Run {
     float sum = 0.0f;
 
     // Token t is next; true where another sequence begins.
-    __device__ __forceinline__ bool next(const BalanceArgs& a, int64_t t, int64_t team, bool writes) {
+    __device__ __forceinline__ bool next(const BalanceArgs& a, int t, int team, bool writes) {
         if (t >= q.begin && t < q.end) return false;
         done(a, team, writes);
         sum = 0.0f;
-        q = sequence_of(a.offsets, a.sequences, a.tokens, t);
+        q = sequence_of(a, t);
         f = q.s >= 0 ? factors_of(a, q.s, q.end - q.begin, __ldg(a.totals + q.s)) : Factors{0.0f, 0.0f, 0.0f};
         return true;
     }
-    __device__ __forceinline__ void done(const BalanceArgs& a, int64_t team, bool writes) const {
+    __device__ __forceinline__ void done(const BalanceArgs& a, int team, bool writes) const {
         if (q.s >= 0 && writes) a.parts[team + q.s] = sum;
     }
 };
 
 // Rows of up to 512 entries: TEAM lanes a row, E logits each. The next token's row is on its way while a warp
-// works on one, and the counts of the sequence stay in registers.
+// works on one, and the counts of the sequence stay in registers. Half as many lanes with twice the logits spend less on
+// what a row costs whatever its length: 65536 rows of 256 bf16 with the gradient, 16 lanes TIME16 us, 32 lanes 33.
 template <int TEAM, int E, bool VEC, bool GRAD, typename L>
-__global__ void __launch_bounds__(128, E <= 8 ? (sizeof(L) == 2 && VEC ? 8 : 6) : 5) balance_lanes_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(128, 5) balance_lanes_kernel(const BalanceArgs a) {
     using R = Row<TEAM, E, VEC, L>;
     constexpr int TEAMS = 128 / TEAM, V = R::V, ACCESSES = E / V;
     constexpr bool AHEAD = R::RAW <= 8;
     grid_dependency_wait();
     grid_launch_dependents();
     const R r(a, threadIdx.x % TEAM);
-    const int64_t team = (int64_t)blockIdx.x * TEAMS + threadIdx.x / TEAM, first = team * a.rows;
+    const int team = blockIdx.x * TEAMS + threadIdx.x / TEAM, first = (int)min((int64_t)team * a.rows, (int64_t)a.tokens);
+    const int count = min(a.rows, a.tokens - first), steps = __reduce_max_sync(kAll, count);
     const bool whole = reinterpret_cast<uintptr_t>(a.counts) % 16 == 0 && a.n % 4 == 0, softmax = a.score == SDM_SOFTMAX;
     Run run;
     float counts[E];
@@ -308,11 +356,10 @@ __global__ void __launch_bounds__(128, E <= 8 ? (sizeof(L) == 2 && VEC ? 8 : 6) 
 #pragma unroll
         for (int i = 0; i < ACCESSES; ++i) r.get(row, on ? r.column(i) : r.n, w + i * R::W, fill);
     };
-    const L* row = static_cast<const L*>(a.logits) + (first < a.tokens ? first : 0) * a.row_stride;
-    if constexpr (AHEAD) get_all(row, first < a.tokens, next, R::kNone);
-    const int count = (int)min(a.rows, max(a.tokens - first, (int64_t)0)), steps = __reduce_max_sync(kAll, count);
+    const L *row = static_cast<const L*>(a.logits) + first * a.row_stride, *add = static_cast<const L*>(a.add) + (a.add ? first * a.add_stride : 0);
+    L* out = static_cast<L*>(a.dlogits) + (GRAD ? first * a.dlogits_stride : 0);
+    if constexpr (AHEAD) get_all(row, count > 0, next, R::kNone);
     for (int i = 0; i < steps; ++i) {  // lanes of a warp that hold several teams stay together
-        const int64_t t = first + i;
         const bool on = i < count;
         if constexpr (AHEAD) {
 #pragma unroll
@@ -322,12 +369,12 @@ __global__ void __launch_bounds__(128, E <= 8 ? (sizeof(L) == 2 && VEC ? 8 : 6) 
             get_all(row, on, raw, R::kNone);
         }
         uint32_t adds[GRAD ? R::RAW : 1];
-        if (GRAD && a.add != nullptr) get_all(static_cast<const L*>(a.add) + (on ? t : 0) * a.add_stride, on, adds, 0u);
-        if (on && run.next(a, t, team, r.tid == 0)) {
+        if (GRAD && a.add != nullptr) get_all(add, on, adds, 0u);
+        if (on && run.next(a, first + i, team, r.tid == 0)) {
 #pragma unroll
             for (int e = 0; e < E; e += V) {
                 if (run.q.s >= 0) {
-                    centred<V>(a.counts + run.q.s * a.n, a.n, whole, run.f.centre, r.column(e / V), counts + e);
+                    centred<V>(a.counts + (int64_t)run.q.s * a.n, a.n, whole, run.f.centre, r.column(e / V), counts + e);
                 } else {
 #pragma unroll
                     for (int v = 0; v < V; ++v) counts[e + v] = 0.0f;
@@ -335,24 +382,28 @@ __global__ void __launch_bounds__(128, E <= 8 ? (sizeof(L) == 2 && VEC ? 8 : 6) 
             }
         }
         __syncwarp();
-        float kept[E], m = 0.0f, z = 0.0f, d = 0.0f;
-        // the shares of exp(x), in all lanes of the warp; `mine`: in this team's
+        float kept[E], z = 0.0f, d = 0.0f;
+        // the shares of exp(x); every lane of the warp takes part, `mine` says whose team means it
         const auto soft = [&](bool mine) {
-            float top = minus_inf(), zs = 0.0f, ds = 0.0f, y[E], e[E];
+            float top = minus_inf(), zs = 0.0f, ds = 0.0f, y[V], e[V];
 #pragma unroll
-            for (int i2 = 0; i2 < ACCESSES; ++i2) R::unpack(raw + i2 * R::W, y + i2 * V);
+            for (int i2 = 0; i2 < ACCESSES; ++i2) {
+                R::unpack(raw + i2 * R::W, y);
 #pragma unroll
-            for (int i2 = 0; i2 < E; ++i2) top = fmaxf(top, y[i2]);  // NaN is left out
+                for (int v = 0; v < V; ++v) top = fmaxf(top, y[v]);  // NaN is left out
+            }
             top = warp_max<TEAM>(top);
 #pragma unroll
-            for (int i2 = 0; i2 < E; i2 += V) R::soft_scores(y + i2, top, counts + i2, e + i2, zs, ds);
+            for (int i2 = 0; i2 < ACCESSES; ++i2) {
+                R::unpack(raw + i2 * R::W, y);
+                R::soft_scores(y, top, counts + i2 * V, e, zs, ds);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (mine) kept[i2 * V + v] = e[v];
+            }
             zs = warp_sum<TEAM>(zs);
             ds = warp_sum<TEAM>(ds);
-            if (mine) {
-                m = top, z = zs, d = ds;
-#pragma unroll
-                for (int i2 = 0; i2 < E; ++i2) kept[i2] = e[i2];
-            }
+            if (mine) z = zs, d = ds;
         };
         if (softmax) {
             soft(true);
@@ -368,20 +419,21 @@ __global__ void __launch_bounds__(128, E <= 8 ? (sizeof(L) == 2 && VEC ? 8 : 6) 
             const bool low = on && z < kLowScores;
             if (__any_sync(kAll, low)) soft(low);
         }
-        const float inverse = z > 0.0f ? __frcp_rn(z) : 0.0f, mean = d * inverse;
+        const float inverse = inverse_of(z), mean = d * inverse;
         if (z > 0.0f) run.sum += fmaf(run.f.unit, mean, 1.0f);
         if (GRAD && on) {
-            L* out = static_cast<L*>(a.dlogits) + t * a.dlogits_stride;
             const float gz = run.f.g * inverse, gm = -gz * mean;
 #pragma unroll
             for (int i2 = 0; i2 < ACCESSES; ++i2) {
-                float add[V];
+                float more[V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) add[v] = 0.0f;
-                if (a.add != nullptr) R::unpack(adds + i2 * R::W, add);
-                R::gradient(kept + i2 * V, counts + i2 * V, gz, gm, add);
+                for (int v = 0; v < V; ++v) more[v] = 0.0f;
+                if (a.add != nullptr) R::unpack(adds + i2 * R::W, more);
+                R::gradient(kept + i2 * V, counts + i2 * V, gz, gm, more);
                 r.put(out, r.column(i2), kept + i2 * V);
             }
+            out += a.dlogits_stride;
+            add += a.add_stride;
         }
         row += a.row_stride;
     }
@@ -401,14 +453,14 @@ __global__ void __launch_bounds__(TEAM, 1024 / TEAM) balance_block_kernel(const 
     grid_launch_dependents();
     float* stage = reinterpret_cast<float*>(stage4);
     const R r(a, threadIdx.x);
-    const int64_t first = blockIdx.x * a.rows, last = min(first + a.rows, a.tokens);
+    const int first = (int)min((int64_t)blockIdx.x * a.rows, (int64_t)a.tokens), last = first + min(a.rows, a.tokens - first);
     const bool whole = reinterpret_cast<uintptr_t>(a.counts) % 16 == 0 && a.n % 4 == 0, softmax = a.score == SDM_SOFTMAX;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Run run;
-    for (int64_t t = first; t < last; ++t) {
+    for (int t = first; t < last; ++t) {
         run.next(a, t, blockIdx.x, threadIdx.x == 0);
         const L* row = static_cast<const L*>(a.logits) + t * a.row_stride;
-        const int32_t* from = run.q.s >= 0 ? a.counts + run.q.s * a.n : nullptr;
+        const int32_t* from = run.q.s >= 0 ? a.counts + (int64_t)run.q.s * a.n : nullptr;
         const auto counts = [&](int j, float* c) {
             if (from != nullptr) {
                 centred<V>(from, a.n, whole, run.f.centre, j, c);
@@ -498,7 +550,7 @@ __global__ void __launch_bounds__(TEAM, 1024 / TEAM) balance_block_kernel(const 
             m = minus_inf();
             z = d = 0.0f;
         }
-        const float inverse = z > 0.0f ? __frcp_rn(z) : 0.0f, mean = d * inverse;
+        const float inverse = inverse_of(z), mean = d * inverse;
         if (z > 0.0f) run.sum += fmaf(run.f.unit, mean, 1.0f);
         if constexpr (GRAD) {
             L* out = static_cast<L*>(a.dlogits) + t * a.dlogits_stride;
@@ -546,16 +598,16 @@ __global__ void __launch_bounds__(kCountThreads) balance_loss_kernel(const Balan
     __shared__ double sums[kCountThreads / 32];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t s = blockIdx.x;
-    int64_t begin = 0, end = a.tokens;
+    const int s = blockIdx.x;
+    int begin = 0, end = a.tokens;
     if (a.offsets != nullptr) {
-        begin = max((int64_t)__ldg(a.offsets + s), (int64_t)0);
-        end = min((int64_t)__ldg(a.offsets + s + 1), a.tokens);
+        begin = max(__ldg(a.offsets + s), 0);
+        end = min(__ldg(a.offsets + s + 1), a.tokens);
     }
     const bool any = end > begin && a.totals[s] > 0;
     double sum = 0.0;
     if (any)
-        for (int64_t p = begin / a.rows + s + threadIdx.x; p <= (end - 1) / a.rows + s; p += kCountThreads) sum += a.parts[p];
+        for (int p = begin / a.rows + s + threadIdx.x; p <= (end - 1) / a.rows + s; p += kCountThreads) sum += a.parts[p];
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
@@ -573,7 +625,7 @@ struct Team {
     size_t smem;
 };
 
-// Eight logits a lane up to 256 entries, in fewer lanes for shorter rows; then blocks of 128 to 512 threads, which
+// Sixteen logits a lane up to 512 entries, in fewer lanes for shorter rows; then blocks of 128 to 512 threads, which
 // stage rows of up to 48 K entries.
 constexpr int kStaged = 48 * 1024;
 template <int TEAM, bool VEC, bool GRAD, typename L>
@@ -585,10 +637,10 @@ Team block_team(int n) {
 }
 template <bool VEC, bool GRAD, typename L>
 Team rows_team(int n) {
-    if (n <= 32) return {(const void*)balance_lanes_kernel<4, 8, VEC, GRAD, L>, 128, 32, 0};
-    if (n <= 64) return {(const void*)balance_lanes_kernel<8, 8, VEC, GRAD, L>, 128, 16, 0};
-    if (n <= 128) return {(const void*)balance_lanes_kernel<16, 8, VEC, GRAD, L>, 128, 8, 0};
-    if (n <= 256) return {(const void*)balance_lanes_kernel<32, 8, VEC, GRAD, L>, 128, 4, 0};
+    if (n <= 32) return {(const void*)balance_lanes_kernel<2, 16, VEC, GRAD, L>, 128, 64, 0};
+    if (n <= 64) return {(const void*)balance_lanes_kernel<4, 16, VEC, GRAD, L>, 128, 32, 0};
+    if (n <= 128) return {(const void*)balance_lanes_kernel<8, 16, VEC, GRAD, L>, 128, 16, 0};
+    if (n <= 256) return {(const void*)balance_lanes_kernel<16, 16, VEC, GRAD, L>, 128, 8, 0};
     if (n <= 512) return {(const void*)balance_lanes_kernel<32, 16, VEC, GRAD, L>, 128, 4, 0};
     if (n <= 6144) return block_team<128, VEC, GRAD, L>(n);
     return n <= 12288 ? block_team<256, VEC, GRAD, L>(n) : block_team<512, VEC, GRAD, L>(n);
@@ -605,29 +657,29 @@ int64_t balance_workspace(int64_t sequences) { return 4 * ((sequences + 63) / 64
 int launch_balance(const BalanceArgs& a0, cudaStream_t stream) {
     BalanceArgs a = a0;
     a.totals = static_cast<int32_t*>(a.workspace);
-    a.parts = reinterpret_cast<float*>(a.totals + (a.sequences + 63) / 64 * 64);
+    a.parts = reinterpret_cast<float*>(a.totals + ((int64_t)a.sequences + 63) / 64 * 64);
     const size_t es = a.logit_bf16 ? 2 : 4;
     const auto whole = [&](const void* p, int64_t stride) {
         return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * es % 16 == 0);
     };
     const bool vec = whole(a.logits, a.row_stride) && whole(a.dlogits, a.dlogits_stride) && whole(a.add, a.add_stride), grad = a.dlogits != nullptr;
     const Team team = a.logit_bf16 ? rows_team<uint16_t>(a.n, vec, grad) : rows_team<float>(a.n, vec, grad);
-    const int64_t sms = sm_count();
+    const int sms = sm_count();
     if (a.sequences > 0) {
-        const int64_t zeros = std::min<int64_t>((a.sequences * a.n + 4 * kCountThreads - 1) / (4 * kCountThreads), 8 * sms);
+        const int64_t zeros = std::min<int64_t>(((int64_t)a.sequences * a.n + 4 * kCountThreads - 1) / (4 * kCountThreads), 8 * sms);
         void* args[] = {&a};
         int rc = launch_pdl_raw((const void*)balance_zero_kernel, dim3((unsigned)zeros), dim3(kCountThreads), 0, stream, args);
         if (rc != 0) return rc;
     }
     if (a.sequences > 0 && a.tokens > 0) {
-        const int64_t entries = a.tokens * a.k;
-        int64_t blocks = std::min<int64_t>(std::min<int64_t>((entries + 4 * kCountThreads - 1) / (4 * kCountThreads), 4 * sms), a.tokens);
-        int64_t run = (a.tokens + blocks - 1) / blocks;
+        const int64_t entries = (int64_t)a.tokens * a.k;
+        int blocks = (int)std::min<int64_t>(std::min<int64_t>((entries + 4 * kCountThreads - 1) / (4 * kCountThreads), 4 * sms), a.tokens);
+        int run = (a.tokens + blocks - 1) / blocks;
         blocks = (a.tokens + run - 1) / run;
-        const bool local = a.n <= kCountBins && entries >= 2 * a.n * (blocks + a.sequences);
+        const bool local = a.n <= kCountBins && entries >= (int64_t)2 * a.n * (blocks + a.sequences);
         void* args[] = {&a, &run};
         const int rc = launch_pdl_raw(local ? (const void*)balance_count_kernel<true> : (const void*)balance_count_kernel<false>,
-                                      dim3((unsigned)blocks), dim3(kCountThreads), 0, stream, args);
+                                      dim3(blocks), dim3(kCountThreads), 0, stream, args);
         if (rc != 0) return rc;
     }
     a.rows = 1;
@@ -635,9 +687,9 @@ int launch_balance(const BalanceArgs& a0, cudaStream_t stream) {
         // runs that fill the GPU once
         int rc = allow_smem(team.fn, team.smem);
         if (rc != 0) return rc;
-        const int64_t most = std::min<int64_t>(kBalanceTeams, sms * std::max(1, blocks_per_sm(team.fn, team.threads, team.smem)) * team.teams);
-        a.rows = (a.tokens + most - 1) / most;
-        const int64_t teams = (a.tokens + a.rows - 1) / a.rows;
+        const int most = std::min(kBalanceTeams, sms * std::max(1, blocks_per_sm(team.fn, team.threads, team.smem)) * team.teams);
+        a.rows = (a.tokens - 1) / most + 1;
+        const int teams = (a.tokens - 1) / a.rows + 1;
         void* args[] = {&a};
         rc = launch_pdl_raw(team.fn, dim3((unsigned)((teams + team.teams - 1) / team.teams)), dim3(team.threads), team.smem, stream, args);
         if (rc != 0) return rc;

@@ -7,7 +7,7 @@
 // each warp and column slice, however unevenly the slots share them: a run of equal slots that crosses the ends of
 // pieces leaves one float32 sum for each of them, which a last launch adds up in order.
 //   up to 512 entries    one launch: the warp of a slot's first entry finds the others by scanning all of them
-//   up to 2048           ranks by counting: an entry's place is the number of entries that come before it
+//   up to 8192           ranks by counting: an entry's place is the number of entries that come before it
 //   more                 a stable radix sort with digits of at most 11 bits: counts, their running sums, places
 // Rows without entries are set to zero by blocks of the same launch as the sums, which search the sorted slots.
 #include <algorithm>
@@ -23,7 +23,7 @@ __device__ unsigned int g_row_sums_status;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr uint32_t kDirect = 512;    // entries that one launch sums
-constexpr uint32_t kRanked = 2048;   // entries ranked by counting
+constexpr uint32_t kRanked = 8192;   // entries ranked by counting
 constexpr int kMostBits = 11;
 constexpr int kZeroRows = 256;       // rows that a block sets to zero, at most
 
@@ -94,19 +94,22 @@ __device__ __forceinline__ Pack<D, V> load_pack(const D* p) {
     return *reinterpret_cast<const Pack<D, V>*>(p);
 }
 
+template <typename O>
+__device__ __forceinline__ O* place_in(const RowSumArgs& a, uint32_t row, int col) {
+    return static_cast<O*>(a.out) + (uint64_t)row * (uint32_t)a.hd + col;
+}
+// A row's sum goes to its place, `there` being what is there where sums are added to it.
 template <typename O, int V>
-__device__ __forceinline__ void put_row(const RowSumArgs& a, uint32_t row, int col, const float* sum) {
-    Pack<O, V>* to = reinterpret_cast<Pack<O, V>*>(static_cast<O*>(a.out) + (uint64_t)row * (uint32_t)a.hd + col);
+__device__ __forceinline__ void put_row(const RowSumArgs& a, uint32_t row, int col, const float* sum, const Pack<O, V>& there) {
     Pack<O, V> y;
     if (a.accumulate) {
-        y = *to;
 #pragma unroll
-        for (int c = 0; c < V; ++c) y.v[c] = from_f32<O>(fmaf(sum[c], a.scale, to_f32(y.v[c])));
+        for (int c = 0; c < V; ++c) y.v[c] = from_f32<O>(fmaf(sum[c], a.scale, to_f32(there.v[c])));
     } else {
 #pragma unroll
         for (int c = 0; c < V; ++c) y.v[c] = from_f32<O>(sum[c] * a.scale);
     }
-    *to = y;
+    *reinterpret_cast<Pack<O, V>*>(place_in<O>(a, row, col)) = y;
 }
 
 // Rows [first, first + count) of the output whose flag is not set become zero, by a block: copies of `zeros` in shared
@@ -196,7 +199,9 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
     float sum[V];
 #pragma unroll
     for (int c = 0; c < V; ++c) sum[c] = 0.0f;
-    constexpr int U = 8;
+    Pack<O, V> there;
+    if (a.accumulate) there = load_pack<O, V>(place_in<O>(a, key, col));  // on its way meanwhile
+    constexpr int U = 16;
     for (int i0 = 0; i0 < found; i0 += U) {
         Pack<D, V> x[U];
         float w[U];
@@ -216,26 +221,32 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
             }
         }
     }
-    put_row<O, V>(a, key, col, sum);
+    put_row<O, V>(a, key, col, sum, there);
 }
 
 // ---------------------------------------------------------------- the sort
 
-// Places by counting. A block takes 32 entries, a warp four of them, and compares with all.
-__global__ void __launch_bounds__(kThreads) rank_kernel(const RowSumArgs a, uint2* sorted) {
-    extern __shared__ uint32_t all[];
-    __shared__ int alive[kWarps];
+// Places by counting. Slot and number of an entry make one number (of type C: 32 bits where both fit), so that an entry
+// comes after all smaller ones. A block takes 64 entries, a warp four of them, and compares with all.
+constexpr int kRankThreads = 512, kRankBits = 13;  // bits of an entry's number
+template <typename C>
+__global__ void __launch_bounds__(kRankThreads) rank_kernel(const RowSumArgs a, uint2* sorted) {
+    extern __shared__ uint64_t rank_smem[];
+    __shared__ int alive[kRankThreads / 32];
+    C* all = reinterpret_cast<C*>(rank_smem);
     grid_dependency_wait();
     grid_launch_dependents();
     const int n = (int)a.entries, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int live = 0;
-    for (int e0 = threadIdx.x; e0 < n; e0 += 8 * kThreads) {
+    for (int e0 = threadIdx.x; e0 < n; e0 += 8 * kRankThreads) {
         uint32_t key[8];
-        keys_of<8>(a, e0, kThreads, key);
+        keys_of<8>(a, e0, kRankThreads, key);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (e0 + i * kThreads < n) all[e0 + i * kThreads] = key[i];
-            live += key[i] < a.n_slots;
+            const int e = e0 + i * kRankThreads;
+            const bool in = key[i] < a.n_slots;
+            if (e < n) all[e] = in ? (C)key[i] << kRankBits | (C)e : ~(C)0;  // those that take no part come last
+            live += in;
         }
     }
     if (blockIdx.x == 0) {
@@ -245,25 +256,25 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const RowSumArgs a, uint
     __syncthreads();
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         live = 0;
-        for (int w = 0; w < kWarps; ++w) live += alive[w];
+        for (int w = 0; w < kRankThreads / 32; ++w) live += alive[w];
         a.counters[0] = live;
         a.counters[1] = 0;
     }
-    const int e0 = blockIdx.x * 32 + warp * 4;
-    uint32_t key[4];
+    const int e0 = (blockIdx.x * (kRankThreads / 32) + warp) * 4;
+    C mine[4];
     int before[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) key[q] = e0 + q < n ? all[e0 + q] : 0u;
-#pragma unroll 4
+    for (int q = 0; q < 4; ++q) mine[q] = e0 + q < n ? all[e0 + q] : (C)0;
+#pragma unroll 8
     for (int i = lane; i < n; i += 32) {
-        const uint32_t k = all[i];
+        const C c = all[i];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) before[q] += k < key[q] || (k == key[q] && i < e0 + q);
+        for (int q = 0; q < 4; ++q) before[q] += c < mine[q];
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         before[q] = __reduce_add_sync(kAll, before[q]);
-        if (lane == q && e0 + q < n && key[q] < a.n_slots) sorted[before[q]] = make_uint2(key[q], e0 + q);
+        if (lane == q && e0 + q < n && mine[q] != ~(C)0) sorted[before[q]] = make_uint2((uint32_t)(mine[q] >> kRankBits), e0 + q);
     }
 }
 
@@ -330,37 +341,56 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t own, uint32_t* sums, uin
     return before + sum - own;
 }
 
-// Each digit's counts become their running sums over the tiles, and their total. A block takes 32 digits, a lane
-// each; its warps share out the tiles.
-constexpr int kScanWarps = 32;
-__global__ void __launch_bounds__(32 * kScanWarps) digit_scan_kernel(uint32_t* counts, uint32_t* totals, int tiles, int bits) {
-    __shared__ uint32_t sums[kScanWarps][32];
+// Each digit's counts become their running sums over the tiles, and their total. A block takes 8 digits, whose
+// counts of a tile are one 32-byte sector; 128 threads a digit share out the tiles.
+constexpr int kScanThreads = 1024, kScanDigits = 8, kScanShares = kScanThreads / kScanDigits;
+__global__ void __launch_bounds__(kScanThreads) digit_scan_kernel(uint32_t* counts, uint32_t* totals, int tiles, int bits) {
+    __shared__ uint32_t sums[kScanShares][kScanDigits + 1];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = (tiles + kScanWarps - 1) / kScanWarps;
-    const int digit = blockIdx.x * 32 + lane, first = warp * share, last = min(first + share, tiles);
-    if (blockIdx.x * 32 >= 1u << bits) return;
+    const int in = threadIdx.x % kScanDigits, share = threadIdx.x / kScanDigits, digit = blockIdx.x * kScanDigits + in;
+    const int each = (tiles + kScanShares - 1) / kScanShares, first = share * each, last = min(first + each, tiles);
     const bool on = digit < 1 << bits;
     uint32_t* column = counts + (on ? digit : 0);
-    uint32_t sum = 0;
-#pragma unroll 16
-    for (int t = first; t < last; ++t) sum += column[(int64_t)t << bits];
-    sums[warp][lane] = sum;
-    __syncthreads();
-    uint32_t before = 0, all = 0;
+    constexpr int U = 16;
+    uint32_t own[U], sum = 0;  // of as many tiles as a thread has, up to 2048 of them; of more they are read again
+    for (int t0 = first; t0 < last; t0 += U) {
 #pragma unroll
-    for (int w = 0; w < kScanWarps; ++w) {
-        if (w < warp) before += sums[w][lane];
-        all += sums[w][lane];
+        for (int i = 0; i < U; ++i) own[i] = t0 + i < last ? column[(int64_t)(t0 + i) << bits] : 0u;
+#pragma unroll
+        for (int i = 0; i < U; ++i) sum += own[i];
     }
+    sums[share][in] = sum;
+    __syncthreads();
+    if (threadIdx.x < 32 * kScanDigits) {  // a warp for each digit, four shares a lane
+        const int d = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        uint32_t part[kScanShares / 32], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kScanShares / 32; ++i) mine += part[i] = sums[lane * (kScanShares / 32) + i][d];
+        uint32_t before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(kAll, before, o);
+            if (lane >= o) before += y;
+        }
+        if (lane == 31 && blockIdx.x * kScanDigits + d < 1 << bits) totals[blockIdx.x * kScanDigits + d] = before;
+        before -= mine;
+#pragma unroll
+        for (int i = 0; i < kScanShares / 32; ++i) {
+            sums[lane * (kScanShares / 32) + i][d] = before;
+            before += part[i];
+        }
+    }
+    __syncthreads();
     if (!on) return;
-    if (warp == 0) totals[digit] = all;
-    for (int t0 = first; t0 < last; t0 += 16) {
-        uint32_t own[16];
+    uint32_t before = sums[share][in];
+    for (int t0 = first; t0 < last; t0 += U) {
+        if (each > U) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) own[i] = t0 + i < last ? column[(int64_t)(t0 + i) << bits] : 0u;
+            for (int i = 0; i < U; ++i) own[i] = t0 + i < last ? column[(int64_t)(t0 + i) << bits] : 0u;
+        }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < U; ++i) {
             if (t0 + i < last) column[(int64_t)(t0 + i) << bits] = before;
             before += own[i];
         }
@@ -518,8 +548,10 @@ struct alignas(16) Entry {
 
 constexpr uint32_t kShort = 32;  // entries of a run beyond the end of a piece that its warp sums as well
 
-template <typename D, typename O, int V>
-__global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : 3) sums_kernel(const RowSumArgs a, int zero_span) {
+// ACC: sums are added to what is there, which is loaded beside the entries that end a run, so that it is at hand
+// when they do.
+template <typename D, typename O, int V, bool ACC>
+__global__ void __launch_bounds__(kThreads, V <= 4 ? (ACC ? 3 : 4) : (ACC ? 2 : 3)) sums_kernel(const RowSumArgs a, int zero_span) {
     __shared__ union {
         uint4 zeros[kZeroBytes / 16];
         Entry<D> batch[kWarps][32];
@@ -583,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : 3) sums_kernel(const Ro
     float sum[V];
 #pragma unroll
     for (int c = 0; c < V; ++c) sum[c] = 0.0f;
-    const auto flush = [&](bool ends) {
+    const auto flush = [&](bool ends, const Pack<O, V>& there) {
         if (continues || !ends) {
             if (on) {
                 Pack<float, V> part;
@@ -593,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : 3) sums_kernel(const Ro
             }
             if (!continues && slice == 0 && lane == 0) a.list[atomicAdd(a.counters + 1, 1u)] = (uint32_t)piece;
         } else if (on) {
-            put_row<O, V>(a, current, col, sum);
+            put_row<O, V>(a, current, col, sum, there);
         }
         continues = false;
 #pragma unroll
@@ -620,17 +652,22 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : 3) sums_kernel(const Ro
         constexpr int U = 8;
         for (int j0 = 0; j0 < left; j0 += U) {
             const int count = left - j0;
+            const unsigned first = begins >> j0;
             Pack<D, V> x[U];
+            Pack<O, V> there[ACC ? U : 1];  // of the run before the entry
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (u < count && on) x[u] = load_pack<D, V>(mine[j0 + u].row + col);
+                if (ACC && (first >> u & 1) && on) {
+                    const uint32_t row = j0 + u > 0 ? mine[j0 + u - 1].key : current;
+                    there[u] = load_pack<O, V>(place_in<O>(a, row, col));
+                }
             }
-            const unsigned first = begins >> j0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (u < count) {
                     if (first >> u & 1) {
-                        flush(true);
+                        flush(true, there[ACC ? u : 0]);
                         current = mine[j0 + u].key;
                     }
                     const float w = mine[j0 + u].w;
@@ -641,7 +678,9 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : 3) sums_kernel(const Ro
         }
         __syncwarp();
     }
-    flush(!goes_on);
+    Pack<O, V> there;
+    if (ACC && on) there = load_pack<O, V>(place_in<O>(a, current, col));
+    flush(!goes_on, there);
 }
 
 // The listed runs, which go on far beyond the piece they begin in: the sum in that piece, then those in the pieces that
@@ -684,7 +723,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const RowSumArgs a) {
                 sum[c] = tail.v[c];
                 for (int w = 0; w < kWarps; ++w) sum[c] += parts[w][in_slice + c];
             }
-            put_row<O, V>(a, key, col, sum);
+            Pack<O, V> there;
+            if (a.accumulate) there = load_pack<O, V>(place_in<O>(a, key, col));
+            put_row<O, V>(a, key, col, sum, there);
         }
         __syncthreads();
     }
@@ -694,12 +735,17 @@ struct Kernels {
     const void *direct, *sums, *join;
 };
 template <typename D, typename O, int V>
-Kernels kernels() {
-    return {(const void*)direct_kernel<D, O, V>, (const void*)sums_kernel<D, O, V>, (const void*)join_kernel<O, V>};
+Kernels kernels(bool accumulate) {
+    return {(const void*)direct_kernel<D, O, V>, accumulate ? (const void*)sums_kernel<D, O, V, true> : (const void*)sums_kernel<D, O, V, false>,
+            (const void*)join_kernel<O, V>};
 }
 template <typename D, typename O>
-Kernels kernels(int v) {
-    return v == 8 ? kernels<D, O, 8>() : v == 4 ? kernels<D, O, 4>() : v == 2 ? kernels<D, O, 2>() : kernels<D, O, 1>();
+Kernels kernels(int v, bool accumulate) {
+    constexpr int MOST = 16 / sizeof(D);
+    return v == MOST       ? kernels<D, O, MOST>(accumulate)
+           : v == MOST / 2 ? kernels<D, O, MOST / 2>(accumulate)
+           : v == MOST / 4 ? kernels<D, O, MOST / 4>(accumulate)
+                           : kernels<D, O, 1>(accumulate);
 }
 
 // Entries of a piece: as many as leave 8192 pieces and slices of 256 columns, so that all warps have work, from 16,
@@ -779,7 +825,7 @@ int launch_sort(const RowSumArgs& a, const Layout& l, uint32_t* words, const uin
         if (rc == 0 && r.scanned) {
             int tiles = (int)r.tiles;
             void* scan_args[] = {&counts, &totals, &tiles, &r.bits};
-            rc = launch_pdl_raw((const void*)digit_scan_kernel, dim3(((1u << r.bits) + 31) / 32), dim3(32 * kScanWarps), 0, stream, scan_args);
+            rc = launch_pdl_raw((const void*)digit_scan_kernel, dim3(((1u << r.bits) + kScanDigits - 1) / kScanDigits), dim3(kScanThreads), 0, stream, scan_args);
         }
         if (rc != 0) return rc;
         void* place_args[] = {&args, &keys, &in, &out, &counts, &totals, &digit};
@@ -815,8 +861,9 @@ int launch_row_sums(const RowSumArgs& a0, cudaStream_t stream) {
     const int packs = (a.hd + v - 1) / v;
     a.slices = (packs + 31) / 32;
     a.slice_cols = (packs + a.slices - 1) / a.slices * v;
-    const Kernels fn = a.dout_bf16 ? (a.out_bf16 ? kernels<uint16_t, uint16_t>(v) : kernels<uint16_t, float>(v))
-                                   : (a.out_bf16 ? kernels<float, uint16_t>(v) : kernels<float, float>(v));
+    const bool acc = a.accumulate != 0;
+    const Kernels fn = a.dout_bf16 ? (a.out_bf16 ? kernels<uint16_t, uint16_t>(v, acc) : kernels<uint16_t, float>(v, acc))
+                                   : (a.out_bf16 ? kernels<float, uint16_t>(v, acc) : kernels<float, float>(v, acc));
     // rows that a block sets to zero: 128 KB of them
     int zero_span = (int)std::clamp<int64_t>((int64_t)128 * 1024 / ((int64_t)a.hd * (a.out_bf16 ? 2 : 4)), 8, kZeroRows);
     a.zero_blocks = a.accumulate ? 0 : (a.n_slots + zero_span - 1) / zero_span;
@@ -839,7 +886,12 @@ int launch_row_sums(const RowSumArgs& a0, cudaStream_t stream) {
     if (a.entries <= kRanked) {
         uint2* sorted = reinterpret_cast<uint2*>(words + l.pairs);
         void* args[] = {&a, &sorted};
-        rc = launch_pdl_raw((const void*)rank_kernel, dim3((a.entries + 31) / 32), dim3(kThreads), a.entries * 4, stream, args);
+        const bool narrow = a.n_slots <= (int64_t)1 << (32 - kRankBits);
+        const void* rank = narrow ? (const void*)rank_kernel<uint32_t> : (const void*)rank_kernel<uint64_t>;
+        const size_t smem = a.entries * (narrow ? 4 : 8);
+        rc = allow_smem(rank, smem + 1024);  // and what the kernel has besides
+        if (rc != 0) return rc;
+        rc = launch_pdl_raw(rank, dim3((a.entries + 63) / 64), dim3(kRankThreads), smem, stream, args);
         a.sorted = sorted;
     } else {
         rc = launch_sort(a, l, words, &a.sorted, stream);

@@ -90,7 +90,7 @@ int sdm_balance(const void* logits, int64_t row_stride, int logit_dtype, const v
     a.idx = idx;
     a.w = w;
     a.offsets = offsets;
-    a.sequences = sequences;
+    a.sequences = static_cast<int>(sequences);
     a.loss = loss;
     a.counts = counts;
     a.dloss = dloss;
@@ -98,7 +98,7 @@ int sdm_balance(const void* logits, int64_t row_stride, int logit_dtype, const v
     a.add_stride = add_stride;
     a.dlogits = dlogits;
     a.dlogits_stride = dlogits_stride;
-    a.tokens = tokens;
+    a.tokens = static_cast<int>(tokens);
     a.n = n;
     a.k = k;
     a.score = score;

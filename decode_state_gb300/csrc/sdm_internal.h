@@ -131,7 +131,7 @@ struct BalanceArgs {
     const void* idx;
     const float* w;  // nullptr: every entry counts
     const int32_t* offsets;  // nullptr: one sequence of all tokens
-    int64_t sequences;
+    int sequences;
     float* loss;
     int32_t* counts;
     const float* dloss;
@@ -139,14 +139,13 @@ struct BalanceArgs {
     int64_t add_stride;
     void* dlogits;
     int64_t dlogits_stride;
-    int64_t tokens;
-    int n, k, score;
+    int tokens, n, k, score;
     float scale;
     int idx64, logit_bf16;
     void* workspace;
     int32_t* totals;  // [sequences] in the workspace: entries counted
     float* parts;     // [teams + sequences] in the workspace: a team's part of a sequence's loss
-    int64_t rows;     // consecutive tokens of a team
+    int rows;         // consecutive tokens of a team
 };
 constexpr int kBalanceTeams = 65536;
 
