@@ -186,14 +186,17 @@ struct Row {
     __device__ __forceinline__ int column(int i) const { return (i * TEAM + tid) * V; }  // of access i
 
     // the V entries from j on as they lie in memory; behind the end of the row, `fill` (the bits of an entry)
+    __device__ __forceinline__ void get_inside(const L* row, int j, uint32_t* w) const {
+        if constexpr (VEC) {
+            const uint4 v = *reinterpret_cast<const uint4*>(row + j);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[W - 1] = v.w;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(row + j);
+        }
+    }
     __device__ __forceinline__ void get(const L* row, int j, uint32_t* w, uint32_t fill) const {
         if (words && j + V <= n) {
-            if constexpr (VEC) {
-                const uint4 v = *reinterpret_cast<const uint4*>(row + j);
-                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[W - 1] = v.w;
-            } else {
-                w[0] = *reinterpret_cast<const uint32_t*>(row + j);
-            }
+            get_inside(row, j, w);
         } else {
 #pragma unroll
             for (int i = 0; i < W; ++i) {
@@ -217,22 +220,25 @@ struct Row {
             }
         }
     }
+    __device__ __forceinline__ void put_inside(L* row, int j, const float* d) const {
+        uint32_t w[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (sizeof(L) == 4) {
+                w[i] = __float_as_uint(d[i]);
+            } else {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(d[2 * i], d[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+        }
+        if constexpr (VEC)
+            *reinterpret_cast<uint4*>(row + j) = make_uint4(w[0], w[1], w[2], w[W - 1]);
+        else
+            *reinterpret_cast<uint32_t*>(row + j) = w[0];
+    }
     __device__ __forceinline__ void put(L* row, int j, const float* d) const {
         if (words && j + V <= n) {
-            uint32_t w[W];
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                if constexpr (sizeof(L) == 4) {
-                    w[i] = __float_as_uint(d[i]);
-                } else {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(d[2 * i], d[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-                }
-            }
-            if constexpr (VEC)
-                *reinterpret_cast<uint4*>(row + j) = make_uint4(w[0], w[1], w[2], w[W - 1]);
-            else
-                *reinterpret_cast<uint32_t*>(row + j) = w[0];
+            put_inside(row, j, d);
         } else {
 #pragma unroll
             for (int c = 0; c < V; ++c)
@@ -240,20 +246,27 @@ struct Row {
         }
     }
 
-    // Of V logits: their scores, those of a softmax relative to m, added to z and, times their counts, to d; `kept` is what
+    // Of N logits: their scores, those of a softmax relative to m, added to z and, times their counts, to d; `kept` is what
     // the gradient takes of each: the score, times what a sigmoid leaves to one.
+    template <int N>
     static __device__ __forceinline__ void soft_scores(const float* y, float m, const float* c, float* kept, float& z, float& d) {
-        const bool plain = fabsf(m) <= 3.402823466e38f;  // neither +inf nor masked throughout
+        if (fabsf(m) <= 3.402823466e38f) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            kept[v] = plain ? exp_score<L>(fmaxf(y[v], minus_inf()) - m) : exp_below(y[v], m);  // NaN is masked
+            for (int v = 0; v < N; ++v) kept[v] = exp_score<L>(fmaxf(y[v], minus_inf()) - m);  // NaN is masked
+        } else {  // +inf, or masked throughout
+#pragma unroll
+            for (int v = 0; v < N; ++v) kept[v] = exp_below(y[v], m);
+        }
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
             z += kept[v];
             d = fmaf(kept[v], c[v], d);
         }
     }
+    template <int N>
     static __device__ __forceinline__ void sigmoid_scores(const float* y, const float* c, float* kept, float& z, float& d) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
+        for (int v = 0; v < N; ++v) {
             const float logit = fmaxf(y[v], minus_inf()), t = exp_score<L>(-fabsf(logit));  // t = 0 and s = 0 where masked
             float r;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));  // 1 ulp
@@ -263,10 +276,11 @@ struct Row {
             d = fmaf(s, c[v], d);
         }
     }
-    // The gradient of V logits, from what was kept of them.
+    // The gradient of N logits, from what was kept of them.
+    template <int N>
     static __device__ __forceinline__ void gradient(float* kept, const float* c, float gz, float gm, const float* add) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) kept[v] = fmaf(kept[v], fmaf(gz, c[v], gm), add[v]);
+        for (int v = 0; v < N; ++v) kept[v] = fmaf(kept[v], fmaf(gz, c[v], gm), add[v]);
     }
 };
 
@@ -396,7 +410,7 @@ __global__ void __launch_bounds__(128, 5) balance_lanes_kernel(const BalanceArgs
 #pragma unroll
             for (int i2 = 0; i2 < ACCESSES; ++i2) {
                 R::unpack(raw + i2 * R::W, y);
-                R::soft_scores(y, top, counts + i2 * V, e, zs, ds);
+                R::template soft_scores<V>(y, top, counts + i2 * V, e, zs, ds);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     if (mine) kept[i2 * V + v] = e[v];
@@ -412,7 +426,7 @@ __global__ void __launch_bounds__(128, 5) balance_lanes_kernel(const BalanceArgs
             for (int i2 = 0; i2 < ACCESSES; ++i2) {
                 float y[V];
                 R::unpack(raw + i2 * R::W, y);
-                R::sigmoid_scores(y, counts + i2 * V, kept + i2 * V, z, d);
+                R::template sigmoid_scores<V>(y, counts + i2 * V, kept + i2 * V, z, d);
             }
             z = warp_sum<TEAM>(z);
             d = warp_sum<TEAM>(d);
@@ -429,7 +443,7 @@ __global__ void __launch_bounds__(128, 5) balance_lanes_kernel(const BalanceArgs
 #pragma unroll
                 for (int v = 0; v < V; ++v) more[v] = 0.0f;
                 if (a.add != nullptr) R::unpack(adds + i2 * R::W, more);
-                R::gradient(kept + i2 * V, counts + i2 * V, gz, gm, more);
+                R::template gradient<V>(kept + i2 * V, counts + i2 * V, gz, gm, more);
                 r.put(out, r.column(i2), kept + i2 * V);
             }
             out += a.dlogits_stride;
@@ -440,95 +454,124 @@ __global__ void __launch_bounds__(128, 5) balance_lanes_kernel(const BalanceArgs
     run.done(a, team, r.tid == 0);
 }
 
-// Longer rows: a block a row. What the gradient takes of each logit waits in shared memory (STAGED) between the
-// sums and the gradient; rows too long for that are read again.
-template <int TEAM, bool VEC, bool GRAD, bool STAGED, typename L>
+// Longer rows: a block a row, 16 logits a thread at a time. What the loss alone needs is summed in one pass, relative
+// to a maximum that grows. For the gradient the logits of a softmax, or what it takes of a sigmoid's, wait in shared
+// memory (STAGED), and with them the counts of the sequence (COUNTED), each thread's own; rows too long for that are read
+// again.
+template <int TEAM, bool VEC, bool GRAD, bool STAGED, bool COUNTED, typename L>
 __global__ void __launch_bounds__(TEAM, 1024 / TEAM) balance_block_kernel(const BalanceArgs a) {
     using R = Row<TEAM, 0, VEC, L>;
-    constexpr int V = R::V, U = 4;  // accesses on their way together
-    extern __shared__ float4 stage4[];
+    constexpr int V = R::V, N = 16, U = N / V;
+    extern __shared__ float stage[];
     __shared__ float joints[2][3][R::WARPS];
     int half = 0;
     grid_dependency_wait();
     grid_launch_dependents();
-    float* stage = reinterpret_cast<float*>(stage4);
     const R r(a, threadIdx.x);
     const int first = (int)min((int64_t)blockIdx.x * a.rows, (int64_t)a.tokens), last = first + min(a.rows, a.tokens - first);
     const bool whole = reinterpret_cast<uintptr_t>(a.counts) % 16 == 0 && a.n % 4 == 0, softmax = a.score == SDM_SOFTMAX;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, chunks = (a.n + TEAM * N - 1) / (TEAM * N), full = r.words ? a.n / (TEAM * N) : 0;
+    float* kept_counts = stage + (STAGED ? (a.n + TEAM * V - 1) / (TEAM * V) * (TEAM * V) : 0);
     Run run;
     for (int t = first; t < last; ++t) {
-        run.next(a, t, blockIdx.x, threadIdx.x == 0);
+        const bool begins = run.next(a, t, blockIdx.x, threadIdx.x == 0);
         const L* row = static_cast<const L*>(a.logits) + t * a.row_stride;
         const int32_t* from = run.q.s >= 0 ? a.counts + (int64_t)run.q.s * a.n : nullptr;
-        const auto counts = [&](int j, float* c) {
-            if (from != nullptr) {
-                centred<V>(from, a.n, whole, run.f.centre, j, c);
-            } else {
+        // the N values of a chunk of a thread in shared memory, which ends with the row's last access
+        const auto put_shared = [&](float* to, int chunk, const float* x) {
+            to += chunk * N * TEAM + threadIdx.x;
 #pragma unroll
-                for (int v = 0; v < V; ++v) c[v] = 0.0f;
+            for (int u = 0; u < U; ++u) {
+                if (chunk >= full && r.column(chunk * U + u) >= a.n) continue;
+#pragma unroll
+                for (int v = 0; v < V; ++v) to[(u * V + v) * TEAM] = x[u * V + v];
             }
         };
-        // f(access, first column, V logits) over this thread's share
-        const auto each = [&](const auto& f) {
-            for (int i0 = 0; r.column(i0) < r.n; i0 += U) {
-                uint32_t w[U][R::W];
+        const auto get_shared = [&](const float* at, int chunk, float* x, float fill) {
+            at += chunk * N * TEAM + threadIdx.x;
+            if (chunk < full) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) r.get(row, r.column(i0 + u), w[u], R::kNone);
+                for (int i = 0; i < N; ++i) x[i] = at[i * TEAM];
+            } else {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    float y[V];
-                    R::unpack(w[u], y);
-                    if (r.column(i0 + u) < r.n) f(i0 + u, r.column(i0 + u), y);
+                    const bool in = r.column(chunk * U + u) < a.n;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) x[u * V + v] = in ? at[(u * V + v) * TEAM] : fill;
                 }
             }
         };
-        // a thread's V values of an access
-        const auto put_stage = [&](int i, const float* x) {
+        const auto load_counts = [&](int chunk, float* c) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) stage[(i * V + v) * TEAM + threadIdx.x] = x[v];
-        };
-        const auto get_stage = [&](int i, float* x) {
+            for (int u = 0; u < U; ++u) {
+                if (from != nullptr) {
+                    centred<V>(from, a.n, whole, run.f.centre, r.column(chunk * U + u), c + u * V);
+                } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) x[v] = stage[(i * V + v) * TEAM + threadIdx.x];
+                    for (int v = 0; v < V; ++v) c[u * V + v] = 0.0f;
+                }
+            }
         };
-        float m = minus_inf(), mine = 0.0f, z = 0.0f, d = 0.0f;
+        if (COUNTED && begins) {
+            for (int chunk = 0; chunk < chunks; ++chunk) {
+                float c[N];
+                load_counts(chunk, c);
+                put_shared(kept_counts, chunk, c);
+            }
+        }
+        const auto counts = [&](int chunk, float* c) {
+            if constexpr (COUNTED)
+                get_shared(kept_counts, chunk, c, 0.0f);
+            else
+                load_counts(chunk, c);
+        };
+        // the logits of a chunk (NaN as masked), or other values that lie like them
+        const auto get = [&](const L* from_row, int chunk, float* x, uint32_t fill) {
+            uint32_t w[U][R::W];
+            if (chunk < full) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) r.get_inside(from_row, r.column(chunk * U + u), w[u]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) r.get(from_row, r.column(chunk * U + u), w[u], fill);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) R::unpack(w[u], x + u * V);
+        };
+        float m = minus_inf(), z = 0.0f, d = 0.0f;
         bool soft = softmax;
         for (;;) {
             if (soft) {
-                each([&](int i, int, const float* y) {
+#pragma unroll 2
+                for (int chunk = 0; chunk < chunks; ++chunk) {
+                    float x[N], c[N], top = m;
+                    get(row, chunk, x, R::kNone);
+                    counts(chunk, c);
+                    if (STAGED) put_shared(stage, chunk, x);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) m = fmaxf(m, y[v]);  // NaN is left out
-                    if (STAGED) put_stage(i, y);
-                });
-                mine = m;
-                const auto add_up = [&](int i, int j, const float* y) {
-                    float c[V], kept[V];
-                    counts(j, c);
-                    R::soft_scores(y, mine, c, kept, z, d);
-                    if (STAGED && GRAD) put_stage(i, kept);
-                };
-                if constexpr (STAGED) {
-#pragma unroll 4
-                    for (int i = 0; r.column(i) < r.n; ++i) {
-                        float y[V];
-                        get_stage(i, y);
-                        add_up(i, r.column(i), y);
+                    for (int i = 0; i < N; ++i) top = fmaxf(top, x[i]);  // NaN is left out
+                    if (top > m) {
+                        const float scale = exp_below(m, top);
+                        z *= scale;
+                        d *= scale;
+                        m = top;
                     }
-                } else {
-                    each(add_up);
+                    R::template soft_scores<N>(x, m, c, x, z, d);
                 }
+                const float mine = m;
                 m = warp_max(m);
                 const float scale = exp_below(mine, m);
                 z *= scale;
                 d *= scale;
             } else {
-                each([&](int i, int j, const float* y) {
-                    float c[V], kept[V];
-                    counts(j, c);
-                    R::sigmoid_scores(y, c, kept, z, d);
-                    if (STAGED && GRAD) put_stage(i, kept);
-                });
+#pragma unroll 2
+                for (int chunk = 0; chunk < chunks; ++chunk) {
+                    float x[N], c[N];
+                    get(row, chunk, x, R::kNone);
+                    counts(chunk, c);
+                    R::template sigmoid_scores<N>(x, c, x, z, d);
+                    if (STAGED && GRAD) put_shared(stage, chunk, x);
+                }
             }
             z = warp_sum(z);
             d = warp_sum(d);
@@ -555,38 +598,33 @@ __global__ void __launch_bounds__(TEAM, 1024 / TEAM) balance_block_kernel(const 
         if constexpr (GRAD) {
             L* out = static_cast<L*>(a.dlogits) + t * a.dlogits_stride;
             const L* add = a.add != nullptr ? static_cast<const L*>(a.add) + t * a.add_stride : nullptr;
-            const float gz = run.f.g * inverse * (soft ? exp_below(mine, m) : 1.0f), gm = -gz * mean;
-            const auto write = [&](int j, float* kept) {
-                float c[V], adds[V];
-                counts(j, c);
-#pragma unroll
-                for (int v = 0; v < V; ++v) adds[v] = 0.0f;
+            const float gz = run.f.g * inverse, gm = -gz * mean;
+            for (int chunk = 0; chunk < chunks; ++chunk) {
+                float x[N], c[N], adds[N];
+                counts(chunk, c);
+                float unused = 0.0f;
+                if constexpr (STAGED)
+                    get_shared(stage, chunk, x, minus_inf());
+                else
+                    get(row, chunk, x, R::kNone);
+                if (soft)
+                    R::template soft_scores<N>(x, m, c, x, unused, unused);
+                else if (!STAGED)
+                    R::template sigmoid_scores<N>(x, c, x, unused, unused);
                 if (add != nullptr) {
-                    uint32_t w[R::W];
-                    r.get(add, j, w, 0u);
-                    R::unpack(w, adds);
-                }
-                R::gradient(kept, c, gz, gm, adds);
-                r.put(out, j, kept);
-            };
-            if constexpr (STAGED) {
-#pragma unroll 4
-                for (int i = 0; r.column(i) < r.n; ++i) {
-                    float kept[V];
-                    get_stage(i, kept);
-                    write(r.column(i), kept);
-                }
-            } else {
-                each([&](int, int j, const float* y) {
-                    float none[V], kept[V], unused = 0.0f;
+                    get(add, chunk, adds, 0u);
+                } else {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) none[v] = 0.0f;
-                    if (soft)
-                        R::soft_scores(y, mine, none, kept, unused, unused);
-                    else
-                        R::sigmoid_scores(y, none, kept, unused, unused);
-                    write(j, kept);
-                });
+                    for (int i = 0; i < N; ++i) adds[i] = 0.0f;
+                }
+                R::template gradient<N>(x, c, gz, gm, adds);
+                if (chunk < full) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) r.put_inside(out, r.column(chunk * U + u), x + u * V);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) r.put(out, r.column(chunk * U + u), x + u * V);
+                }
             }
         }
     }
@@ -625,15 +663,21 @@ struct Team {
     size_t smem;
 };
 
-// Sixteen logits a lane up to 512 entries, in fewer lanes for shorter rows; then blocks of 128 to 512 threads, which
-// stage rows of up to 48 K entries.
-constexpr int kStaged = 48 * 1024;
+// Sixteen logits a lane up to 512 entries, in fewer lanes for shorter rows; then blocks of 128 to 512 threads. For the
+// gradient they stage the counts up to 8192 entries, and rows up to 48 K.
+constexpr int kStaged = 48 * 1024, kCounted = 8192;
 template <int TEAM, bool VEC, bool GRAD, typename L>
 Team block_team(int n) {
     constexpr int V = (VEC ? 16 : 4) / sizeof(L);
     const size_t smem = (size_t)(n + TEAM * V - 1) / (TEAM * V) * (TEAM * V) * sizeof(float);
-    if (n <= kStaged) return {(const void*)balance_block_kernel<TEAM, VEC, GRAD, true, L>, TEAM, 1, smem};
-    return {(const void*)balance_block_kernel<TEAM, VEC, GRAD, false, L>, TEAM, 1, 0};
+    if constexpr (!GRAD) {
+        return {(const void*)balance_block_kernel<TEAM, VEC, false, false, false, L>, TEAM, 1, 0};
+    } else if constexpr (TEAM < 512) {  // rows of at most kCounted entries
+        return {(const void*)balance_block_kernel<TEAM, VEC, true, true, true, L>, TEAM, 1, 2 * smem};
+    } else {
+        if (n <= kStaged) return {(const void*)balance_block_kernel<TEAM, VEC, true, true, false, L>, TEAM, 1, smem};
+        return {(const void*)balance_block_kernel<TEAM, VEC, true, false, false, L>, TEAM, 1, 0};
+    }
 }
 template <bool VEC, bool GRAD, typename L>
 Team rows_team(int n) {
@@ -642,8 +686,8 @@ Team rows_team(int n) {
     if (n <= 128) return {(const void*)balance_lanes_kernel<8, 16, VEC, GRAD, L>, 128, 16, 0};
     if (n <= 256) return {(const void*)balance_lanes_kernel<16, 16, VEC, GRAD, L>, 128, 8, 0};
     if (n <= 512) return {(const void*)balance_lanes_kernel<32, 16, VEC, GRAD, L>, 128, 4, 0};
-    if (n <= 6144) return block_team<128, VEC, GRAD, L>(n);
-    return n <= 12288 ? block_team<256, VEC, GRAD, L>(n) : block_team<512, VEC, GRAD, L>(n);
+    if (n <= 2048) return block_team<128, VEC, GRAD, L>(n);
+    return n <= kCounted ? block_team<256, VEC, GRAD, L>(n) : block_team<512, VEC, GRAD, L>(n);
 }
 template <typename L>
 Team rows_team(int n, bool vec, bool grad) {
@@ -685,7 +729,7 @@ int launch_balance(const BalanceArgs& a0, cudaStream_t stream) {
     a.rows = 1;
     if (a.tokens > 0) {
         // runs that fill the GPU once
-        int rc = allow_smem(team.fn, team.smem);
+        int rc = allow_smem(team.fn, team.smem + 1024);  // and what the kernel has besides
         if (rc != 0) return rc;
         const int most = std::min(kBalanceTeams, sms * std::max(1, blocks_per_sm(team.fn, team.threads, team.smem)) * team.teams);
         a.rows = (a.tokens - 1) / most + 1;

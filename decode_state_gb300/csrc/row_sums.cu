@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
 // ---------------------------------------------------------------- the sort
 
 // Places by counting. Slot and number of an entry make one number (of type C: 32 bits where both fit), so that an entry
-// comes after all smaller ones. A block takes 64 entries, a warp four of them, and compares with all.
+// comes after all smaller ones. A block takes 32 entries, a warp two of them, and compares with all.
 constexpr int kRankThreads = 512, kRankBits = 13;  // bits of an entry's number
 template <typename C>
 __global__ void __launch_bounds__(kRankThreads) rank_kernel(const RowSumArgs a, uint2* sorted) {
@@ -260,19 +260,20 @@ __global__ void __launch_bounds__(kRankThreads) rank_kernel(const RowSumArgs a, 
         a.counters[0] = live;
         a.counters[1] = 0;
     }
-    const int e0 = (blockIdx.x * (kRankThreads / 32) + warp) * 4;
-    C mine[4];
-    int before[4] = {0, 0, 0, 0};
+    constexpr int Q = 2;
+    const int e0 = (blockIdx.x * (kRankThreads / 32) + warp) * Q;
+    C mine[Q];
+    int before[Q] = {0, 0};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) mine[q] = e0 + q < n ? all[e0 + q] : (C)0;
+    for (int q = 0; q < Q; ++q) mine[q] = e0 + q < n ? all[e0 + q] : (C)0;
 #pragma unroll 8
     for (int i = lane; i < n; i += 32) {
         const C c = all[i];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) before[q] += c < mine[q];
+        for (int q = 0; q < Q; ++q) before[q] += c < mine[q];
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < Q; ++q) {
         before[q] = __reduce_add_sync(kAll, before[q]);
         if (lane == q && e0 + q < n && mine[q] != ~(C)0) sorted[before[q]] = make_uint2((uint32_t)(mine[q] >> kRankBits), e0 + q);
     }
@@ -551,7 +552,7 @@ constexpr uint32_t kShort = 32;  // entries of a run beyond the end of a piece t
 // ACC: sums are added to what is there, which is loaded beside the entries that end a run, so that it is at hand
 // when they do.
 template <typename D, typename O, int V, bool ACC>
-__global__ void __launch_bounds__(kThreads, V <= 4 ? (ACC ? 3 : 4) : (ACC ? 2 : 3)) sums_kernel(const RowSumArgs a, int zero_span) {
+__global__ void __launch_bounds__(kThreads, V <= 4 ? (ACC ? 2 : 4) : (ACC ? 1 : 3)) sums_kernel(const RowSumArgs a, int zero_span) {
     __shared__ union {
         uint4 zeros[kZeroBytes / 16];
         Entry<D> batch[kWarps][32];
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? (ACC ? 3 : 4) : (ACC ? 2 : 
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (u < count && on) x[u] = load_pack<D, V>(mine[j0 + u].row + col);
-                if (ACC && (first >> u & 1) && on) {
+                if (ACC && u < count && on) {
                     const uint32_t row = j0 + u > 0 ? mine[j0 + u - 1].key : current;
                     there[u] = load_pack<O, V>(place_in<O>(a, row, col));
                 }
@@ -891,7 +892,7 @@ int launch_row_sums(const RowSumArgs& a0, cudaStream_t stream) {
         const size_t smem = a.entries * (narrow ? 4 : 8);
         rc = allow_smem(rank, smem + 1024);  // and what the kernel has besides
         if (rc != 0) return rc;
-        rc = launch_pdl_raw(rank, dim3((a.entries + 63) / 64), dim3(kRankThreads), smem, stream, args);
+        rc = launch_pdl_raw(rank, dim3((a.entries + 31) / 32), dim3(kRankThreads), smem, stream, args);
         a.sorted = sorted;
     } else {
         rc = launch_sort(a, l, words, &a.sorted, stream);
