@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(OUT_DIR, "libsdm.so")
 BINDING_PATH = os.path.join(OUT_DIR, "sdm_torch.so")
 BINDING = "torch_binding.cpp"
 SOURCES = ["sdm_abi.cu", "sdm_abi_quant.cu", "sdm_abi_train.cu", "decode.cu", "gather.cu", "quant.cu", "qgather.cu", "qgather_ring.cu",
-           "qdecode.cu", "route.cu", "balance.cu", "lookup.cu", "row_sums.cu"]
+           "qdecode.cu", "route.cu", "balance.cu", "balance_bf16.cu", "balance_f32.cu", "lookup.cu", "row_sums.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -7,12 +7,13 @@
 // each warp and column slice, however unevenly the slots share them: a run of equal slots that crosses the ends of
 // pieces leaves one float32 sum for each of them, which a last launch adds up in order.
 //   up to 512 entries    one launch: the warp of a slot's first entry finds the others by scanning all of them
-//   up to 8192           ranks by counting: an entry's place is the number of entries that come before it
-//   more                 a stable radix sort with digits of at most 11 bits: counts, their running sums, places
+//   up to 65536          a stable radix sort in the shared memory of a cluster of blocks
+//   more                 the same in launches, with digits of at most 11 bits: counts, their running sums, places
 // Rows without entries are set to zero by blocks of the same launch as the sums, which search the sorted slots.
 #include <algorithm>
 #include <climits>
 
+#include "cluster_device.cuh"
 #include "score_device.cuh"
 #include "sdm_internal.h"
 
@@ -23,7 +24,7 @@ __device__ unsigned int g_row_sums_status;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr uint32_t kDirect = 512;    // entries that one launch sums
-constexpr uint32_t kRanked = 8192;   // entries ranked by counting
+constexpr int kItems = 16, kTile = kThreads * kItems;  // entries of a tile of the sort
 constexpr int kMostBits = 11;
 constexpr int kZeroRows = 256;       // rows that a block sets to zero, at most
 
@@ -182,14 +183,12 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
     if (e >= n) return;
     const uint32_t key = keys[e];
     if (key >= a.n_slots) return;
-    bool earlier = false;
-    for (int i = lane; i < e; i += 32) earlier |= keys[i] == key;
-    if (__any_sync(kAll, earlier)) return;
     int found = 0;  // the entries of the slot, in order
-    for (int base = e & ~31; base < n; base += 32) {
+    for (int base = 0; base < n; base += 32) {
         const int i = base + lane;
-        const bool same = i >= e && i < n && keys[i] == key;
+        const bool same = i < n && keys[i] == key;
         const unsigned mask = __ballot_sync(kAll, same);
+        if (found == 0 && mask != 0 && base + __ffs(mask) - 1 < e) return;  // another warp's
         if (same) list[warp][found + __popc(mask & ((1u << lane) - 1))] = (uint16_t)i;
         found += __popc(mask);
     }
@@ -226,59 +225,6 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
 
 // ---------------------------------------------------------------- the sort
 
-// Places by counting. Slot and number of an entry make one number (of type C: 32 bits where both fit), so that an entry
-// comes after all smaller ones. A block takes 32 entries, a warp two of them, and compares with all.
-constexpr int kRankThreads = 512, kRankBits = 13;  // bits of an entry's number
-template <typename C>
-__global__ void __launch_bounds__(kRankThreads) rank_kernel(const RowSumArgs a, uint2* sorted) {
-    extern __shared__ uint64_t rank_smem[];
-    __shared__ int alive[kRankThreads / 32];
-    C* all = reinterpret_cast<C*>(rank_smem);
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int n = (int)a.entries, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int live = 0;
-    for (int e0 = threadIdx.x; e0 < n; e0 += 8 * kRankThreads) {
-        uint32_t key[8];
-        keys_of<8>(a, e0, kRankThreads, key);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i * kRankThreads;
-            const bool in = key[i] < a.n_slots;
-            if (e < n) all[e] = in ? (C)key[i] << kRankBits | (C)e : ~(C)0;  // those that take no part come last
-            live += in;
-        }
-    }
-    if (blockIdx.x == 0) {
-        live = __reduce_add_sync(kAll, live);
-        if (lane == 0) alive[warp] = live;
-    }
-    __syncthreads();
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        live = 0;
-        for (int w = 0; w < kRankThreads / 32; ++w) live += alive[w];
-        a.counters[0] = live;
-        a.counters[1] = 0;
-    }
-    constexpr int Q = 2;
-    const int e0 = (blockIdx.x * (kRankThreads / 32) + warp) * Q;
-    C mine[Q];
-    int before[Q] = {0, 0};
-#pragma unroll
-    for (int q = 0; q < Q; ++q) mine[q] = e0 + q < n ? all[e0 + q] : (C)0;
-#pragma unroll 8
-    for (int i = lane; i < n; i += 32) {
-        const C c = all[i];
-#pragma unroll
-        for (int q = 0; q < Q; ++q) before[q] += c < mine[q];
-    }
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        before[q] = __reduce_add_sync(kAll, before[q]);
-        if (lane == q && e0 + q < n && mine[q] != ~(C)0) sorted[before[q]] = make_uint2((uint32_t)(mine[q] >> kRankBits), e0 + q);
-    }
-}
-
 // The digits of a pass.
 struct Digit {
     int shift, bits;
@@ -287,18 +233,18 @@ struct Digit {
 
 // The counts of a tile's digits, counts[tile][digit]. FIRST: the keys are made here and kept, and entries
 // that take no part are not counted; later passes have the others only.
-template <bool FIRST, int ITEMS>
+template <bool FIRST>
 __global__ void __launch_bounds__(kThreads) digit_count_kernel(const RowSumArgs a, uint32_t* keys, const uint2* in, uint32_t* counts, Digit digit) {
     __shared__ uint32_t bins[1 << kMostBits];
     grid_dependency_wait();
     grid_launch_dependents();
-    const uint32_t entries = FIRST ? a.entries : a.counters[0], from = blockIdx.x * (uint32_t)(kThreads * ITEMS);
+    const uint32_t entries = FIRST ? a.entries : a.counters[0], from = blockIdx.x * (uint32_t)kTile;
     if (FIRST && blockIdx.x == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
     const int all = 1 << digit.bits;
     for (int b = threadIdx.x; b < all; b += kThreads) bins[b] = 0;
     __syncthreads();
-    constexpr int BATCH = ITEMS < 8 ? ITEMS : 8;
-    for (int i0 = 0; i0 < ITEMS; i0 += BATCH) {
+    constexpr int BATCH = 8;
+    for (int i0 = 0; i0 < kItems; i0 += BATCH) {
         const uint32_t first = from + i0 * kThreads + threadIdx.x;
         uint32_t key[BATCH];
         if constexpr (FIRST) {
@@ -322,6 +268,7 @@ __global__ void __launch_bounds__(kThreads) digit_count_kernel(const RowSumArgs 
 }
 
 // The sum of `own` over the block's threads before this one, and over all of them.
+template <int WARPS>
 __device__ __forceinline__ uint32_t sum_before(uint32_t own, uint32_t* sums, uint32_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t sum = own;
@@ -334,7 +281,7 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t own, uint32_t* sums, uin
     __syncthreads();
     uint32_t before = 0, every = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += sums[w];
         every += sums[w];
     }
@@ -398,13 +345,115 @@ __global__ void __launch_bounds__(kScanThreads) digit_scan_kernel(uint32_t* coun
     }
 }
 
+// ---------------------------------------------------------------- up to 65536 entries: one cluster
+
+// The blocks of a cluster hold the entries in shared memory and each other's within reach, so that a pass of the sort
+// costs two barriers of the cluster where launches cost three times that: 65536 entries in CLUSTER us, by launches LAUNCHES.
+constexpr int kCluster = 16, kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32, kClusterBits = 10;
+constexpr uint32_t kClustered = kCluster * kClusterThreads * 4;
+
+// Block r holds places r * size .. of the entries, `size` a power of two, ITEMS entries a thread.
+template <int ITEMS>
+__global__ void __launch_bounds__(kClusterThreads, 1) cluster_sort_kernel(const RowSumArgs a, uint2* sorted, int passes, int bits) {
+    constexpr uint32_t size = kClusterThreads * ITEMS;
+    extern __shared__ uint2 cluster_smem[];
+    __shared__ uint32_t sums[kClusterWarps];
+    const int all = 1 << bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint2* buffers = cluster_smem;  // two of `size` pairs, the second for a third pass on
+    uint32_t* hist = reinterpret_cast<uint32_t*>(buffers + (passes > 2 ? 2 : 1) * size);  // this block's count of each digit
+    uint32_t* offset = hist + all;                                                        // where it puts the first of them
+    uint16_t* own = reinterpret_cast<uint16_t*>(offset + all) + warp * all;               // a warp's counts, then their sums
+    const uint16_t* owns = reinterpret_cast<uint16_t*>(offset + all);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const uint32_t rank = cluster_rank(), first = rank * size;
+    uint32_t entries = a.entries;  // those left
+    for (int p = 0; p < passes; ++p) {
+        const Digit digit{p * bits, bits};
+        const uint2* in = buffers + ((p - 1) & 1) * size;
+        for (int b = lane; b < all; b += 32) own[b] = 0;
+        __syncwarp();
+        // a warp's entries are consecutive, 32 at a time
+        const uint32_t local = warp * (32 * ITEMS) + lane;
+        uint32_t key[ITEMS], place[ITEMS];
+        if (p == 0) {
+            keys_of<ITEMS>(a, first + local, 32, key);
+        } else {
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) key[i] = first + local + i * 32 < entries ? in[local + i * 32].x : (uint32_t)a.n_slots;
+        }
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) place[i] = __ballot_sync(kAll, key[i] < a.n_slots);
+        for (int b = digit.shift; b < digit.shift + digit.bits; ++b) {
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                const uint32_t bit = key[i] >> b & 1;
+                place[i] &= ~(__ballot_sync(kAll, bit) ^ (0u - bit));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const unsigned same = place[i];
+            const uint32_t d = digit.of(key[i]), before = own[d];
+            __syncwarp();
+            if (key[i] < a.n_slots && lane == 31 - __clz(same)) own[d] = (uint16_t)(before + __popc(same));
+            __syncwarp();
+            place[i] = before + __popc(same & ((1u << lane) - 1));
+        }
+        __syncthreads();
+        // a thread for each digit: its sums over the warps, and then over the blocks
+        if (tid < all) {
+            uint32_t run = 0;
+#pragma unroll 8
+            for (int w = 0; w < kClusterWarps; ++w) {
+                uint16_t* at = const_cast<uint16_t*>(owns) + w * all + tid;
+                const uint32_t c = *at;
+                *at = (uint16_t)run;
+                run += c;
+            }
+            hist[tid] = run;
+        }
+        cluster_sync();
+        uint32_t total = 0, earlier = 0, live;
+        if (tid < all) {
+#pragma unroll
+            for (uint32_t q = 0; q < kCluster; ++q) {
+                const uint32_t c = cluster_load(cluster_address(hist + tid, q));
+                total += c;
+                if (q < rank) earlier += c;
+            }
+        }
+        const uint32_t start = sum_before<kClusterWarps>(total, sums, &live);
+        if (tid < all) offset[tid] = start + earlier;
+        if (p == 0 && rank == 0 && tid == 0) {
+            a.counters[0] = live;
+            a.counters[1] = 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            if (key[i] < a.n_slots) {
+                const uint32_t d = digit.of(key[i]), to = offset[d] + own[d] + place[i];
+                const uint2 pair = make_uint2(key[i], p == 0 ? first + local + i * 32 : in[local + i * 32].y);
+                if (p + 1 == passes)
+                    sorted[to] = pair;
+                else
+                    cluster_store(cluster_address(buffers + (p & 1) * size + to % size, to / size), pair);
+            }
+        }
+        entries = live;
+        cluster_sync();  // what others wrote here is here, and nobody reads here any more
+    }
+}
+
+// ---------------------------------------------------------------- more: a launch for each step
+
 // A tile's entries go to their places: behind all smaller digits, behind the same digit of earlier tiles, in order. They
-// are put in order in shared memory first, so that what goes to one place is written side by side. SCANNED: counts are
-// running sums over the tiles, totals their ends; else a block adds up the counts of the few tiles itself.
-template <bool FIRST, bool SCANNED, int ITEMS>
+// are put in order in shared memory first, so that what goes to one place is written side by side.
+template <bool FIRST>
 __global__ void __launch_bounds__(kThreads, 3) digit_place_kernel(const RowSumArgs a, const uint32_t* keys, const uint2* in, uint2* out,
-                                                               const uint32_t* counts, const uint32_t* totals, Digit digit) {
-    constexpr int TILE = kThreads * ITEMS;
+                                                                  const uint32_t* counts, const uint32_t* totals, Digit digit) {
+    constexpr int TILE = kTile, ITEMS = kItems;
     // a warp's counts of each digit; then the tile's entries
     __shared__ union {
         uint16_t own[kWarps][1 << kMostBits];
@@ -415,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 3) digit_place_kernel(const RowSumAr
     grid_dependency_wait();
     grid_launch_dependents();
     const int all = 1 << digit.bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t entries = FIRST ? a.entries : a.counters[0], tile = blockIdx.x, tiles = gridDim.x;
+    const uint32_t entries = FIRST ? a.entries : a.counters[0], tile = blockIdx.x;
     if (tile * (uint32_t)TILE >= entries && !(FIRST && tile == 0)) return;
     for (int b = lane * 2; b < all; b += 64) *reinterpret_cast<uint32_t*>(&m.own[warp][b]) = 0;
     __syncwarp();
@@ -458,27 +507,18 @@ __global__ void __launch_bounds__(kThreads, 3) digit_place_kernel(const RowSumAr
         total[i] = earlier[i] = 0;
         const int b = b0 + i;
         if (i < per && b < all) {
-            if constexpr (SCANNED) {
-                total[i] = __ldg(totals + b);
-                earlier[i] = __ldg(counts + ((int64_t)tile << digit.bits) + b);
-            } else {
-#pragma unroll 8
-                for (uint32_t t = 0; t < tiles; ++t) {
-                    const uint32_t c = __ldg(counts + ((int64_t)t << digit.bits) + b);
-                    total[i] += c;
-                    if (t < tile) earlier[i] += c;
-                }
-            }
+            total[i] = __ldg(totals + b);
+            earlier[i] = __ldg(counts + ((int64_t)tile << digit.bits) + b);
             of_all += total[i];
             uint32_t run = 0;
             for (int w = 0; w < kWarps; ++w) run += m.own[w][b];
             of_tile += run;
         }
     }
-    uint32_t start = sum_before(of_all, sums, &unused), live;
+    uint32_t start = sum_before<kWarps>(of_all, sums, &unused), live;
     if (FIRST && tile == 0 && threadIdx.x == 0) a.counters[0] = unused;
     __syncthreads();
-    uint32_t local = sum_before(of_tile, sums, &live);
+    uint32_t local = sum_before<kWarps>(of_tile, sums, &live);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int b = b0 + i;
@@ -766,23 +806,15 @@ Divisor divisor(int d) {
     return {(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), l - 1};
 }
 
-// The passes of the sort over slots below n_slots. Tiles of 1024 entries, of which few entries make more blocks, else
-// of 4096, whose digits come in longer runs; up to 32 tiles are added up by each block that needs their sums.
+// The passes of the sort over slots below n_slots, with digits of `most` bits at most.
 struct Radix {
-    int passes, bits, items;
-    int64_t tiles;
-    bool scanned;
+    int passes, bits;
 };
-Radix radix_of(int64_t entries, int64_t n_slots) {
+Radix radix_of(int64_t n_slots, int most) {
     int significant = 1;
     while ((n_slots - 1) >> significant != 0) ++significant;
-    Radix r{};
-    r.passes = (significant + kMostBits - 1) / kMostBits;
-    r.bits = (significant + r.passes - 1) / r.passes;
-    r.items = entries <= 131072 ? 4 : 16;
-    r.tiles = (entries + kThreads * r.items - 1) / (kThreads * r.items);
-    r.scanned = r.tiles > 32;
-    return r;
+    const int passes = (significant + most - 1) / most;
+    return {passes, (significant + passes - 1) / passes};
 }
 
 // Where everything lies in the workspace, in words.
@@ -790,29 +822,44 @@ struct Layout {
     int64_t counters, pairs, keys, counts, totals, heads, tails, list, words;
 };
 Layout layout_of(int64_t entries, int64_t n_slots, int hd) {
-    const Radix radix = radix_of(entries, n_slots);
-    const bool sorted = entries > kRanked;
+    const bool launches = entries > kClustered;
     const int64_t e = round_up(entries, 64), piece = piece_of(entries, hd), pieces = (entries + piece - 1) / piece;
+    const int64_t tiles = (entries + kTile - 1) / kTile;
     Layout l{};
     l.pairs = l.counters + 64;
-    l.keys = l.pairs + (sorted ? 4 : 2) * e;
-    l.counts = l.keys + (sorted ? e : 0);
-    l.totals = l.counts + (sorted ? round_up((int64_t)radix.tiles << radix.bits, 64) : 0);
-    l.heads = l.totals + (sorted ? 1 << kMostBits : 0);
+    l.keys = l.pairs + (launches ? 4 : 2) * e;
+    l.counts = l.keys + (launches ? e : 0);
+    l.totals = l.counts + (launches ? round_up(tiles << radix_of(n_slots, kMostBits).bits, 64) : 0);
+    l.heads = l.totals + (launches ? 1 << kMostBits : 0);
     l.tails = l.heads + round_up(pieces * hd, 64);
     l.list = l.tails + round_up(pieces * hd, 64);
     l.words = l.list + round_up(pieces, 64);
     return l;
 }
 
-template <bool FIRST, bool SCANNED>
-const void* place_kernel(int items) {
-    return items == 4 ? (const void*)digit_place_kernel<FIRST, SCANNED, 4> : (const void*)digit_place_kernel<FIRST, SCANNED, 16>;
+// The sort by a cluster.
+int launch_cluster_sort(const RowSumArgs& a, uint2* sorted, cudaStream_t stream) {
+    const Radix r = radix_of(a.n_slots, kClusterBits);
+    const uint32_t each = (a.entries + kCluster * kClusterThreads - 1) / (kCluster * kClusterThreads);  // entries of a thread
+    const int items = each <= 1 ? 1 : each <= 2 ? 2 : 4;
+    const void* fn = items == 1   ? (const void*)cluster_sort_kernel<1>
+                     : items == 2 ? (const void*)cluster_sort_kernel<2>
+                                  : (const void*)cluster_sort_kernel<4>;
+    const size_t smem = (size_t)(r.passes > 2 ? 2 : 1) * kClusterThreads * items * sizeof(uint2) + ((size_t)8 << r.bits) +
+                        ((size_t)kClusterWarps * 2 << r.bits);
+    int rc = allow_smem(fn, smem + 1024);  // and what the kernel has besides
+    if (rc == 0) rc = (int)cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (rc != 0) return rc;
+    RowSumArgs args_a = a;
+    int passes = r.passes, bits = r.bits;
+    void* args[] = {&args_a, &sorted, &passes, &bits};
+    return launch_cluster_raw(fn, kCluster, dim3(kCluster), dim3(kClusterThreads), smem, stream, args);
 }
 
 // Sorts the entries; `sorted` becomes where they are.
 int launch_sort(const RowSumArgs& a, const Layout& l, uint32_t* words, const uint2** sorted, cudaStream_t stream) {
-    Radix r = radix_of(a.entries, a.n_slots);
+    Radix r = radix_of(a.n_slots, kMostBits);
+    int tiles = (int)((a.entries + (int64_t)kTile - 1) / kTile);
     uint32_t *keys = words + l.keys, *counts = words + l.counts, *totals = words + l.totals;
     uint2* pairs[2] = {reinterpret_cast<uint2*>(words + l.pairs), reinterpret_cast<uint2*>(words + l.pairs) + round_up(a.entries, 64)};
     RowSumArgs args = a;
@@ -820,19 +867,16 @@ int launch_sort(const RowSumArgs& a, const Layout& l, uint32_t* words, const uin
         Digit digit{p * r.bits, r.bits};
         uint2 *in = pairs[~p & 1], *out = pairs[p & 1];
         void* count_args[] = {&args, &keys, &in, &counts, &digit};
-        const void* count = p == 0 ? (r.items == 4 ? (const void*)digit_count_kernel<true, 4> : (const void*)digit_count_kernel<true, 16>)
-                                   : (r.items == 4 ? (const void*)digit_count_kernel<false, 4> : (const void*)digit_count_kernel<false, 16>);
-        int rc = launch_pdl_raw(count, dim3(r.tiles), dim3(kThreads), 0, stream, count_args);
-        if (rc == 0 && r.scanned) {
-            int tiles = (int)r.tiles;
-            void* scan_args[] = {&counts, &totals, &tiles, &r.bits};
-            rc = launch_pdl_raw((const void*)digit_scan_kernel, dim3(((1u << r.bits) + kScanDigits - 1) / kScanDigits), dim3(kScanThreads), 0, stream, scan_args);
-        }
+        int rc = launch_pdl_raw(p == 0 ? (const void*)digit_count_kernel<true> : (const void*)digit_count_kernel<false>, dim3(tiles),
+                                dim3(kThreads), 0, stream, count_args);
+        if (rc != 0) return rc;
+        void* scan_args[] = {&counts, &totals, &tiles, &r.bits};
+        rc = launch_pdl_raw((const void*)digit_scan_kernel, dim3(((1u << r.bits) + kScanDigits - 1) / kScanDigits), dim3(kScanThreads), 0,
+                            stream, scan_args);
         if (rc != 0) return rc;
         void* place_args[] = {&args, &keys, &in, &out, &counts, &totals, &digit};
-        const void* place = p == 0 ? (r.scanned ? place_kernel<true, true>(r.items) : place_kernel<true, false>(r.items))
-                                   : (r.scanned ? place_kernel<false, true>(r.items) : place_kernel<false, false>(r.items));
-        rc = launch_pdl_raw(place, dim3(r.tiles), dim3(kThreads), 0, stream, place_args);
+        rc = launch_pdl_raw(p == 0 ? (const void*)digit_place_kernel<true> : (const void*)digit_place_kernel<false>, dim3(tiles),
+                            dim3(kThreads), 0, stream, place_args);
         if (rc != 0) return rc;
         *sorted = out;
     }
@@ -884,15 +928,9 @@ int launch_row_sums(const RowSumArgs& a0, cudaStream_t stream) {
     const int64_t pieces = ((int64_t)a.entries + a.piece - 1) / a.piece, blocks = a.zero_blocks + (pieces * a.slices + kWarps - 1) / kWarps;
     if (blocks > INT_MAX) return SDM_ECOUNT;
     int rc;
-    if (a.entries <= kRanked) {
+    if (a.entries <= kClustered) {
         uint2* sorted = reinterpret_cast<uint2*>(words + l.pairs);
-        void* args[] = {&a, &sorted};
-        const bool narrow = a.n_slots <= (int64_t)1 << (32 - kRankBits);
-        const void* rank = narrow ? (const void*)rank_kernel<uint32_t> : (const void*)rank_kernel<uint64_t>;
-        const size_t smem = a.entries * (narrow ? 4 : 8);
-        rc = allow_smem(rank, smem + 1024);  // and what the kernel has besides
-        if (rc != 0) return rc;
-        rc = launch_pdl_raw(rank, dim3((a.entries + 31) / 32), dim3(kRankThreads), smem, stream, args);
+        rc = launch_cluster_sort(a, sorted, stream);
         a.sorted = sorted;
     } else {
         rc = launch_sort(a, l, words, &a.sorted, stream);

@@ -276,24 +276,30 @@ int allow_smem(const void* kernel, size_t smem);
 int blocks_per_sm(const void* kernel, int threads, size_t smem);
 
 // Launch the kernel at address `kernel` (arguments as an array of pointers to them) with
-// programmatic stream serialization (see grid_dependency_wait). The dynamic shared-memory limit
+// programmatic stream serialization (see grid_dependency_wait), in clusters of `cluster` blocks. The dynamic shared-memory limit
 // must already allow `smem` (allow_smem). Returns the cudaError_t of the launch call itself; the
 // error state of the runtime is consumed only when that call failed, so an earlier error left by
 // other code is neither reported nor cleared here.
-inline int launch_pdl_raw(const void* kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void** args) {
-    cudaLaunchAttribute attr[1];
+inline int launch_cluster_raw(const void* kernel, int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void** args) {
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
     if (e != cudaSuccess) (void)cudaGetLastError();
     return (int)e;
+}
+inline int launch_pdl_raw(const void* kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void** args) {
+    return launch_cluster_raw(kernel, 1, grid, block, smem, stream, args);
 }
 
 }  // namespace sdm
