@@ -7,7 +7,7 @@
 // each warp and column slice, however unevenly the slots share them: a run of equal slots that crosses the ends of
 // pieces leaves one float32 sum for each of them, which a last launch adds up in order.
 //   up to 512 entries    one launch: the warp of a slot's first entry finds the others by scanning all of them
-//   up to 65536          a stable radix sort in the shared memory of a cluster of blocks
+//   up to 32768          a stable radix sort in the shared memory of a cluster of blocks
 //   more                 the same in launches, with digits of at most 11 bits: counts, their running sums, places
 // Rows without entries are set to zero by blocks of the same launch as the sums, which search the sorted slots.
 #include <algorithm>
@@ -24,7 +24,6 @@ __device__ unsigned int g_row_sums_status;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr uint32_t kDirect = 512;    // entries that one launch sums
-constexpr int kItems = 16, kTile = kThreads * kItems;  // entries of a tile of the sort
 constexpr int kMostBits = 11;
 constexpr int kZeroRows = 256;       // rows that a block sets to zero, at most
 
@@ -233,18 +232,18 @@ struct Digit {
 
 // The counts of a tile's digits, counts[tile][digit]. FIRST: the keys are made here and kept, and entries
 // that take no part are not counted; later passes have the others only.
-template <bool FIRST>
+template <bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(kThreads) digit_count_kernel(const RowSumArgs a, uint32_t* keys, const uint2* in, uint32_t* counts, Digit digit) {
     __shared__ uint32_t bins[1 << kMostBits];
     grid_dependency_wait();
     grid_launch_dependents();
-    const uint32_t entries = FIRST ? a.entries : a.counters[0], from = blockIdx.x * (uint32_t)kTile;
+    const uint32_t entries = FIRST ? a.entries : a.counters[0], from = blockIdx.x * (uint32_t)(kThreads * ITEMS);
     if (FIRST && blockIdx.x == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
     const int all = 1 << digit.bits;
     for (int b = threadIdx.x; b < all; b += kThreads) bins[b] = 0;
     __syncthreads();
-    constexpr int BATCH = 8;
-    for (int i0 = 0; i0 < kItems; i0 += BATCH) {
+    constexpr int BATCH = ITEMS < 8 ? ITEMS : 8;
+    for (int i0 = 0; i0 < ITEMS; i0 += BATCH) {
         const uint32_t first = from + i0 * kThreads + threadIdx.x;
         uint32_t key[BATCH];
         if constexpr (FIRST) {
@@ -345,12 +344,13 @@ __global__ void __launch_bounds__(kScanThreads) digit_scan_kernel(uint32_t* coun
     }
 }
 
-// ---------------------------------------------------------------- up to 65536 entries: one cluster
+// ---------------------------------------------------------------- up to 32768 entries: one cluster
 
 // The blocks of a cluster hold the entries in shared memory and each other's within reach, so that a pass of the sort
-// costs two barriers of the cluster where launches cost three times that: 65536 entries in CLUSTER us, by launches LAUNCHES.
+// costs two barriers of the cluster and not three launches. What goes to other blocks goes there in pieces of 8 bytes,
+// though: with four entries a thread launches are faster again (65536 entries: 21 us and launches 18, both alone).
 constexpr int kCluster = 16, kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32, kClusterBits = 10;
-constexpr uint32_t kClustered = kCluster * kClusterThreads * 4;
+constexpr uint32_t kClustered = kCluster * kClusterThreads * 2;
 
 // Block r holds places r * size .. of the entries, `size` a power of two, ITEMS entries a thread.
 template <int ITEMS>
@@ -450,10 +450,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_sort_kernel(const 
 
 // A tile's entries go to their places: behind all smaller digits, behind the same digit of earlier tiles, in order. They
 // are put in order in shared memory first, so that what goes to one place is written side by side.
-template <bool FIRST>
+template <bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(kThreads, 3) digit_place_kernel(const RowSumArgs a, const uint32_t* keys, const uint2* in, uint2* out,
                                                                   const uint32_t* counts, const uint32_t* totals, Digit digit) {
-    constexpr int TILE = kTile, ITEMS = kItems;
+    constexpr int TILE = kThreads * ITEMS;
     // a warp's counts of each digit; then the tile's entries
     __shared__ union {
         uint16_t own[kWarps][1 << kMostBits];
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? (ACC ? 2 : 4) : (ACC ? 1 : 
             for (int u = 0; u < U; ++u) {
                 if (u < count && on) x[u] = load_pack<D, V>(mine[j0 + u].row + col);
                 if (ACC && u < count && on) {
-                    const uint32_t row = j0 + u > 0 ? mine[j0 + u - 1].key : current;
+                    const uint32_t row = u > 0 ? mine[j0 + u - 1].key : current;
                     there[u] = load_pack<O, V>(place_in<O>(a, row, col));
                 }
             }
@@ -817,6 +817,11 @@ Radix radix_of(int64_t n_slots, int most) {
     return {passes, (significant + passes - 1) / passes};
 }
 
+// Entries of a thread of the sort by launches: tiles of 1024 entries, of which few entries make more blocks, else of
+// 4096, whose digits come in longer runs.
+int items_of(int64_t entries) { return entries <= 131072 ? 4 : 16; }
+int64_t tiles_of(int64_t entries) { return (entries + kThreads * items_of(entries) - 1) / (kThreads * items_of(entries)); }
+
 // Where everything lies in the workspace, in words.
 struct Layout {
     int64_t counters, pairs, keys, counts, totals, heads, tails, list, words;
@@ -824,7 +829,7 @@ struct Layout {
 Layout layout_of(int64_t entries, int64_t n_slots, int hd) {
     const bool launches = entries > kClustered;
     const int64_t e = round_up(entries, 64), piece = piece_of(entries, hd), pieces = (entries + piece - 1) / piece;
-    const int64_t tiles = (entries + kTile - 1) / kTile;
+    const int64_t tiles = tiles_of(entries);
     Layout l{};
     l.pairs = l.counters + 64;
     l.keys = l.pairs + (launches ? 4 : 2) * e;
@@ -841,10 +846,8 @@ Layout layout_of(int64_t entries, int64_t n_slots, int hd) {
 int launch_cluster_sort(const RowSumArgs& a, uint2* sorted, cudaStream_t stream) {
     const Radix r = radix_of(a.n_slots, kClusterBits);
     const uint32_t each = (a.entries + kCluster * kClusterThreads - 1) / (kCluster * kClusterThreads);  // entries of a thread
-    const int items = each <= 1 ? 1 : each <= 2 ? 2 : 4;
-    const void* fn = items == 1   ? (const void*)cluster_sort_kernel<1>
-                     : items == 2 ? (const void*)cluster_sort_kernel<2>
-                                  : (const void*)cluster_sort_kernel<4>;
+    const int items = each <= 1 ? 1 : 2;
+    const void* fn = items == 1 ? (const void*)cluster_sort_kernel<1> : (const void*)cluster_sort_kernel<2>;
     const size_t smem = (size_t)(r.passes > 2 ? 2 : 1) * kClusterThreads * items * sizeof(uint2) + ((size_t)8 << r.bits) +
                         ((size_t)kClusterWarps * 2 << r.bits);
     int rc = allow_smem(fn, smem + 1024);  // and what the kernel has besides
@@ -859,7 +862,8 @@ int launch_cluster_sort(const RowSumArgs& a, uint2* sorted, cudaStream_t stream)
 // Sorts the entries; `sorted` becomes where they are.
 int launch_sort(const RowSumArgs& a, const Layout& l, uint32_t* words, const uint2** sorted, cudaStream_t stream) {
     Radix r = radix_of(a.n_slots, kMostBits);
-    int tiles = (int)((a.entries + (int64_t)kTile - 1) / kTile);
+    int tiles = (int)tiles_of(a.entries);
+    const bool few = items_of(a.entries) == 4;
     uint32_t *keys = words + l.keys, *counts = words + l.counts, *totals = words + l.totals;
     uint2* pairs[2] = {reinterpret_cast<uint2*>(words + l.pairs), reinterpret_cast<uint2*>(words + l.pairs) + round_up(a.entries, 64)};
     RowSumArgs args = a;
@@ -867,16 +871,18 @@ int launch_sort(const RowSumArgs& a, const Layout& l, uint32_t* words, const uin
         Digit digit{p * r.bits, r.bits};
         uint2 *in = pairs[~p & 1], *out = pairs[p & 1];
         void* count_args[] = {&args, &keys, &in, &counts, &digit};
-        int rc = launch_pdl_raw(p == 0 ? (const void*)digit_count_kernel<true> : (const void*)digit_count_kernel<false>, dim3(tiles),
-                                dim3(kThreads), 0, stream, count_args);
+        const void* count = p == 0 ? (few ? (const void*)digit_count_kernel<true, 4> : (const void*)digit_count_kernel<true, 16>)
+                                   : (few ? (const void*)digit_count_kernel<false, 4> : (const void*)digit_count_kernel<false, 16>);
+        int rc = launch_pdl_raw(count, dim3(tiles), dim3(kThreads), 0, stream, count_args);
         if (rc != 0) return rc;
         void* scan_args[] = {&counts, &totals, &tiles, &r.bits};
         rc = launch_pdl_raw((const void*)digit_scan_kernel, dim3(((1u << r.bits) + kScanDigits - 1) / kScanDigits), dim3(kScanThreads), 0,
                             stream, scan_args);
         if (rc != 0) return rc;
         void* place_args[] = {&args, &keys, &in, &out, &counts, &totals, &digit};
-        rc = launch_pdl_raw(p == 0 ? (const void*)digit_place_kernel<true> : (const void*)digit_place_kernel<false>, dim3(tiles),
-                            dim3(kThreads), 0, stream, place_args);
+        const void* place = p == 0 ? (few ? (const void*)digit_place_kernel<true, 4> : (const void*)digit_place_kernel<true, 16>)
+                                   : (few ? (const void*)digit_place_kernel<false, 4> : (const void*)digit_place_kernel<false, 16>);
+        rc = launch_pdl_raw(place, dim3(tiles), dim3(kThreads), 0, stream, place_args);
         if (rc != 0) return rc;
         *sorted = out;
     }
