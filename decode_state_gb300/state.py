@@ -7,8 +7,8 @@ swaps in a new bank and advances the count, ``reset`` zeroes the bank and the co
 
 ``RoutedLayerState`` is the same for a quantised bank that streams address by logits over their slots:
 it chooses the slots (``sdm_route``), advances the bank (``sdm_qdecode_step`` / ``sdm_qdecode_seq``),
-reads it without writing (``sdm_qgather``) and takes a reading's gradient back to the logits
-(``sdm_gather_dw``, ``sdm_route_backward``).
+reads it without writing (``sdm_qgather``), takes a reading's gradient back to the logits (``sdm_gather_dw``,
+``sdm_route_backward``) and to the rows (``sdm_gather_drows``), and balances the choices (``sdm_balance``).
 """
 
 from __future__ import annotations
@@ -154,3 +154,24 @@ class RoutedLayerState:
         dw, = quant.gather_dw(self.memory, [(idx, dout)])
         given = {n: self.router[n] for n in ("score", "renorm", "scale") if n in self.router}
         return routing.route_backward(q_logits, idx, dw, base=self._first, w=w, **given)
+
+    def rows_gradient(self, idx: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, *, out=None, accumulate: bool = False) -> torch.Tensor:
+        """Gradient [streams * slots, hd] float32 of the rows that ``read`` summed (of the values that their codes stand for),
+        from that of its readings (float32 [S, hd]); ``idx`` and ``w`` as it returned them. ``out`` and ``accumulate`` as in
+        ``quant.gather_drows``."""
+        return quant.gather_drows([(idx, w, dout)], self.memory.n_slots, out=out, accumulate=accumulate)
+
+    def balance(self, logits: torch.Tensor, idx: torch.Tensor, w=None, *, scale: float = 1.0, gradient: bool = False, dloss=None, add=None):
+        """The balance loss of choices ``idx`` (and ``w``) [.., S, k] that logits [.., S, slots] made, over the places
+        0 .. slots - 1 that the streams' slots share: (loss [1], counts [1, slots]), with ``gradient`` the logits' gradient
+        too, added to ``add`` (e.g. what ``read_backward`` returned). ``scale`` and ``dloss`` as in ``routing.balance``."""
+        if logits.shape[-2:] != (self.streams, self.slots):
+            raise ValueError(f"logits must be [.., {self.streams}, {self.slots}], got {tuple(logits.shape)}")
+        if idx.shape[:-1] != logits.shape[:-1]:
+            raise ValueError(f"idx must be [.., {self.streams}, k] as the logits, got {tuple(idx.shape)}")
+        tokens, k = logits.shape[:-2].numel(), idx.shape[-1]
+        first = self._first if tokens == 1 else self._first.repeat(tokens)
+        loss, counts, *grad = routing.balance(
+            logits.reshape(-1, self.slots), idx.reshape(-1, k), score=self.router.get("score", "softmax"), base=first, scale=scale,
+            w=None if w is None else w.reshape(-1, k), gradient=gradient, dloss=dloss, add=None if add is None else add.reshape(-1, self.slots))
+        return (loss, counts, grad[0].view(logits.shape)) if gradient else (loss, counts)
