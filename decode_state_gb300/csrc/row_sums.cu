@@ -51,24 +51,37 @@ template <int N>
 __device__ __forceinline__ void keys_of(const RowSumArgs& a, uint32_t e, uint32_t step, uint32_t* key) {
     int64_t j[N];
     float w[N];
+    const bool padded = a.chunk_valid != nullptr || a.valid < a.chunk;
+    const auto load = [&](int i, int op, uint32_t at) {
+        bool live = true;
+        if (padded) {
+            const uint32_t token = divided(at, op ? a.by_width[1] : a.by_width[0]), chunk = divided(token, a.by_chunk);
+            const int valid = a.chunk_valid != nullptr ? __ldg(a.chunk_valid + chunk) : a.valid;
+            live = (int)(token - chunk * a.chunk) < valid;
+        }
+        if (live) {
+            const void* idx = op ? a.idx[1] : a.idx[0];
+            j[i] = a.idx64 ? __ldg(static_cast<const int64_t*>(idx) + at) : __ldg(static_cast<const int32_t*>(idx) + at);
+            w[i] = weight_of(a, op, at);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const uint32_t at = e + i * step;
         j[i] = a.padding;
         w[i] = 0.0f;
-        if (at < a.entries) {
-            const Place p = place_of(a, at);
-            bool live = true;
-            if (a.chunk_valid != nullptr || a.valid < a.chunk) {
-                const uint32_t chunk = divided(p.token, a.by_chunk);
-                const int valid = a.chunk_valid != nullptr ? __ldg(a.chunk_valid + chunk) : a.valid;
-                live = (int)(p.token - chunk * a.chunk) < valid;
-            }
-            if (live) {
-                const void* idx = p.op ? a.idx[1] : a.idx[0];
-                j[i] = a.idx64 ? __ldg(static_cast<const int64_t*>(idx) + p.at) : __ldg(static_cast<const int32_t*>(idx) + p.at);
-                w[i] = weight_of(a, p.op, p.at);
-            }
+    }
+    // entries of one operand, as nearly all warps have them, choose between its arrays once
+    if (__all_sync(kAll, e + (N - 1) * step < a.split)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) load(i, 0, e + i * step);
+    } else if (__all_sync(kAll, e >= a.split && e + (N - 1) * step < a.entries)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) load(i, 1, e + i * step - a.split);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t at = e + i * step;
+            if (at < a.entries) load(i, at >= a.split, at >= a.split ? at - a.split : at);
         }
     }
     bool outside = false;
@@ -150,12 +163,21 @@ __device__ __forceinline__ int64_t zero_block(const RowSumArgs& a) {
     return (b + 1) * z / gridDim.x > before ? (int64_t)before : -1 - (int64_t)(b - before);
 }
 
+// An entry as its warp sums it.
+template <typename D>
+struct alignas(16) Entry {
+    const D* row;
+    float w;
+    uint32_t key;
+};
+
 // ---------------------------------------------------------------- few entries
 
 template <typename D, typename O, int V>
 __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, int zero_span) {
     __shared__ uint32_t keys[kDirect];
     __shared__ uint16_t list[kWarps][kDirect];
+    __shared__ Entry<D> batch[kWarps][32];
     __shared__ uint8_t touched[kZeroRows];
     __shared__ uint4 zeros[kZeroBytes / 16];
     grid_dependency_wait();
@@ -192,33 +214,39 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
         found += __popc(mask);
     }
     __syncwarp();
-    const int col = (int)(unit % a.slices) * a.slice_cols + lane * V;
-    if (lane * V >= a.slice_cols || col >= a.hd) return;
+    const int in_slice = lane * V, col = (int)(unit % a.slices) * a.slice_cols + in_slice;
+    const bool on = in_slice < a.slice_cols && col < a.hd;
     float sum[V];
 #pragma unroll
     for (int c = 0; c < V; ++c) sum[c] = 0.0f;
     Pack<O, V> there;
-    if (a.accumulate) there = load_pack<O, V>(place_in<O>(a, key, col));  // on its way meanwhile
-    constexpr int U = 16;
-    for (int i0 = 0; i0 < found; i0 += U) {
-        Pack<D, V> x[U];
-        float w[U];
+    if (a.accumulate && on) there = load_pack<O, V>(place_in<O>(a, key, col));  // on its way meanwhile
+    Entry<D>* mine = batch[warp];
+    for (int base = 0; base < found; base += 32) {
+        if (base + lane < found) {
+            const Place p = place_of(a, list[warp][base + lane]);
+            mine[lane] = {static_cast<const D*>(p.op ? a.dout[1] : a.dout[0]) + (uint64_t)p.token * (uint32_t)a.hd, weight_of(a, p.op, p.at), key};
+        }
+        __syncwarp();
+        const int left = min(found - base, 32);
+        constexpr int U = 16;
+        for (int j0 = 0; j0 < left; j0 += U) {
+            Pack<D, V> x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u < found) {
-                const Place p = place_of(a, list[warp][i0 + u]);
-                w[u] = weight_of(a, p.op, p.at);
-                x[u] = load_pack<D, V>(static_cast<const D*>(p.op ? a.dout[1] : a.dout[0]) + (int64_t)p.token * a.hd + col);
+            for (int u = 0; u < U; ++u)
+                if (j0 + u < left && on) x[u] = load_pack<D, V>(mine[j0 + u].row + col);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (j0 + u < left) {
+                    const float w = mine[j0 + u].w;
+#pragma unroll
+                    for (int c = 0; c < V; ++c) sum[c] = fmaf(w, to_f32(x[u].v[c]), sum[c]);
+                }
             }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u < found) {
-#pragma unroll
-                for (int c = 0; c < V; ++c) sum[c] = fmaf(w[u], to_f32(x[u].v[c]), sum[c]);
-            }
-        }
+        __syncwarp();
     }
+    if (!on) return;
     put_row<O, V>(a, key, col, sum, there);
 }
 
@@ -490,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 3) digit_place_kernel(const RowSumAr
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         const unsigned same = rank[i];
+        if (FIRST && !__any_sync(kAll, same)) continue;  // padding comes in runs
         const uint32_t d = digit.of(key[i]), before = m.own[warp][d];
         __syncwarp();
         if (key[i] < a.n_slots && lane == 31 - __clz(same)) m.own[warp][d] = (uint16_t)(before + __popc(same));
@@ -578,14 +607,6 @@ __device__ __forceinline__ uint32_t warp_lower_bound(const uint2* sorted, uint32
     }
     return lo;
 }
-
-// A sorted entry as its warp sums it.
-template <typename D>
-struct alignas(16) Entry {
-    const D* row;
-    float w;
-    uint32_t key;
-};
 
 constexpr uint32_t kShort = 32;  // entries of a run beyond the end of a piece that its warp sums as well
 
