@@ -1,9 +1,11 @@
 """The balance loss, its counts and its gradient against a plain form in 64 bits, on every kernel path.
 
-Tolerances. A share is an exponential (2 steps of 2^-23, and the rounding of its argument, at most 2^-24 * 20
-where the share is above 2^-28 of the largest) over a sum of at most 128 terms a thread and ten joins; the loss and the
-gradient are sums and products of shares and centred counts. So each share is off by at most PARTS = 200 steps of
-2^-24, and the outputs by what that moves them by (train_reference.balance), plus one rounding to their type."""
+Tolerances. A share is an exponential over a sum. The exponential is off by 4 steps of 2^-24 and by 2.5 more for each unit of its
+argument (a difference, a product and a constant are rounded), which is up to 60 here: 154. The sum's positive terms are
+as far off as they, weighted by their size, so that those near the largest, with few units, decide; adding up to 128 of them a
+thread and ten joins, the products and quotients that follow, with half a step each on average, take no more than the
+remaining 46. So each share is off by at most PARTS = 200 steps of 2^-24, and the outputs by what that moves them by
+(train_reference.balance), plus one rounding to their type."""
 
 from __future__ import annotations
 
@@ -120,6 +122,15 @@ def test_masked_infinite_and_far_logits(n, dtype, score):
     x[15, 0] = 1e4
     x[16, 0], x[16, 1:] = 30.0, -30.0
     _check(x, idx, score=score)
+
+
+@pytest.mark.parametrize("n", (40, 300, 900, 20000))
+@pytest.mark.parametrize("offset", (3e4, -3e4, 1e7, -1e7, 3e10, -3e10, 2e38, -2e38))
+def test_logits_far_from_zero(n, offset):
+    """Rows whose logits differ by little and lie anywhere."""
+    x, idx, gen = _inputs(9, n, 4, torch.float32, seed=n)
+    steps = torch.randint(0, 6, (9, n), generator=gen).float() * max(1.0, abs(offset) * 2.0 ** -23)  # whole units in the last place
+    _check(steps + offset, idx, score="softmax")
 
 
 def test_counts_far_from_even():
