@@ -84,8 +84,8 @@ __device__ __forceinline__ void counted_columns(const BalanceArgs& a, uint32_t e
 
 // exp(x - m) for x <= m is 2^((x - m) * log2(e)) by the hardware's 2^x, which is good for 2 ulp. Its argument is rounded
 // twice, and log2(e) once: 2.5 steps of 2^-24 of the result for each unit of x - m. expf, which makes up for the second and
-// third of these, takes twice the instructions: 1024 float32 rows of 16384 29 us with it and EX2A without, 4097 of 4099 with
-// the gradient 64 and EX2B. (x * log2(e) - m * log2(e) in one operation is off by what m, not x - m, amounts to.)
+// third of these, takes twice the instructions: 1024 float32 rows of 16384 29 us with it and 26 without, 4097 of 4099 with
+// the gradient 64 and 60. (x * log2(e) - m * log2(e) in one operation is off by what m, not x - m, amounts to.)
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float exp2_of(float x) {
     float y;
@@ -385,10 +385,11 @@ __device__ __forceinline__ float lanes_pass(const Row<TEAM, E, VEC, L>& r, const
 }
 
 // Rows of up to 512 entries: TEAM lanes a row, E logits each. The next token's row is on its way while a warp
-// works on one, and the counts of the sequence stay in registers. Half as many lanes with twice the logits spend less on
-// what a row costs whatever its length: 65536 rows of 256 bf16 with the gradient, 16 lanes TIME16 us, 32 lanes 33.
+// works on one, and the counts of the sequence stay in registers. Sixteen logits a lane spend less than eight on what a row
+// costs whatever its length: a call with 65536 rows of 256 bf16 and the gradient takes 37 us, with eight 42. Its registers
+// fit four blocks an SM; with five (43 us) some are spilled, three (39 us) hide less latency.
 template <int TEAM, int E, bool VEC, bool GRAD, typename L>
-__global__ void __launch_bounds__(128, 5) balance_lanes_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(128, 4) balance_lanes_kernel(const BalanceArgs a) {
     using R = Row<TEAM, E, VEC, L>;
     constexpr int TEAMS = 128 / TEAM, V = R::V, ACCESSES = E / V;
     constexpr bool AHEAD = R::RAW <= 8;
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(128, 5) balance_lanes_kernel(const BalanceArgs
 
 // Few tokens: one launch, with a cluster of blocks for each sequence. Each of its blocks counts all of the sequence's
 // entries in shared memory and goes over its share of the rows; the first has the counts and the loss. The last cluster, of a
-// call with offsets, writes the rows of the tokens that are in no sequence. 64 rows of 256 bf16: SMALL us, in four launches 8.0.
+// call with offsets, writes the rows of the tokens that are in no sequence. 64 rows of 256 bf16: 6.2 us, in four launches 8.0.
 constexpr int kSmallCluster = 8, kSmallThreads = 256, kSmallBins = 512;
 template <int TEAM, bool GRAD, typename L>
 __global__ void __launch_bounds__(kSmallThreads) balance_small_kernel(const BalanceArgs a) {

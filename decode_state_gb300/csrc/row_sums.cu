@@ -113,16 +113,20 @@ __device__ __forceinline__ O* place_in(const RowSumArgs& a, uint32_t row, int co
 }
 // A row's sum goes to its place, `there` being what is there where sums are added to it.
 template <typename O, int V>
-__device__ __forceinline__ void put_row(const RowSumArgs& a, uint32_t row, int col, const float* sum, const Pack<O, V>& there) {
+__device__ __forceinline__ void put_row(const RowSumArgs& a, bool accumulate, uint32_t row, int col, const float* sum, const Pack<O, V>& there) {
     Pack<O, V> y;
-    if (a.accumulate) {
+    if (accumulate) {
 #pragma unroll
         for (int c = 0; c < V; ++c) y.v[c] = from_f32<O>(fmaf(sum[c], a.scale, to_f32(there.v[c])));
     } else {
 #pragma unroll
         for (int c = 0; c < V; ++c) y.v[c] = from_f32<O>(sum[c] * a.scale);
     }
-    *reinterpret_cast<Pack<O, V>*>(place_in<O>(a, row, col)) = y;
+    // streaming: rows of dout that other warps will read stay in L2
+    if constexpr (sizeof(y) == 16)
+        __stcs(reinterpret_cast<uint4*>(place_in<O>(a, row, col)), *reinterpret_cast<const uint4*>(&y));
+    else
+        *reinterpret_cast<Pack<O, V>*>(place_in<O>(a, row, col)) = y;
 }
 
 // Rows [first, first + count) of the output whose flag is not set become zero, by a block: copies of `zeros` in shared
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
         __syncwarp();
     }
     if (!on) return;
-    put_row<O, V>(a, key, col, sum, there);
+    put_row<O, V>(a, a.accumulate, key, col, sum, there);
 }
 
 // ---------------------------------------------------------------- the sort
@@ -256,6 +260,7 @@ __global__ void __launch_bounds__(kThreads) direct_kernel(const RowSumArgs a, in
 struct Digit {
     int shift, bits;
     __device__ __forceinline__ uint32_t of(uint32_t key) const { return key >> shift & ((1u << bits) - 1); }
+    __device__ __forceinline__ int end() const { return min(shift + bits, 32); }  // the last digit may be short
 };
 
 // The counts of a tile's digits, counts[tile][digit]. FIRST: the keys are made here and kept, and entries
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_sort_kernel(const 
         }
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) place[i] = __ballot_sync(kAll, key[i] < a.n_slots);
-        for (int b = digit.shift; b < digit.shift + digit.bits; ++b) {
+        for (int b = digit.shift; b < digit.end(); ++b) {
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
                 const uint32_t bit = key[i] >> b & 1;
@@ -508,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 3) digit_place_kernel(const RowSumAr
     // lanes with the same digit, bit by bit (a match over all bits at once took half as long again)
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) rank[i] = __ballot_sync(kAll, key[i] < a.n_slots);
-    for (int b = digit.shift; b < digit.shift + digit.bits; ++b) {
+    for (int b = digit.shift; b < digit.end(); ++b) {
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const uint32_t bit = key[i] >> b & 1;
@@ -610,10 +615,13 @@ __device__ __forceinline__ uint32_t warp_lower_bound(const uint2* sorted, uint32
 
 constexpr uint32_t kShort = 32;  // entries of a run beyond the end of a piece that its warp sums as well
 
-// ACC: sums are added to what is there, which is loaded beside the entries that end a run, so that it is at hand
-// when they do.
+// A warp loads U rows of dout together, and the entries of the next batch meanwhile. Bound by latency and by what L2 gives:
+// 65536 tokens of 64 and 32 entries over 2^20 rows of 128 read 1.6 GB of dout out of L2, and a call with 4 rows together and
+// registers for 5 blocks an SM takes 292 us; 8 and 4 323, 2 and 6 298, 4 and 6 (spilled) 340; rows that wait in shared memory
+// instead, 16 of them by cp.async, 381.
+// ACC: sums are added to what is there, which is loaded beside the entries, so that it is at hand when a run ends.
 template <typename D, typename O, int V, bool ACC>
-__global__ void __launch_bounds__(kThreads, V <= 4 ? (ACC ? 2 : 4) : (ACC ? 1 : 3)) sums_kernel(const RowSumArgs a, int zero_span) {
+__global__ void __launch_bounds__(kThreads, V <= 4 ? (ACC ? 3 : 5) : (ACC ? 2 : 3)) sums_kernel(const RowSumArgs a, int zero_span) {
     __shared__ union {
         uint4 zeros[kZeroBytes / 16];
         Entry<D> batch[kWarps][32];
@@ -687,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? (ACC ? 2 : 4) : (ACC ? 1 : 
             }
             if (!continues && slice == 0 && lane == 0) a.list[atomicAdd(a.counters + 1, 1u)] = (uint32_t)piece;
         } else if (on) {
-            put_row<O, V>(a, current, col, sum, there);
+            put_row<O, V>(a, ACC, current, col, sum, there);
         }
         continues = false;
 #pragma unroll
@@ -711,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? (ACC ? 2 : 4) : (ACC ? 1 : 
         if (lane == 0) before = current;
         __syncwarp();
         const unsigned begins = __ballot_sync(kAll, lane < left && key != before);  // entries that begin another run
-        constexpr int U = 8;
+        constexpr int U = 4;
         for (int j0 = 0; j0 < left; j0 += U) {
             const int count = left - j0;
             const unsigned first = begins >> j0;
@@ -787,7 +795,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const RowSumArgs a) {
             }
             Pack<O, V> there;
             if (a.accumulate) there = load_pack<O, V>(place_in<O>(a, key, col));
-            put_row<O, V>(a, key, col, sum, there);
+            put_row<O, V>(a, a.accumulate, key, col, sum, there);
         }
         __syncthreads();
     }

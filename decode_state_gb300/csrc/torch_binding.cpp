@@ -633,7 +633,6 @@ struct RowsOut {
     RowsOut(const Args& a, int dtype, int out, int accumulate, int64_t rows, int64_t hd, const at::Device& dev) {
         flags = a.truth(accumulate) ? SDM_ACCUMULATE : 0u;
         TORCH_CHECK_VALUE(!flags || !a.none(out), "there must be an out to add to");
-        TORCH_CHECK_VALUE(rows >= 0, "a negative number of rows");
         if (a.none(out)) {
             const auto ty = a.dtype(dtype, "dtype");
             float_code(ty, "dtype");
@@ -661,10 +660,10 @@ PyObject* lookup_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     need(tokens, "tokens", dev, dout.sizes().slice(0, dout.dim() - 1));
     need(dout, "dout", dev, dout.sizes());
     const int64_t count = tokens.numel(), rows = a.integer(2);
-    Launch l(dev, a.a[8]);
-    const RowsOut out(a, 5, 6, 7, rows, hd, dev);
     int64_t bytes = 0;
     check("sdm_lookup_backward_workspace", sdm_lookup_backward_workspace(count, rows, static_cast<int>(hd), &bytes));
+    Launch l(dev, a.a[8]);
+    const RowsOut out(a, 5, 6, 7, rows, hd, dev);
     const Tensor scratch = l.workspace(bytes, dev);
     check("sdm_lookup_backward", sdm_lookup_backward(dout.data_ptr(), dt, tokens.data_ptr(), it, count, padding_of(a, 4), a.real(3),
                                                      out.t->data_ptr(), rows, static_cast<int>(hd), out.type, out.flags, scratch.data_ptr(),
@@ -730,10 +729,10 @@ PyObject* gather_drows(PyObject*, PyObject* const* args, Py_ssize_t n) {
         valid = 0;
     }
     const int64_t n_slots = a.integer(1);
-    Launch l(dev, a.a[8]);
-    const RowsOut out(a, 5, 6, 7, n_slots, hd, dev);
     int64_t bytes = 0;
     check("sdm_gather_drows_workspace", sdm_gather_drows_workspace(entries, n_slots, static_cast<int>(hd), &bytes));
+    Launch l(dev, a.a[8]);
+    const RowsOut out(a, 5, 6, 7, n_slots, hd, dev);
     const Tensor scratch = l.workspace(bytes, dev);
     check("sdm_gather_drows", sdm_gather_drows(static_cast<int>(k), idx, w, dout, width, it, wt, out.t->data_ptr(), n_slots,
                                                static_cast<int>(hd), out.type, out.flags, tokens, chunk, valid, cv, scratch.data_ptr(), bytes,

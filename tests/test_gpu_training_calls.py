@@ -142,7 +142,7 @@ def test_refusals():
         lambda: embedding.lookup(table, tokens.cpu()), lambda: embedding.lookup(table[:, ::2], tokens), lambda: embedding.lookup(table, tokens[::2]),
         lambda: embedding.lookup(table, tokens, out=dout[:5]), lambda: embedding.lookup(table, tokens, out=dout.cpu()),
         lambda: embedding.backward(dout, tokens[:5], 500), lambda: embedding.backward(dout, tokens, 500, accumulate=True),
-        lambda: embedding.backward(dout, tokens, 500, out=table[:400]), lambda: embedding.backward(dout, tokens, -1),
+        lambda: embedding.backward(dout, tokens, 500, out=table[:400]),
         lambda: embedding.backward(dout[:, ::2], tokens, 500), lambda: embedding.backward(dout.view(-1), tokens, 500),
         lambda: quant.gather_drows([(tokens, w, dout)], 500), lambda: quant.gather_drows([(chosen, w, dout)], 500),
         lambda: quant.gather_drows([(tokens[:, None], w[:, :1], dout)], 500), lambda: quant.gather_drows([(tokens.view(-1, 2), w[:10000], dout)], 500),
@@ -166,7 +166,8 @@ def test_refusals():
     codes = [
         (lambda: routing.balance(x, chosen, gradient=True, out=x), -10), (lambda: routing.balance(x, chosen, counts=chosen.view(torch.int32).view(-1)[:96].view(1, 96)), -10),
         (lambda: embedding.lookup(table, tokens[:500], out=table), -10), (lambda: embedding.backward(table, tokens[:500], 500, out=table), -10),
-        (lambda: embedding.backward(dout, tokens, 0), -7),
+        (lambda: embedding.backward(dout, tokens, 0), -7), (lambda: embedding.backward(dout, tokens, -1), -7),
+        (lambda: embedding.backward(dout, tokens, 1 << 40), -7), (lambda: quant.gather_drows([(tokens[:, None], w[:, :1].contiguous(), dout)], 1 << 31), -7),
     ]
     for i, (call, code) in enumerate(codes):
         with pytest.raises(sdm.SDMError) as e:
