@@ -90,12 +90,16 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const Bala
     }
 }
 
-// A sequence's loss out of its parts: those of the teams that met it lie side by side.
+// A sequence's loss out of its parts: those of the teams that met it lie side by side. LANES threads a sequence: a block, or a
+// warp where there are many.
+template <int LANES>
 __global__ void __launch_bounds__(kCountThreads) balance_loss_kernel(const BalanceArgs a) {
     __shared__ double sums[kCountThreads / 32];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int s = blockIdx.x;
+    const int lane = threadIdx.x % LANES;
+    const int64_t s = (int64_t)blockIdx.x * (kCountThreads / LANES) + threadIdx.x / LANES;
+    if (s >= a.sequences) return;  // whole warps
     int begin = 0, end = a.tokens;
     if (a.offsets != nullptr) {
         begin = max(__ldg(a.offsets + s), 0);
@@ -104,16 +108,18 @@ __global__ void __launch_bounds__(kCountThreads) balance_loss_kernel(const Balan
     const bool any = end > begin && a.totals[s] > 0;
     double sum = 0.0;
     if (any)
-        for (int p = begin / a.rows + s + threadIdx.x; p <= (end - 1) / a.rows + s; p += kCountThreads) sum += a.parts[p];
+        for (int64_t p = begin / a.rows + s + lane; p <= (end - 1) / a.rows + s; p += LANES) sum += a.parts[p];
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double all = 0.0;
-        for (int w = 0; w < kCountThreads / 32; ++w) all += sums[w];
-        a.loss[s] = any ? (float)(a.scale * all / (double)(end - begin)) : 0.0f;
+    if constexpr (LANES > 32) {
+        if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            sum = 0.0;
+            for (int w = 0; w < kCountThreads / 32; ++w) sum += sums[w];
+        }
     }
+    if (lane == 0) a.loss[s] = any ? (float)(a.scale * sum / (double)(end - begin)) : 0.0f;
 }
 
 // Calls that one launch takes, in which a cluster may have all rows and entries to itself.
@@ -174,7 +180,10 @@ int launch_balance(const BalanceArgs& a0, cudaStream_t stream) {
     }
     if (a.sequences == 0) return 0;
     void* args[] = {&a};
-    return launch_pdl_raw((const void*)balance_loss_kernel, dim3((unsigned)a.sequences), dim3(kCountThreads), 0, stream, args);
+    if (a.sequences <= 1024)
+        return launch_pdl_raw((const void*)balance_loss_kernel<kCountThreads>, dim3(a.sequences), dim3(kCountThreads), 0, stream, args);
+    constexpr int each = kCountThreads / 32;
+    return launch_pdl_raw((const void*)balance_loss_kernel<32>, dim3((a.sequences + each - 1) / each), dim3(kCountThreads), 0, stream, args);
 }
 
 cudaError_t balance_status(void** word) { return cudaGetSymbolAddress(word, g_balance_status); }

@@ -260,15 +260,16 @@ struct Row {
     }
 };
 
-// 1 / z of a sum of scores, which is at least 2^-60 or 0 (1 ulp).
+// 1 / z of a sum of scores, which is at least 2^-30 or 0 (1 ulp).
 __device__ __forceinline__ float inverse_of(float z) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(z));
     return z > 0.0f ? r : 0.0f;
 }
 
-// Sums of sigmoid scores below this lose bits; the row's shares are then those of exp(x), as for a softmax.
-constexpr float kLowScores = 0x1p-60f;
+// Where a row's sigmoid scores sum to less than this, its shares are those of exp(x), as for a softmax: what the scores leave to
+// one is one then, but for 2^-30, and scores that are 0 in float32 have their shares (above it, 0 is below 2^-96 of the sum).
+constexpr float kLowScores = 0x1p-30f;
 
 // A sequence's factors: the mean of its counts, its inverse, and what its gradient is multiplied by.
 struct Factors {

@@ -133,6 +133,20 @@ def test_logits_far_from_zero(n, offset):
     _check(steps + offset, idx, score="softmax")
 
 
+@pytest.mark.parametrize("n", (20, 300, 2000, 18000))
+@pytest.mark.parametrize("offset", (-10.0, -25.0, -45.0, -70.0, -86.0))
+def test_tiny_sigmoid_scores(n, offset):
+    """Shares of scores far below one, some of them 0 in float32."""
+    x, idx, gen = _inputs(14, n, 4, torch.float32, seed=n, spread=8.0)
+    x, want = x + offset, ref.count(idx, n)
+    loss, counts, grad = routing.balance(x.cuda(), idx.cuda(), score="sigmoid", gradient=True)
+    l64, g64, moved_l, moved_g = ref.balance(x, want, score="sigmoid")
+    ref.close(loss, l64, moved_l, "loss", PARTS)
+    # a score below 2^-126 is 0 where the row's scores sum to 2^-30 or more: its share, up to 2^-96, is left out
+    left_out = 2.0 ** -96 * n * (counts.cpu().double().max() + 1) / (14 * 56)
+    ref.close(grad, g64, moved_g + left_out / PARTS, "gradient", PARTS)
+
+
 def test_counts_far_from_even():
     """All choices on one entry, and on two; a loss of n for shares on one entry."""
     n, tokens = 64, 500
