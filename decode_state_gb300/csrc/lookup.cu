@@ -38,14 +38,14 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const LookupArgs a) {
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const int64_t t = first + r * teams;
-        slot[r] = a.padding;
+        slot[r] = 0;
         if (t < a.n_tokens) slot[r] = a.idx64 ? __ldg(static_cast<const int64_t*>(a.tokens) + t) : __ldg(static_cast<const int32_t*>(a.tokens) + t);
     }
     Pack<T, V> x[ROWS];
     bool outside = false;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        const bool in = slot[r] >= 0 && slot[r] < a.n_rows, none = slot[r] == a.padding;
+        const bool in = slot[r] >= 0 && slot[r] < a.n_rows, none = slot[r] == a.padding && a.padding != SDM_NO_PADDING;
         outside |= !in && !none;
         if (!in || none) slot[r] = -1;
         if (slot[r] >= 0) x[r] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(a.table) + slot[r] * a.hd + col);

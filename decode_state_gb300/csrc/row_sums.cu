@@ -51,6 +51,7 @@ template <int N>
 __device__ __forceinline__ void keys_of(const RowSumArgs& a, uint32_t e, uint32_t step, uint32_t* key) {
     int64_t j[N];
     float w[N];
+    uint32_t read = 0;  // which entries have an index
     const bool padded = a.chunk_valid != nullptr || a.valid < a.chunk;
     const auto load = [&](int i, int op, uint32_t at) {
         bool live = true;
@@ -63,11 +64,12 @@ __device__ __forceinline__ void keys_of(const RowSumArgs& a, uint32_t e, uint32_
             const void* idx = op ? a.idx[1] : a.idx[0];
             j[i] = a.idx64 ? __ldg(static_cast<const int64_t*>(idx) + at) : __ldg(static_cast<const int32_t*>(idx) + at);
             w[i] = weight_of(a, op, at);
+            read |= 1u << i;
         }
     };
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        j[i] = a.padding;
+        j[i] = -1;
         w[i] = 0.0f;
     }
     // entries of one operand, as nearly all warps have them, choose between its arrays once
@@ -87,8 +89,8 @@ __device__ __forceinline__ void keys_of(const RowSumArgs& a, uint32_t e, uint32_
     bool outside = false;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const bool in = j[i] >= 0 && j[i] < a.n_slots, none = j[i] == a.padding;
-        outside |= !in && !none;
+        const bool in = j[i] >= 0 && j[i] < a.n_slots, none = j[i] == a.padding && a.padding != SDM_NO_PADDING;
+        outside |= (read >> i & 1) && !in && !none;
         key[i] = in && !none && w[i] != 0.0f ? (uint32_t)j[i] : (uint32_t)a.n_slots;
     }
     if (outside) atomicOr(&g_row_sums_status, SDM_DEV_BAD_INDEX);

@@ -75,6 +75,9 @@ def test_lookup_outside_the_table():
     sdm.device_status()
     got = embedding.lookup(t, tokens)
     assert sdm.device_status() == sdm.SDM_DEV_BAD_INDEX
+    least = torch.full((3,), -(1 << 63), device="cuda")  # the number that stands for no padding in the C call
+    assert not embedding.lookup(t, least).any() and sdm.device_status() == sdm.SDM_DEV_BAD_INDEX
+    assert not embedding.backward(t[:3], least, 9).any() and sdm.device_status() == sdm.SDM_DEV_BAD_INDEX
     assert torch.equal(got[[0, 2]], t[[0, 8]]) and not got[[1, 3, 4, 5]].any()
     got = embedding.lookup(t, tokens[:3], padding=-1)  # a padding token outside the table is no error
     assert sdm.device_status() == 0 and not got[1].any()
