@@ -252,3 +252,18 @@ def test_same_bits_each_time_and_in_a_graph():
         idx.copy_(index)
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(got, routing.balance(x, idx, offsets=offsets, gradient=True)))
+
+
+@pytest.mark.parametrize("n,tokens", ((16384, 140000), (256, 9000000)))
+def test_more_than_32_bits_of_logits(n, tokens):
+    """More than 2^31 logits, all alike: every row has the gradient (c - C / n) / (T C), the last as the first."""
+    x = torch.zeros((tokens, n), dtype=torch.bfloat16, device="cuda")
+    idx = torch.randint(0, n, (tokens, 2), device="cuda", dtype=torch.int32)
+    loss, counts, grad = routing.balance(x, idx, gradient=True)
+    assert torch.equal(counts[0].long(), torch.bincount(idx.view(-1).long(), minlength=n))
+    total = 2 * tokens
+    assert abs(float(loss) - 1) <= 200 * ref.STEP
+    want = (counts[0].double().cpu() - total / n) / (tokens * float(total))
+    moved = ref.STEP * ((counts[0].double().cpu() - total / n).abs() + total / n * ref.STEP) / (tokens * float(total)) * 2
+    for t in (0, tokens // 2, (1 << 31) // n - 1, (1 << 31) // n, tokens - 1):
+        ref.close(grad[t], want, moved + moved.mean(), f"row {t}", PARTS)

@@ -277,3 +277,18 @@ def test_two_streams_at_once():
         got = [embedding.backward(d, t, 700, stream=s) for (d, t), s in zip(sets, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_lookup_of_more_than_32_bits():
+    """An output of more than 2^32 elements."""
+    hd, count = 2048, 2200000
+    table = torch.randn(50, hd, device="cuda").bfloat16()
+    tokens = torch.randint(0, 50, (count,), device="cuda", dtype=torch.int32)
+    out = embedding.lookup(table, tokens)
+    for at in (0, (1 << 31) // hd - 1, (1 << 31) // hd, (1 << 32) // hd - 1, (1 << 32) // hd, count - 1):
+        assert torch.equal(out[at], table[tokens[at]])
+    dout = out[-3000000000 // hd:]  # the gradient of the last rows, from an address far into a tensor
+    got = embedding.backward(dout, tokens[-len(dout):], 50)
+    times = torch.bincount(tokens[-len(dout):].long(), minlength=50).double()
+    want = times[:, None] * table.double()  # each of the sums is of equal terms, bf16 by whole numbers
+    assert float((got.double() - want).abs().max()) <= float((times[:, None] * ref.STEP * want.abs()).max())
