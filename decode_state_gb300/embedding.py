@@ -1,6 +1,6 @@
 """Embedding rows: scaled rows of a table by token, and the gradient of the table.
 
-Tables are [rows, hd] bfloat16 or float32, tokens int32 or int64 of any shape. ``padding`` names a token that stands for
+Tables are [rows, hd] bfloat16 or float32, tokens int32 or int64 of any shape, all of them contiguous. ``padding`` names a token that stands for
 nothing: it gives zeros and has no gradient. A token outside the table does likewise and raises the device status
 (``sdm.device_status``). Work goes to the current stream unless ``stream`` is given; outputs are then made in that
 stream's memory. The definitions stand at ``sdm_lookup`` and ``sdm_lookup_backward`` in ``include/sdm.h``.
