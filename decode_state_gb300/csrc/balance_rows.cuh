@@ -83,9 +83,9 @@ __device__ __forceinline__ void counted_columns(const BalanceArgs& a, uint32_t e
 }
 
 // exp(x - m) for x <= m is 2^((x - m) * log2(e)) by the hardware's 2^x, which is good for 2 ulp. Its argument is rounded
-// twice, and log2(e) once: 2.5 steps of 2^-24 of the result for each unit of x - m. expf, which makes up for the second and
-// third of these, takes twice the instructions: 1024 float32 rows of 16384 29 us with it and 26 without, 4097 of 4099 with
-// the gradient 64 and 60. (x * log2(e) - m * log2(e) in one operation is off by what m, not x - m, amounts to.)
+// twice, and log2(e) once: 2.5 steps of 2^-24 of the result for each unit of x - m. With expf in its place 1024 float32 rows
+// of 16384 take 29 us for 26, and 4097 of 4099 with the gradient 64 for 60. (x * log2(e) - m * log2(e) in one operation is
+// off by what m, not x - m, amounts to.)
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float exp2_of(float x) {
     float y;
