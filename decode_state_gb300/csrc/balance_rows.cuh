@@ -308,13 +308,20 @@ __device__ __forceinline__ void centred(const int32_t* counts, int n, bool whole
 struct Run {
     Sequence q{-1, 0, 0};
     Factors f{0.0f, 0.0f, 0.0f};
-    float sum = 0.0f;
+    float sum = 0.0f, lost = 0.0f;
 
+    // A row's part. Parts that are nearly alike would all be rounded the same way as the sum grows, by 280 steps of 2^-24 of
+    // it after 1850 rows, so what each addition loses goes into the next (Kahan).
+    __device__ __forceinline__ void add(float part) {
+        const float y = part - lost, t = sum + y;
+        lost = (t - sum) - y;
+        sum = t;
+    }
     // Token t is next; true where another sequence begins.
     __device__ __forceinline__ bool next(const BalanceArgs& a, int t, int team, bool writes) {
         if (t >= q.begin && t < q.end) return false;
         done(a, team, writes);
-        sum = 0.0f;
+        sum = lost = 0.0f;
         q = sequence_of(a, t);
         f = q.s >= 0 ? factors_of(a, q.s, q.end - q.begin, __ldg(a.totals + q.s)) : Factors{0.0f, 0.0f, 0.0f};
         return true;
@@ -436,7 +443,7 @@ __global__ void __launch_bounds__(128, 4) balance_lanes_kernel(const BalanceArgs
         }
         __syncwarp();
         const float part = lanes_pass<GRAD>(r, raw, adds, counts, on, softmax, run.f, GRAD && a.add != nullptr, out);
-        run.sum += part;
+        run.add(part);
         if (GRAD && on) {
             out += a.dlogits_stride;
             add += a.add_stride;
@@ -670,7 +677,7 @@ __global__ void __launch_bounds__(TEAM, 1024 / TEAM) balance_block_kernel(const 
             z = d = 0.0f;
         }
         const float inverse = inverse_of(z), mean = d * inverse;
-        if (z > 0.0f) run.sum += fmaf(run.f.unit, mean, 1.0f);
+        if (z > 0.0f) run.add(fmaf(run.f.unit, mean, 1.0f));
         if constexpr (GRAD) {
             L* out = static_cast<L*>(a.dlogits) + t * a.dlogits_stride;
             const L* add = a.add != nullptr ? static_cast<const L*>(a.add) + t * a.add_stride : nullptr;
