@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const Bala
     constexpr int N = 4;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int first = blockIdx.x * run, last = min(first + run, a.tokens), tid = threadIdx.x;
+    const int first = blockIdx.x * run, last = first + min(run, a.tokens - first), tid = threadIdx.x;  // tokens may be near 2^31
     if constexpr (LOCAL) {
         for (int t = first; t < last;) {
             const Sequence q = warp_sequence_of(a, t);
@@ -158,8 +158,8 @@ int launch_balance(const BalanceArgs& a0, cudaStream_t stream) {
     if (a.sequences > 0 && a.tokens > 0) {
         const int64_t entries = (int64_t)a.tokens * a.k;
         int blocks = (int)std::min<int64_t>(std::min<int64_t>((entries + 4 * kCountThreads - 1) / (4 * kCountThreads), 4 * sms), a.tokens);
-        int run = (a.tokens + blocks - 1) / blocks;
-        blocks = (a.tokens + run - 1) / run;
+        int run = (a.tokens - 1) / blocks + 1;
+        blocks = (a.tokens - 1) / run + 1;
         const bool local = a.n <= kCountBins && entries >= (int64_t)2 * a.n * (blocks + a.sequences);
         void* args[] = {&a, &run};
         const int rc = launch_pdl_raw(local ? (const void*)balance_count_kernel<true> : (const void*)balance_count_kernel<false>,
