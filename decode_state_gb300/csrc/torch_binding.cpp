@@ -105,13 +105,34 @@ void need_f32(const Tensor& t, const char* name, const at::Device& dev, at::IntA
     need(t, name, dev, shape);
 }
 
-Tensor empty(at::IntArrayRef shape, at::ScalarType t, const at::Device& dev) {
-    return Tensor(at::detail::empty_cuda(shape, t, dev, std::nullopt));
+void check_cuda(cudaError_t e) {
+    if (e == cudaSuccess) return;
+    (void)cudaGetLastError();
+    TORCH_CHECK(false, "CUDA error: ", cudaGetErrorString(e));
 }
 
-// The device of the work made current, and the stream it goes to. Outputs made while a given stream is
+// The thread's stream waits for the work of the current one, `current`. The legacy default stream has this from itself. Where
+// one of the two is being captured and the other is not, or in another graph, no event joins them.
+void thread_stream_waits(cudaStream_t current) {
+    if (current == nullptr || current == cudaStreamLegacy || current == cudaStreamPerThread) return;
+    cudaStreamCaptureStatus status[2];
+    unsigned long long graph[2] = {0, 0};
+    check_cuda(cudaStreamGetCaptureInfo(current, &status[0], &graph[0]));
+    check_cuda(cudaStreamGetCaptureInfo(cudaStreamPerThread, &status[1], &graph[1]));
+    if (status[0] != status[1] || (status[0] != cudaStreamCaptureStatusNone && graph[0] != graph[1])) return;
+    cudaEvent_t event = nullptr;
+    check_cuda(cudaEventCreateWithFlags(&event, cudaEventDisableTiming));
+    cudaError_t e = cudaEventRecord(event, current);
+    if (e == cudaSuccess) e = cudaStreamWaitEvent(cudaStreamPerThread, event, 0);
+    (void)cudaEventDestroy(event);  // when it has been reached
+    check_cuda(e);
+}
+
+// The device of the work made current, and the stream it goes to. Outputs and workspaces made while a given stream is
 // current come from that stream's memory: what else is free may still be in use by the current stream,
-// whose work the given one does not wait for.
+// whose work the given one does not wait for. The stream of the thread (handle 2) is another one in each thread, and has no
+// memory of its own: it waits for the current stream, whose memory it takes, and what it took is not given to others before
+// it is done with it.
 struct Launch {
     c10::cuda::OptionalCUDAGuard guard;
     c10::cuda::OptionalCUDAStreamGuard stream_guard;
@@ -134,15 +155,20 @@ struct Launch {
     }
 
     bool per_thread = false;
+    mutable bool waits = false;  // the thread's stream, for the current one
 
-    // Memory for the call to work in, given back when the caller lets go of it: free for what the stream does next,
-    // and not before the stream is done with it where it is another one than the memory's.
-    Tensor workspace(int64_t bytes, const at::Device& dev) const {
-        Tensor t = empty({bytes}, at::kByte, dev);
-        if (per_thread && bytes > 0)
-            c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), c10::cuda::getStreamFromExternal(cudaStreamPerThread, dev.index()));
-        return t;
+    Tensor empty(at::IntArrayRef shape, at::ScalarType t, const at::Device& dev) const {
+        Tensor made(at::detail::empty_cuda(shape, t, dev, std::nullopt));
+        if (per_thread && made.numel() > 0) {
+            if (!waits) thread_stream_waits(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
+            waits = true;
+            c10::cuda::CUDACachingAllocator::recordStream(made.storage().data_ptr(), c10::cuda::getStreamFromExternal(cudaStreamPerThread, dev.index()));
+        }
+        return made;
     }
+
+    // Memory for the call to work in, given back when the caller lets go of it: free for what the stream does next.
+    Tensor workspace(int64_t bytes, const at::Device& dev) const { return empty({bytes}, at::kByte, dev); }
 };
 
 // Raise SDMError for a status that is not 0.
@@ -241,7 +267,7 @@ PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (a.none(2)) {
         const auto t = a.dtype(4, "dtype");
         float_code(t, "dtype");
-        made = empty({count < 0 ? b.n_slots : count, b.hd}, t, b.dev);
+        made = l.empty({count < 0 ? b.n_slots : count, b.hd}, t, b.dev);
     }
     const Tensor& r = a.none(2) ? made : a.tensor(2, name);
     const int rt = float_code(r.scalar_type(), name);
@@ -312,7 +338,7 @@ PyObject* gather(PyObject*, PyObject* const* args, Py_ssize_t n) {
             need(x, second, b.dev, i.sizes());
         }
         const int64_t cols = grad ? i.size(1) : b.hd;
-        if (!given) made[o] = empty({tokens, cols}, grad ? a.dtype(5, "dtype") : at::kFloat, b.dev);
+        if (!given) made[o] = l.empty({tokens, cols}, grad ? a.dtype(5, "dtype") : at::kFloat, b.dev);
         const Tensor& r = given ? Args::unpack(PySequence_Fast_GET_ITEM(given, o), third) : made[o];
         if (grad) {
             const int rt = float_code(r.scalar_type(), "the gradients");
@@ -388,7 +414,7 @@ PyObject* decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
         need_f32(beta, "beta", b.dev, {A});
     Launch l(b.dev, a.a[12]);
     Tensor made;
-    if (a.none(8)) made = empty(with(b.hd), a.dtype(9, "out_dtype"), b.dev);
+    if (a.none(8)) made = l.empty(with(b.hd), a.dtype(9, "out_dtype"), b.dev);
     const Tensor& out = a.none(8) ? made : a.tensor(8, "out");
     const int ot = float_code(out.scalar_type(), "readings");
     need(out, "out", b.dev, with(b.hd));
@@ -454,9 +480,9 @@ PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (a.none(11)) {
         const auto t = a.dtype(10, "idx_dtype");
         index_code(t, "idx_dtype");
-        made_idx = empty({x.tokens, k}, t, dev);
+        made_idx = l.empty({x.tokens, k}, t, dev);
     }
-    if (a.none(12)) made_w = empty({x.tokens, k}, at::kFloat, dev);
+    if (a.none(12)) made_w = l.empty({x.tokens, k}, at::kFloat, dev);
     const Tensor& idx = a.none(11) ? made_idx : a.tensor(11, "idx");
     const Tensor& w = a.none(12) ? made_w : a.tensor(12, "w");
     const int it = index_code(idx.scalar_type(), "idx");
@@ -495,7 +521,7 @@ PyObject* route_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     Launch l(dev, a.a[9]);
     Tensor made;
-    if (a.none(8)) made = empty(x.t.sizes(), x.t.scalar_type(), dev);
+    if (a.none(8)) made = l.empty(x.t.sizes(), x.t.scalar_type(), dev);
     const Logits out(a.none(8) ? made : a.tensor(8, "out"), "out");
     TORCH_CHECK_TYPE(out.type == x.type && out.t.device() == dev, "out must have the dtype and the device of the logits");
     TORCH_CHECK_VALUE(out.t.sizes() == x.t.sizes(), "out has shape ", out.t.sizes(), ", expected ", x.t.sizes());
@@ -544,8 +570,8 @@ PyObject* balance(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     Launch l(dev, a.a[13]);
     Tensor made_loss, made_counts, made_out;
-    if (a.none(10)) made_loss = empty({sequences}, at::kFloat, dev);
-    if (a.none(11)) made_counts = empty({sequences, x.t.size(1)}, at::kInt, dev);
+    if (a.none(10)) made_loss = l.empty({sequences}, at::kFloat, dev);
+    if (a.none(11)) made_counts = l.empty({sequences, x.t.size(1)}, at::kInt, dev);
     const Tensor& loss = a.none(10) ? made_loss : a.tensor(10, "loss");
     const Tensor& counts = a.none(11) ? made_counts : a.tensor(11, "counts");
     need_f32(loss, "loss", dev, {sequences});
@@ -565,7 +591,7 @@ PyObject* balance(PyObject*, PyObject* const* args, Py_ssize_t n) {
             add = g.t.data_ptr();
             add_stride = g.stride;
         }
-        if (a.none(12)) made_out = empty(x.t.sizes(), x.t.scalar_type(), dev);
+        if (a.none(12)) made_out = l.empty(x.t.sizes(), x.t.scalar_type(), dev);
         const Logits g(a.none(12) ? made_out : a.tensor(12, "out"), "out");
         like_logits(g, "out");
         dlogits = g.t.data_ptr();
@@ -612,7 +638,7 @@ PyObject* lookup(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (a.none(5)) {
         const auto t = a.none(4) ? table.scalar_type() : a.dtype(4, "dtype");
         float_code(t, "dtype");
-        made = empty(shape, t, b.dev);
+        made = l.empty(shape, t, b.dev);
     }
     const Tensor& out = a.none(5) ? made : a.tensor(5, "out");
     const int ot = float_code(out.scalar_type(), "out");
@@ -630,13 +656,13 @@ struct RowsOut {
     int type;
     unsigned flags;
 
-    RowsOut(const Args& a, int dtype, int out, int accumulate, int64_t rows, int64_t hd, const at::Device& dev) {
+    RowsOut(const Args& a, const Launch& l, int dtype, int out, int accumulate, int64_t rows, int64_t hd, const at::Device& dev) {
         flags = a.truth(accumulate) ? SDM_ACCUMULATE : 0u;
         TORCH_CHECK_VALUE(!flags || !a.none(out), "there must be an out to add to");
         if (a.none(out)) {
             const auto ty = a.dtype(dtype, "dtype");
             float_code(ty, "dtype");
-            made = empty({rows, hd}, ty, dev);
+            made = l.empty({rows, hd}, ty, dev);
         }
         t = a.none(out) ? &made : &a.tensor(out, "out");
         type = float_code(t->scalar_type(), "the gradient");
@@ -663,7 +689,7 @@ PyObject* lookup_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int64_t bytes = 0;
     check("sdm_lookup_backward_workspace", sdm_lookup_backward_workspace(count, rows, static_cast<int>(hd), &bytes));
     Launch l(dev, a.a[8]);
-    const RowsOut out(a, 5, 6, 7, rows, hd, dev);
+    const RowsOut out(a, l, 5, 6, 7, rows, hd, dev);
     const Tensor scratch = l.workspace(bytes, dev);
     check("sdm_lookup_backward", sdm_lookup_backward(dout.data_ptr(), dt, tokens.data_ptr(), it, count, padding_of(a, 4), a.real(3),
                                                      out.t->data_ptr(), rows, static_cast<int>(hd), out.type, out.flags, scratch.data_ptr(),
@@ -732,7 +758,7 @@ PyObject* gather_drows(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int64_t bytes = 0;
     check("sdm_gather_drows_workspace", sdm_gather_drows_workspace(entries, n_slots, static_cast<int>(hd), &bytes));
     Launch l(dev, a.a[8]);
-    const RowsOut out(a, 5, 6, 7, n_slots, hd, dev);
+    const RowsOut out(a, l, 5, 6, 7, n_slots, hd, dev);
     const Tensor scratch = l.workspace(bytes, dev);
     check("sdm_gather_drows", sdm_gather_drows(static_cast<int>(k), idx, w, dout, width, it, wt, out.t->data_ptr(), n_slots,
                                                static_cast<int>(hd), out.type, out.flags, tokens, chunk, valid, cv, scratch.data_ptr(), bytes,

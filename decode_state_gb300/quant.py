@@ -9,6 +9,8 @@ floating-point bank. Everything runs in the CUDA library; the native binding che
 passes pointers. Work goes to the current stream of the bank's device unless ``stream`` is given (a
 ``torch.cuda.Stream`` or a handle); outputs are then made in that stream's memory, and whoever uses
 them on another stream waits for it first, and records its use (``Tensor.record_stream``) before they go.
+The stream of the thread (handle 2) has no memory of its own: where a call makes something for it, it waits for the
+current stream and takes that one's.
 
 A user's choice of format: int8 rounds a row's values by about as much as bfloat16 does (1/254 of
 the group's largest value at most) and suits rows that are written again and again; fp8 keeps three
