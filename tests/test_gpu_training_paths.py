@@ -68,11 +68,12 @@ def test_several_rows_and_sequences_a_block(n, tokens, sequences, dtype, score, 
 
 
 @pytest.mark.parametrize("tokens,n,k,sequences", ((4096, 16, 2, 4096), (4096, 16, 2, 1000), (512, 128, 4, 512), (128, 512, 5, 40), (2048, 32, 4, 100),
-                                                  (65536, 1, 1, 30), (2730, 24, 3, 4097), (4097, 16, 2, 20)))
+                                                  (65536, 1, 1, 30), (2730, 24, 3, 4097), (4097, 16, 2, 20), (4096, 16, 2, 32), (2048, 32, 4, 32), (256, 256, 32, 33),
+                                                  (1024, 16, 4, 1), (1024, 16, 1, 1), (1025, 16, 1, 1), (2048, 16, 4, 2), (1000, 64, 8, 31), (500, 128, 9, 1)))
 @pytest.mark.parametrize("score", ("softmax", "sigmoid"))
-def test_a_cluster_for_each_sequence(tokens, n, k, sequences, score):
-    """The largest calls of one launch, and the smallest beyond them."""
-    _balance(tokens, n, k, F32, score, sequences, inside=True, add=True, seed=sequences)
+def test_one_launch_and_four(tokens, n, k, sequences, score):
+    """The largest calls of one launch, a cluster for each sequence, and calls beyond them."""
+    _balance(tokens, n, k, F32, score, sequences, inside=sequences > 1, add=True, seed=sequences)
 
 
 # ---------------------------------------------------------------- sums of rows
