@@ -98,7 +98,7 @@ def _tokens(count, rows, gen):
     return torch.randperm(rows, generator=gen)[rank]
 
 
-@pytest.mark.parametrize("count", (512, 513, 16384, 16385, 32768, 32769, 131072, 131073))
+@pytest.mark.parametrize("count", (512, 513, 16384, 16385, 32768, 32769, 131072, 131073, 1 << 20, (1 << 20) + 1))
 @pytest.mark.parametrize("rows", (997, 1 << 17))
 @pytest.mark.parametrize("accumulate", (False, True))
 def test_both_sides_of_each_path(count, rows, accumulate):
@@ -111,7 +111,7 @@ def test_both_sides_of_each_path(count, rows, accumulate):
 
 
 @pytest.mark.parametrize("rows", (1 << 11, (1 << 11) + 1, 1 << 17, 1 << 20, 1 << 22, (1 << 22) + 1))
-@pytest.mark.parametrize("count", (40_000, 200_000, 600_000))
+@pytest.mark.parametrize("count", (40_000, 200_000, 1_200_000))
 @pytest.mark.parametrize("dtype,out", ((BF16, F32), (F32, BF16)))
 def test_passes_of_the_sort(rows, count, dtype, out):
     """One, two and three passes by launches, in tiles of both sizes."""
@@ -127,7 +127,7 @@ def test_passes_of_the_sort(rows, count, dtype, out):
 def test_many_entries_of_a_gather(rows, accumulate):
     """Two operands, padding, weights of zero, in tiles of 4096 entries."""
     gen = torch.Generator().manual_seed(rows)
-    chunks, chunk, hd = 900, 16, 5
+    chunks, chunk, hd = 4500, 16, 3
     tokens = chunks * chunk
     valid = torch.randint(0, chunk + 1, (chunks,), generator=gen).to(torch.int32)
     ops = []
@@ -172,7 +172,7 @@ def test_most_entries():
     assert torch.equal(got[:, 0], want)
 
 
-@pytest.mark.parametrize("count,rows", ((40_000, 700), (300_000, 1 << 18)))
+@pytest.mark.parametrize("count,rows", ((40_000, 700), (300_000, 1 << 18), (1_100_000, 1 << 12)))
 def test_launches_of_the_sort_in_graphs_and_on_two_streams(count, rows):
     gen = torch.Generator().manual_seed(count)
     sets = [(torch.randn(count, 24, generator=gen).cuda(), _tokens(count, rows, gen).cuda()) for _ in range(2)]
