@@ -456,6 +456,7 @@ __global__ void __launch_bounds__(128, 4) balance_lanes_kernel(const BalanceArgs
 // Few tokens: one launch, with a cluster of blocks for each sequence. Each of its blocks counts all of the sequence's
 // entries in shared memory and goes over its share of the rows; the first has the counts and the loss. The last cluster, of a
 // call with offsets, writes the rows of the tokens that are in no sequence. 64 rows of 256 bf16: 6.2 us, in four launches 8.0.
+// (Float32 logits with the gradient spill 36 bytes a thread.)
 constexpr int kSmallCluster = 8, kSmallThreads = 256, kSmallBins = 512;
 template <int TEAM, bool GRAD, typename L>
 __global__ void __launch_bounds__(kSmallThreads) balance_small_kernel(const BalanceArgs a) {
@@ -550,11 +551,12 @@ __global__ void __launch_bounds__(kSmallThreads) balance_small_kernel(const Bala
 // Longer rows: a block a row, 8 logits a thread at a time. What the loss alone needs is summed in one pass, relative
 // to a maximum that grows. For the gradient the logits of a softmax, or what it takes of a sigmoid's, wait in shared
 // memory (STAGED), and with them the counts of the sequence (COUNTED), each thread's own; rows too long for that are read
-// again.
+// again (of float32 that start anywhere, 100 bytes a thread are spilled there). How many rows a block has follows from what
+// fits an SM, with the gradient fewer than without, so that the two losses may differ in their last bit.
 template <int TEAM, bool VEC, bool GRAD, bool STAGED, bool COUNTED, typename L>
 __global__ void __launch_bounds__(TEAM, 1024 / TEAM) balance_block_kernel(const BalanceArgs a) {
     using R = Row<TEAM, 0, VEC, L>;
-    constexpr int V = R::V, N = 8, U = N / V;  // the same with and without the gradient, and so the loss
+    constexpr int V = R::V, N = 8, U = N / V;
     extern __shared__ float stage[];
     __shared__ float joints[2][3][R::WARPS];
     int half = 0;

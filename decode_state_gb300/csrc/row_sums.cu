@@ -486,7 +486,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_sort_kernel(const 
 // ---------------------------------------------------------------- more: a launch for each step
 
 // A tile's entries go to their places: behind all smaller digits, behind the same digit of earlier tiles, in order. They
-// are put in order in shared memory first, so that what goes to one place is written side by side.
+// are put in order in shared memory first, so that what goes to one place is written side by side. (Later passes over
+// tiles of 4096 spill 32 bytes a thread, for a third block an SM.)
 template <bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(kThreads, 3) digit_place_kernel(const RowSumArgs a, const uint32_t* keys, const uint2* in, uint2* out,
                                                                   const uint32_t* counts, const uint32_t* totals, Digit digit) {

@@ -518,7 +518,9 @@ int sdm_route_backward_ex(const void* logits, int64_t row_stride, int logit_dtyp
  * sequence, when offsets is NULL), with T their number:
  *     p_tj      = s_tj / sum_i s_ti          the shares of a token's scores (those of sdm_route; masked
  *                                            entries, and all of a row that is masked throughout, have 0)
- *                                            in float32: a share below 2^-96 may be 0
+ *                                            in float32: a share below 2^-96 may be 0, and one is off by up
+ *                                            to 50 steps of 2^-24 and 2.5 more for each unit that its logit
+ *                                            lies below the row's largest (softmax) or below 0 (sigmoid)
  *     counts[s, j] = how often the sequence's tokens chose entry j
  *     loss[s]   = scale * n / (T * C) * sum_t sum_j counts[s, j] * p_tj,   C = sum_j counts[s, j]
  * (0 where T or C is 0): scale where choices or scores are spread evenly, up to scale * n where both are on
