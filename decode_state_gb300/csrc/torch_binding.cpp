@@ -244,6 +244,18 @@ PyObject* check_bank(PyObject*, PyObject* const* args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// room(rows, columns, dtype, stream): an uninitialised [len(rows), columns] on the device of `rows`, for the stream to write
+PyObject* room(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const Args a{args, n};
+    expect(a, 4, "room");
+    const Tensor& r = a.tensor(0, "rows");
+    TORCH_CHECK_VALUE(r.is_cuda(), "rows must be a CUDA tensor, got ", r.device());
+    Launch l(r.device(), a.a[3]);
+    return THPVariable_Wrap(l.empty({r.size(0), a.integer(1)}, a.dtype(2, "dtype"), r.device()));
+    END_HANDLE_TH_ERRORS
+}
+
 // rows(write, bank, rows or None, slots or None, dtype, stream): rows into the bank, or out of it
 PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -780,6 +792,7 @@ PyCFunction fast(F f) {
 }
 
 PyMethodDef methods[] = {{"check_bank", fast(check_bank), METH_FASTCALL, nullptr},
+                         {"room", fast(room), METH_FASTCALL, nullptr},
                          {"rows", fast(rows), METH_FASTCALL, nullptr},
                          {"gather", fast(gather), METH_FASTCALL, nullptr},
                          {"decode", fast(decode), METH_FASTCALL, nullptr},

@@ -3,6 +3,8 @@ the outputs nor the workspaces of a call are memory that the current stream stil
 
 from __future__ import annotations
 
+import threading
+
 import pytest
 import torch
 
@@ -115,3 +117,32 @@ def test_captured_with_the_current_stream():
         got.fill_(0)
         graph.replay()
         assert torch.equal(got, want)
+
+
+def test_banks_of_two_threads():
+    """Two threads' streams go by the same handle: a bank that is gone in one is not the other's before its stream is done."""
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    first, second = (torch.randn(4096, 128, generator=gen, device="cuda") for _ in range(2))
+    want = quant.QuantBank.from_rows(second)
+    a = torch.ones((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    made, finish = threading.Event(), threading.Event()
+
+    def busy():
+        with torch.cuda.stream(torch.cuda.ExternalStream(THREAD)):
+            _busy(a)
+        quant.QuantBank.from_rows(first, stream=THREAD)  # goes at once
+        made.set()
+        finish.wait(60)
+
+    thread = threading.Thread(target=busy)
+    thread.start()
+    try:
+        assert made.wait(60)
+        got = quant.QuantBank.from_rows(second, stream=THREAD)
+        torch.cuda.synchronize()
+    finally:
+        finish.set()
+        thread.join()
+    assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
